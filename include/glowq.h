@@ -328,6 +328,78 @@ GLOWQ_API glowq_status glowq_solo_forward_w4a8(const glowq_module* mod, int64_t 
                                                size_t workspace_bytes, void* stream);
 
 /*
+ * W8A8: 8-bit integer base weights with one scale per output channel and 8-bit
+ * integer activations with one scale per token (not on the GlowQ pages: the
+ * integer format that serving stacks use beside FP8), corrected like the other
+ * formats:
+ *   weights      s_o = fp32(max_k |w| / 127)   (1 for an all-zero row)
+ *                q   = rint(fp32(w / s_o))     in -127..127
+ *   activations  s_t, c the same per token of X
+ *   y[t][o] = fp16(s_t s_o sum_k c[t][k] q[o][k] + sum_j R[t][j] A[o][j]),
+ *   R = fp16(X B^T) from the unquantised X.
+ * The integer sum is exact.  All quantiser arithmetic is IEEE fp32, rint to
+ * even.  A row (of W) or token (of X) that holds an infinity or a NaN gets
+ * the scale NaN and codes 0: every output it enters is NaN.
+ *
+ * One 8-bit module of a group.  Device pointers:
+ *   codes    [O][d] int8, row-major, 16-byte aligned
+ *   scales   [O] fp32
+ *   A, out_features, Y, ldY  as in glowq_module
+ */
+typedef struct glowq_int8_module {
+    const int8_t* codes;
+    const float* scales;
+    const uint16_t* A;
+    int64_t out_features;
+    uint16_t* Y;
+    int64_t ldY;
+} glowq_int8_module;
+
+/*
+ * Quantise W (device, O x d fp32, d % 128 == 0, 16-byte aligned) to codes
+ * (device, O x d int8) and scales (device, O floats); and back:
+ * W_deq[o][k] = fp16_RN(q s_o) (device, O x d fp16 bits), to check the format.
+ */
+GLOWQ_API glowq_status glowq_pack_int8(const float* W, int64_t O, int64_t d, int8_t* codes, float* scales,
+                                       void* stream);
+GLOWQ_API glowq_status glowq_dequant_int8(const int8_t* codes, const float* scales, int64_t O, int64_t d,
+                                          uint16_t* W_deq, void* stream);
+
+/*
+ * Per-token int8 activations: X (device, T x d fp16, d % 128 == 0) -> codes
+ * (device, T x d int8), scales (device, T floats).  The forward calls below
+ * quantise inside; this is the quantiser alone.
+ */
+GLOWQ_API glowq_status glowq_quantize_act_int8(const uint16_t* X, int64_t T, int64_t d, int8_t* codes,
+                                               float* scales, void* stream);
+
+/*
+ * Device scratch of one W8A8 forward call (out_features: host array of the m
+ * modules' widths).  The first 65536 bytes must be zero before the first call
+ * that uses the workspace; every call that completes leaves them zero, and no
+ * other byte's value matters.  After GLOWQ_ERR_CUDA or a recorded
+ * GLOWQ_ERR_TIMEOUT zero them again.  Calls that may overlap need separate
+ * workspaces.  0 for arguments that the forward calls refuse.
+ */
+GLOWQ_API size_t glowq_w8a8_workspace_bytes(int64_t T, int64_t d, int32_t r, const int64_t* out_features,
+                                            int32_t m);
+
+/*
+ * W8A8 group and solo forward.  Arguments as for glowq_group_forward /
+ * glowq_solo_forward; X is the fp16 input (quantised inside the call), d at
+ * most 131072 (the integer sum stays below 2^31), workspace of
+ * glowq_w8a8_workspace_bytes(T, d, r, out_features, m) bytes (always needed
+ * when T > 0).
+ */
+GLOWQ_API glowq_status glowq_group_forward_w8a8(const glowq_int8_module* mods, int32_t m, int64_t d,
+                                                const uint16_t* B, int32_t r, const uint16_t* X, int64_t T,
+                                                uint16_t* R_out, void* workspace, size_t workspace_bytes,
+                                                void* stream);
+GLOWQ_API glowq_status glowq_solo_forward_w8a8(const glowq_int8_module* mod, int64_t d, const uint16_t* B,
+                                               int32_t r, const uint16_t* X, int64_t T, void* workspace,
+                                               size_t workspace_bytes, void* stream);
+
+/*
  * Solo module forward that allocates nothing (the GlowQ pages have no
  * counterpart: this is a deployment convenience of this library).
  *

@@ -166,6 +166,85 @@ static glowq_status fp4_views(glowq_format fmt, const glowq_fp4_module* mods, in
     return GLOWQ_OK;
 }
 
+// W8A8 workspace: [zero region: tickets][codes][token scales][solo R][R partials][k-split sums]
+struct W8A8Layout {
+    size_t codes, scales, R, partial, slots, total;
+    Int8GemvPlan gemv;
+    int64_t chunk;       // tokens per pass
+};
+static W8A8Layout w8a8_layout(int64_t T, int64_t d, int32_t r, int64_t tiles) {
+    W8A8Layout L;
+    L.chunk = T < kInt8SmallTokens ? T : kInt8SmallTokens;
+    const int64_t tok = int8_small_tokens(L.chunk);
+    L.gemv = plan_int8_gemv(L.chunk, d, tiles, r, device_sm_count());
+    L.codes = kInt8ZeroBytes;
+    L.scales = L.codes + align_up((size_t)tok * d, 256);
+    L.R = L.scales + align_up((size_t)tok * 4, 256);
+    L.partial = L.R + align_up((size_t)T * r * 2, 256);
+    L.slots = L.partial;
+    L.total = L.slots + L.gemv.slot_bytes;
+    return L;
+}
+
+// Validation of 8-bit integer modules and their conversion to module views.
+static glowq_status int8_views(const glowq_int8_module* mods, int32_t m, int64_t d, const uint16_t* B, int32_t r,
+                               const uint16_t* X, int64_t T, Int8ModuleView* hm, int64_t* tiles) {
+    if (!mods || m < 1 || m > GLOWQ_MAX_MODULES) return GLOWQ_ERR_ARG;
+    glowq_module tmp[GLOWQ_MAX_MODULES];
+    *tiles = 0;
+    for (int i = 0; i < m; ++i) {
+        const glowq_int8_module& f = mods[i];
+        if (!f.scales) return GLOWQ_ERR_ARG;
+        if (reinterpret_cast<uintptr_t>(f.scales) & 3u) return GLOWQ_ERR_ALIGN;
+        // the shared checks of the INT4 path (zeros are not used: any non-null value)
+        tmp[i] = {reinterpret_cast<const uint32_t*>(f.codes), reinterpret_cast<const uint16_t*>(f.scales),
+                  reinterpret_cast<const uint8_t*>(f.scales), f.A, f.out_features, f.Y, f.ldY};
+    }
+    glowq_status v = validate_forward(tmp, m, d, B, r, X, T);
+    if (v != GLOWQ_OK) return v;
+    if (d > kInt8MaxD) return GLOWQ_ERR_SHAPE;
+    for (int i = 0; i < m; ++i) {
+        hm[i] = {mods[i].codes, mods[i].scales, (r > 0) ? mods[i].A : nullptr, mods[i].Y, mods[i].ldY,
+                 mods[i].out_features};
+        *tiles += mods[i].out_features / 16;
+    }
+    return GLOWQ_OK;
+}
+
+static glowq_status w8a8_impl(const glowq_int8_module* mods, int32_t m, int64_t d, const uint16_t* B, int32_t r,
+                              const uint16_t* X, int64_t T, uint16_t* R_out, void* workspace, size_t workspace_bytes,
+                              cudaStream_t st, bool solo) {
+    Int8ModuleView hm[GLOWQ_MAX_MODULES];
+    int64_t tiles = 0;
+    glowq_status v = int8_views(mods, m, d, B, r, X, T, hm, &tiles);
+    if (v != GLOWQ_OK) return v;
+    if (T == 0) return GLOWQ_OK;
+    if (!solo && r > 0) {
+        if (!R_out) return GLOWQ_ERR_ARG;
+        if (!aligned16(R_out)) return GLOWQ_ERR_ALIGN;
+    }
+    const W8A8Layout L = w8a8_layout(T, d, r, tiles);
+    if (!workspace || workspace_bytes < L.total) return GLOWQ_ERR_ARG;
+    if (!aligned16(workspace)) return GLOWQ_ERR_ALIGN;
+    if (!L.gemv.ok) return GLOWQ_ERR_UNSUPPORTED;
+    char* ws = static_cast<char*>(workspace);
+    uint16_t* R = solo ? reinterpret_cast<uint16_t*>(ws + L.R) : R_out;
+    for (int64_t t0 = 0; t0 < T; t0 += L.chunk) {
+        const int64_t n = T - t0 < L.chunk ? T - t0 : L.chunk;
+        const Int8GemvPlan p = plan_int8_gemv(L.chunk, d, tiles, r, device_sm_count());
+        Int8ModuleView cm[GLOWQ_MAX_MODULES];
+        for (int i = 0; i < m; ++i) {
+            cm[i] = hm[i];
+            cm[i].Y += t0 * hm[i].ldY;
+        }
+        if (launch_int8_small(cm, m, (int)d, (int)n, (int)L.chunk, r, X + t0 * d, B, R ? R + t0 * r : nullptr,
+                              reinterpret_cast<int8_t*>(ws + L.codes), reinterpret_cast<float*>(ws + L.scales),
+                              reinterpret_cast<unsigned int*>(ws), reinterpret_cast<int*>(ws + L.slots), p, st) != cudaSuccess)
+            return GLOWQ_ERR_CUDA;
+    }
+    return GLOWQ_OK;
+}
+
 }  // namespace glowq
 
 using namespace glowq;
@@ -457,6 +536,61 @@ glowq_status glowq_solo_forward_w4a8(const glowq_module* mod, int64_t d, const u
                                      const uint16_t* X, int64_t T, void* workspace, size_t workspace_bytes,
                                      void* stream) {
     return w4a8_impl(mod, 1, d, B, r, X, T, nullptr, workspace, workspace_bytes, (cudaStream_t)stream, true);
+}
+
+glowq_status glowq_pack_int8(const float* W, int64_t O, int64_t d, int8_t* codes, float* scales, void* stream) {
+    if (O < 0 || d < 0) return GLOWQ_ERR_ARG;
+    if (d % GLOWQ_GROUP_SIZE != 0 || O > ((int64_t)1 << 30)) return GLOWQ_ERR_SHAPE;
+    if (O == 0 || d == 0) return GLOWQ_OK;
+    if (!W || !codes || !scales) return GLOWQ_ERR_ARG;
+    if (!aligned16(W) || !aligned16(codes) || (reinterpret_cast<uintptr_t>(scales) & 3u)) return GLOWQ_ERR_ALIGN;
+    return launch_pack_int8(W, O, d, codes, scales, (cudaStream_t)stream) == cudaSuccess ? GLOWQ_OK : GLOWQ_ERR_CUDA;
+}
+
+glowq_status glowq_dequant_int8(const int8_t* codes, const float* scales, int64_t O, int64_t d, uint16_t* W_deq,
+                                void* stream) {
+    if (O < 0 || d < 0) return GLOWQ_ERR_ARG;
+    if (d % GLOWQ_GROUP_SIZE != 0 || O > ((int64_t)1 << 30)) return GLOWQ_ERR_SHAPE;
+    if (O == 0 || d == 0) return GLOWQ_OK;
+    if (!codes || !scales || !W_deq) return GLOWQ_ERR_ARG;
+    if (!aligned16(codes) || !aligned16(W_deq) || (reinterpret_cast<uintptr_t>(scales) & 3u)) return GLOWQ_ERR_ALIGN;
+    return launch_dequant_int8(codes, scales, O, d, W_deq, (cudaStream_t)stream) == cudaSuccess ? GLOWQ_OK
+                                                                                              : GLOWQ_ERR_CUDA;
+}
+
+glowq_status glowq_quantize_act_int8(const uint16_t* X, int64_t T, int64_t d, int8_t* codes, float* scales,
+                                     void* stream) {
+    if (T < 0 || d < 0) return GLOWQ_ERR_ARG;
+    if (d % GLOWQ_GROUP_SIZE != 0 || T > ((int64_t)1 << 30)) return GLOWQ_ERR_SHAPE;
+    if (T == 0 || d == 0) return GLOWQ_OK;
+    if (!X || !codes || !scales) return GLOWQ_ERR_ARG;
+    if (!aligned16(X) || !aligned16(codes) || (reinterpret_cast<uintptr_t>(scales) & 3u)) return GLOWQ_ERR_ALIGN;
+    return launch_quantize_act_int8(X, T, d, codes, scales, (cudaStream_t)stream) == cudaSuccess ? GLOWQ_OK
+                                                                                               : GLOWQ_ERR_CUDA;
+}
+
+size_t glowq_w8a8_workspace_bytes(int64_t T, int64_t d, int32_t r, const int64_t* out_features, int32_t m) {
+    if (T <= 0 || T > ((int64_t)1 << 30) || d <= 0 || d % GLOWQ_GROUP_SIZE != 0 || d > kInt8MaxD || r < 0 ||
+        r > GLOWQ_MAX_RANK || r % 8 != 0 || !out_features || m < 1 || m > GLOWQ_MAX_MODULES)
+        return 0;
+    int64_t tiles = 0;
+    for (int i = 0; i < m; ++i) {
+        if (out_features[i] <= 0 || out_features[i] % 16 != 0 || out_features[i] > ((int64_t)1 << 30)) return 0;
+        tiles += out_features[i] / 16;
+    }
+    return w8a8_layout(T, d, r, tiles).total;
+}
+
+glowq_status glowq_group_forward_w8a8(const glowq_int8_module* mods, int32_t m, int64_t d, const uint16_t* B,
+                                      int32_t r, const uint16_t* X, int64_t T, uint16_t* R_out, void* workspace,
+                                      size_t workspace_bytes, void* stream) {
+    return w8a8_impl(mods, m, d, B, r, X, T, R_out, workspace, workspace_bytes, (cudaStream_t)stream, false);
+}
+
+glowq_status glowq_solo_forward_w8a8(const glowq_int8_module* mod, int64_t d, const uint16_t* B, int32_t r,
+                                     const uint16_t* X, int64_t T, void* workspace, size_t workspace_bytes,
+                                     void* stream) {
+    return w8a8_impl(mod, 1, d, B, r, X, T, nullptr, workspace, workspace_bytes, (cudaStream_t)stream, true);
 }
 
 glowq_status glowq_selftest_wait_timeout(uint32_t polls, void* stream) {

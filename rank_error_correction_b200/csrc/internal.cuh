@@ -74,6 +74,35 @@ cudaError_t launch_pack_fp4(int fmt, const float* W, int64_t O, int64_t d, uint3
                             float* tensor_scale, cudaStream_t st);
 cudaError_t launch_dequant_fp4(int fmt, const uint32_t* codes, const uint8_t* scales, const float* tensor_scale,
                                int64_t O, int64_t d, uint16_t* out, cudaStream_t st);
+// int8.cu: 8-bit integer weights and activations
+struct Int8ModuleView {
+    const int8_t* q;     // codes [O][d]
+    const float* s;      // scales [O]
+    const uint16_t* A;   // nullptr: correction off for this module
+    uint16_t* Y;
+    int64_t ldY;
+    int64_t O;
+};
+constexpr int64_t kInt8MaxD = 131072;          // 127^2 d < 2^31
+constexpr int kInt8SmallTokens = 64;           // tokens up to which the weight-streaming product runs
+constexpr int kInt8ZeroBytes = 65536;          // tickets at the workspace's start
+constexpr int kInt8MaxTickets = kInt8ZeroBytes / 4;
+// Decomposition of the small-T product: S CTAs share a tile's k, wk warps of a CTA.
+struct Int8GemvPlan {
+    bool ok;             // false: the shape is left to the tensor-core GEMM
+    int S, wk, grid, smem;
+    size_t slot_bytes;   // partial sums (S > 1)
+};
+int int8_small_tokens(int64_t T);
+Int8GemvPlan plan_int8_gemv(int64_t T, int64_t d, int64_t tiles, int r, int num_sms);
+cudaError_t launch_pack_int8(const float* W, int64_t O, int64_t d, int8_t* codes, float* scales, cudaStream_t st);
+cudaError_t launch_dequant_int8(const int8_t* codes, const float* scales, int64_t O, int64_t d, uint16_t* out,
+                                cudaStream_t st);
+cudaError_t launch_quantize_act_int8(const uint16_t* X, int64_t T, int64_t d, int8_t* codes, float* scales,
+                                     cudaStream_t st);
+cudaError_t launch_int8_small(const Int8ModuleView* mods, int m, int d, int T, int width, int r, const uint16_t* X,
+                              const uint16_t* B, uint16_t* R, int8_t* xq, float* xs, unsigned int* tickets, int* slots,
+                              const Int8GemvPlan& p, cudaStream_t st);
 // solve.cu: the offline group solve (float64)
 struct SolveModule {
     const float* W;      // O x d fp32 weights

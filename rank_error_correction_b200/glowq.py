@@ -8,6 +8,7 @@ exception is raised.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes as C
 import dataclasses
 import os
@@ -50,6 +51,11 @@ class _Module(C.Structure):
                 ("A", C.c_void_p), ("out_features", C.c_int64), ("Y", C.c_void_p), ("ldY", C.c_int64)]
 
 
+class _Int8Module(C.Structure):
+    _fields_ = [("codes", C.c_void_p), ("scales", C.c_void_p), ("A", C.c_void_p), ("out_features", C.c_int64),
+                ("Y", C.c_void_p), ("ldY", C.c_int64)]
+
+
 _lib = None
 
 
@@ -82,6 +88,13 @@ def lib() -> C.CDLL:
         L.glowq_w4a8_workspace_bytes.restype = C.c_size_t
         L.glowq_group_forward_w4a8.argtypes = [C.POINTER(_Module), i32, i64, p, i32, p, i64, p, p, C.c_size_t, p]
         L.glowq_solo_forward_w4a8.argtypes = [C.POINTER(_Module), i64, p, i32, p, i64, p, C.c_size_t, p]
+        L.glowq_pack_int8.argtypes = [p, i64, i64, p, p, p]
+        L.glowq_dequant_int8.argtypes = [p, p, i64, i64, p, p]
+        L.glowq_quantize_act_int8.argtypes = [p, i64, i64, p, p, p]
+        L.glowq_w8a8_workspace_bytes.argtypes = [i64, i64, i32, p, i32]
+        L.glowq_w8a8_workspace_bytes.restype = C.c_size_t
+        L.glowq_group_forward_w8a8.argtypes = [C.POINTER(_Int8Module), i32, i64, p, i32, p, i64, p, p, C.c_size_t, p]
+        L.glowq_solo_forward_w8a8.argtypes = [C.POINTER(_Int8Module), i64, p, i32, p, i64, p, C.c_size_t, p]
         L.glowq_solve_workspace_bytes.argtypes = [i64, i64, i32, i32]
         L.glowq_solve_workspace_bytes.restype = C.c_size_t
         L.glowq_group_solve.argtypes = [C.POINTER(_SolveModule), i32, i64, p, p, i32, i32, i32, p, p, p, p, p, p, p,
@@ -97,7 +110,8 @@ def lib() -> C.CDLL:
                   "glowq_solo_forward_noalloc", "glowq_group_forward_fp4", "glowq_solo_forward_fp4",
                   "glowq_select_restore", "glowq_select_restore_scores", "glowq_error_norms", "glowq_group_solve",
                   "glowq_quantize_act_e4m3", "glowq_group_forward_w4a8", "glowq_solo_forward_w4a8",
-                  "glowq_get_device_status",
+                  "glowq_pack_int8", "glowq_dequant_int8", "glowq_quantize_act_int8", "glowq_group_forward_w8a8",
+                  "glowq_solo_forward_w8a8", "glowq_get_device_status",
                   "glowq_selftest_wait_timeout"):
             getattr(L, f).restype = st
         _lib = L
@@ -522,6 +536,185 @@ def solo_forward_w4a8(mod: QModule, B, X, Y=None, workspace=None, stream=None):
     _check(lib().glowq_solo_forward_w4a8(arr, d, _ptr(B), r, _ptr(X), T, _ptr(workspace), ws_n, _stream(stream)),
            "glowq_solo_forward_w4a8")
     return Y
+
+
+# ------------------------------------------------------------------- W8A8 ----
+
+def _require(t, name: str, dtype, device=None, dim: Optional[int] = None, contiguous: bool = True):
+    """A CUDA tensor of this dtype (and device, and rank); contiguous unless said otherwise."""
+    if not t.is_cuda:
+        raise ValueError(f"{name}: libglowq operates on CUDA tensors only")
+    if t.dtype != dtype or (dim is not None and t.dim() != dim):
+        raise ValueError(f"{name} must be a {'' if dim is None else f'{dim}-D '}{dtype} tensor")
+    if device is not None and t.device != device:
+        raise ValueError(f"{name} is on {t.device}, not on {device}")
+    if contiguous and not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+
+
+def _on(stream):
+    """What a call allocates belongs to the stream that the call runs on."""
+    import torch
+    return contextlib.nullcontext() if stream is None else torch.cuda.stream(stream)
+
+
+class _Call:
+    """A library call with its arguments marshalled once.  Calling it enqueues
+    the kernels on `stream` (default: the current stream of the tensors'
+    device) and returns the outputs.  The tensors must stay alive and at the
+    same addresses while the call is used (it holds references to them)."""
+
+    def __init__(self, name: str, device, args, outputs, keep):
+        self._name, self._fn, self._args, self._keep = name, getattr(lib(), name), args, keep
+        self._device, self.outputs = device, outputs
+
+    def __call__(self, stream=None):
+        import torch
+        if stream is None:
+            stream = torch.cuda.current_stream(self._device)
+        if torch.cuda.current_device() == self._device.index:
+            rc = self._fn(*self._args, C.c_void_p(stream.cuda_stream))
+        else:
+            with torch.cuda.device(self._device):
+                rc = self._fn(*self._args, C.c_void_p(stream.cuda_stream))
+        if rc != 0:
+            raise GlowQError(rc, self._name)
+        return self.outputs
+
+
+def pack_int8(W, stream=None):
+    """W (O x d fp32, CUDA) -> (codes int8 [O, d], scales float32 [O], one per output channel)."""
+    import torch
+    _require(W, "W", torch.float32, dim=2)
+    O, d = W.shape
+    q = torch.empty((O, d), dtype=torch.int8, device=W.device)
+    s = torch.empty(O, dtype=torch.float32, device=W.device)
+    return _Call("glowq_pack_int8", W.device, (_ptr(W), O, d, _ptr(q), _ptr(s)), (q, s), W)(stream)
+
+
+def dequant_int8(codes, scales, stream=None):
+    """fp16 weights of the codes and scales of pack_int8."""
+    import torch
+    _require(codes, "codes", torch.int8, dim=2)
+    _require(scales, "scales", torch.float32, codes.device, 1)
+    O, d = codes.shape
+    if scales.shape[0] != O:
+        raise ValueError("scales must have one value per row of codes")
+    out = torch.empty((O, d), dtype=torch.float16, device=codes.device)
+    return _Call("glowq_dequant_int8", codes.device, (_ptr(codes), _ptr(scales), O, d, _ptr(out)), out,
+                 (codes, scales))(stream)
+
+
+def quantize_act_int8(X, stream=None):
+    """Per-token int8 activations: X (T x d fp16, CUDA) -> (codes int8 [T, d], scales float32 [T])."""
+    import torch
+    _require(X, "X", torch.float16, dim=2)
+    T, d = X.shape
+    codes = torch.empty((T, d), dtype=torch.int8, device=X.device)
+    scales = torch.empty(T, dtype=torch.float32, device=X.device)
+    return _Call("glowq_quantize_act_int8", X.device, (_ptr(X), T, d, _ptr(codes), _ptr(scales)), (codes, scales),
+                 X)(stream)
+
+
+@dataclasses.dataclass
+class Int8Module:
+    """One 8-bit integer module: codes (int8 [O, d]), scales (float32 [O], one per
+    output channel) and optional left factor A (O x r fp16)."""
+    codes: "object"
+    scales: "object"
+    A: Optional["object"] = None
+
+    @property
+    def out_features(self) -> int:
+        return int(self.codes.shape[0])
+
+
+def w8a8_workspace_bytes(T: int, d: int, r: int, out_features: Sequence[int]) -> int:
+    outs = (C.c_int64 * len(out_features))(*[int(o) for o in out_features])
+    return int(lib().glowq_w8a8_workspace_bytes(T, d, r, outs, len(out_features)))
+
+
+def w8a8_workspace(T: int, d: int, r: int, out_features: Sequence[int], device="cuda"):
+    """Zero-filled (the tickets at its start must begin at zero; every call leaves them so)."""
+    import torch
+    n = max(w8a8_workspace_bytes(T, d, r, out_features), 16)
+    return torch.zeros(n, dtype=torch.uint8, device=device)
+
+
+class Int8ForwardPlan(_Call):
+    """A W8A8 group (or, with solo=True, solo) forward with its arguments
+    marshalled once.  Calling it returns Ys; R is in `.R` (None for a solo
+    module or without a correction)."""
+
+    # A workspace made here is zeroed on the stream that is current at that
+    # moment: calls on another stream have to be ordered behind it.
+    def __init__(self, mods: Sequence[Int8Module], B, X, Ys=None, R_out=None, workspace=None, solo: bool = False):
+        import torch
+        f16 = torch.float16
+        _require(X, "X", f16, dim=2)
+        T, d = X.shape
+        dev = X.device
+        r = 0
+        if B is not None:
+            _require(B, "B", f16, dev, 2)
+            r = int(B.shape[0])
+            if B.shape[1] != d:
+                raise ValueError("B must be r x d")
+        if solo and len(mods) != 1:
+            raise ValueError("a solo call has one module")
+        if Ys is None:
+            Ys = [torch.empty((T, m.out_features), dtype=f16, device=dev) for m in mods]
+        items = []
+        for m, Y in zip(mods, Ys, strict=True):
+            _require(m.codes, "codes", torch.int8, dev, 2)
+            _require(m.scales, "scales", torch.float32, dev, 1)
+            _require(Y, "Y", f16, dev, 2, contiguous=False)
+            O = m.out_features
+            if m.codes.shape[1] != d or m.scales.shape[0] != O:
+                raise ValueError("codes must be O x d and scales O")
+            if Y.shape[0] < T or Y.shape[1] < O or Y.stride(1) != 1:
+                raise ValueError("outputs must be T x O with unit column stride")
+            if m.A is not None and r > 0:
+                _require(m.A, "A", f16, dev, 2)
+                if tuple(m.A.shape) != (O, r):
+                    raise ValueError("A must be O x r")
+            # a tensor of one row may report any row stride
+            ld = Y.stride(0) if Y.shape[0] > 1 else max(Y.stride(0), (O + 7) // 8 * 8)
+            items.append(_Int8Module(m.codes.data_ptr(), m.scales.data_ptr(), _ptr(m.A) if r > 0 else None, O,
+                                     Y.data_ptr(), ld))
+        outs = [m.out_features for m in mods]
+        if workspace is None:
+            workspace = w8a8_workspace(T, d, r, outs, dev)
+        _require(workspace, "workspace", torch.uint8, dev)
+        if not solo and r > 0:
+            if R_out is None:
+                R_out = torch.empty((T, r), dtype=f16, device=dev)
+            _require(R_out, "R_out", f16, dev, 2)
+            if R_out.shape[0] < T or R_out.shape[1] != r:
+                raise ValueError("R_out must be T x r")
+        else:
+            R_out = None
+        self.R = R_out
+        arr = (_Int8Module * len(items))(*items)
+        tail = (_ptr(workspace), workspace.numel())
+        if solo:
+            name, args = "glowq_solo_forward_w8a8", (arr, d, _ptr(B), r, _ptr(X), T) + tail
+        else:
+            name, args = "glowq_group_forward_w8a8", (arr, len(items), d, _ptr(B), r, _ptr(X), T, _ptr(R_out)) + tail
+        super().__init__(name, dev, args, list(Ys), (list(mods), B, X, workspace, R_out))
+
+
+def group_forward_w8a8(mods: Sequence[Int8Module], B, X, Ys=None, R_out=None, workspace=None, stream=None):
+    """group_forward with 8-bit integer weights (a scale per output channel) and
+    activations (a scale per token); X is fp16 and is quantised inside the call."""
+    with _on(stream):
+        plan = Int8ForwardPlan(mods, B, X, Ys, R_out, workspace)
+        return plan(stream), plan.R
+
+
+def solo_forward_w8a8(mod: Int8Module, B, X, Y=None, workspace=None, stream=None):
+    with _on(stream):
+        return Int8ForwardPlan([mod], B, X, None if Y is None else [Y], None, workspace, solo=True)(stream)[0]
 
 
 # ---------------------------------------------------------- offline solve ----
