@@ -57,7 +57,8 @@ typedef enum glowq_status {
     GLOWQ_ERR_CUDA = 4,         /* CUDA runtime error while enqueueing      */
     GLOWQ_ERR_TIMEOUT = 5,      /* a device-side bounded wait ran out       */
     GLOWQ_ERR_UNSUPPORTED = 6,  /* valid request outside this build's scope */
-    GLOWQ_ERR_NUMERIC = 7       /* a factorisation met a non-positive pivot  */
+    GLOWQ_ERR_NUMERIC = 7,      /* a factorisation met a non-positive pivot  */
+    GLOWQ_ERR_INDEX = 8         /* device data (page, slot, length, row) out of range */
 } glowq_status;
 
 #define GLOWQ_GROUP_SIZE 128    /* INT4 quantisation group along d          */
@@ -533,8 +534,128 @@ GLOWQ_API glowq_status glowq_error_norms(const float* W, const uint32_t* qweight
                                const uint16_t* scales, const uint8_t* zeros,
                                int64_t O, int64_t d, double* row_norms, void* stream);
 
+/*
+ * Paged 8-bit key/value cache: what stands between a layer's Q/K/V group and
+ * its o_proj when serving (the pages leave attention out; the format is this
+ * library's).  A page holds GLOWQ_KV_PAGE consecutive tokens of one sequence.
+ * A complete page is stored in 8-bit integers with one scale per kv head for
+ * its keys and one for its values:
+ *   s = fp32(max(max |x|, 2^-24) / 127) over the page's 64 x D values of the
+ *   head, code = rint(fp32(x / s)) in -127..127 (IEEE fp32, rint to even;
+ *   a block that holds an infinity or a NaN: s = NaN, codes 0).
+ * The tokens of a sequence's incomplete last page stay in fp16 in the
+ * sequence's tail until the page completes.  Each code is so rounded once, and
+ * what the cache holds depends on the tokens alone, not on how they were cut
+ * into appends.  Complete pages never change.
+ * Device pointers (16-byte aligned), caller-owned:
+ *   k_codes   [pages][kv_heads][D/64][64 tokens][64]   int8 (panels of 64 dimensions)
+ *   v_codes   [pages][kv_heads][D][64 tokens]          int8 (tokens innermost)
+ *   k_scales, v_scales  [pages][kv_heads] fp32
+ *   k_tail, v_tail      [slots][kv_heads][64 tokens][D] fp16
+ * head_dim D is 64 or 128.
+ */
+#define GLOWQ_KV_PAGE 64
+typedef struct glowq_kv_cache {
+    int8_t* k_codes;
+    int8_t* v_codes;
+    float* k_scales;
+    float* v_scales;
+    uint16_t* k_tail;
+    uint16_t* v_tail;
+    int64_t pages;
+    int64_t slots;
+    int32_t kv_heads;
+    int32_t head_dim;
+} glowq_kv_cache;
+
+/*
+ * One step's batch of sequences.  Token-major arrays of the step (queries,
+ * keys, values, outputs) have `rows` rows; those of sequence b are
+ * q_start[b] .. q_start[b+1] - 1, its new tokens in order, at positions
+ * kv_len[b] - n .. kv_len[b] - 1 (n its new tokens: kv_len counts them).
+ *   q_start     device int32 [n_seq + 1]
+ *   kv_len      device int32 [n_seq], tokens of the sequence with this step's
+ *   page_table  device int32 [n_seq][max_pages], page of tokens 64 p .. 64 p + 63
+ *               (read for complete pages only)
+ *   slot        device int32 [n_seq], the sequence's tail
+ *   max_new     no sequence has more new tokens (host bound that sizes the launch)
+ * Rows from q_start[n_seq] on are padding: neither read nor written.  No two
+ * sequences of a batch share a slot; they may share complete pages that the
+ * step does not write.  The device data are checked where they are used: a
+ * value out of range records GLOWQ_ERR_INDEX in the device status word
+ * (glowq_get_device_status), touches nothing outside the caller's arrays, and
+ *   - a sequence whose rows are not inside the batch, or more than max_new, is skipped;
+ *   - append: a sequence whose length, slot or position is out of range is
+ *     skipped, a page out of range is not written;
+ *   - attention: a page out of range is left out; a sequence whose length or
+ *     slot is out of range gives zero rows;
+ *   - read: what cannot be read is zero.
+ */
+typedef struct glowq_kv_batch {
+    const int32_t* q_start;
+    const int32_t* kv_len;
+    const int32_t* page_table;
+    const int32_t* slot;
+    int32_t n_seq;
+    int32_t max_pages;
+    int64_t rows;
+    int32_t max_new;
+} glowq_kv_batch;
+
+/*
+ * Append the step's keys and values, rotated by position on the way.
+ *   K, V     device fp16, rows x kv_heads D columns, row pitches ldK, ldV
+ *            (elements, % 8 == 0): e.g. column slices of a Q/K/V group's output
+ *   Q        device fp16, rows x q_heads D (pitch ldQ), or NULL (q_heads 0):
+ *            rotated into Q_out (pitch ldQ_out), which may be Q itself
+ *   rope     device fp32 [rope_len][D]: cosines of the D/2 pairs of the row's
+ *            position, then their sines; pair i is (x_i, x_{i + D/2}) ->
+ *            (x_i cos - x_{i+D/2} sin, x_{i+D/2} cos + x_i sin), two fp32
+ *            products and a sum, unfused, rounded to fp16.  NULL: no rotation
+ *            (Q, if given, is copied).  Positions from rope_len on are out of range.
+ * Running the same step again writes the same values, unless the step began
+ * inside a page, completed it and left another page incomplete (the tail that
+ * it began with is then overwritten).
+ */
+GLOWQ_API glowq_status glowq_kv_append(const glowq_kv_cache* cache, const glowq_kv_batch* batch, const uint16_t* Q,
+                                       int64_t ldQ, int32_t q_heads, const uint16_t* K, int64_t ldK,
+                                       const uint16_t* V, int64_t ldV, const float* rope, int64_t rope_len,
+                                       uint16_t* Q_out, int64_t ldQ_out, void* stream);
+
+/*
+ * What the cache holds at positions first[b] .. first[b] + count - 1 of every
+ * sequence (first: device int32 [n_seq], NULL: 0), to check or export it:
+ * K, V  device fp16 [n_seq][count][kv_heads][D]: fp16_RN(code * scale) of
+ * complete pages, the tail's values, zero from kv_len on.  count <= 2^29.
+ */
+GLOWQ_API glowq_status glowq_kv_read(const glowq_kv_cache* cache, const glowq_kv_batch* batch, const int32_t* first,
+                                     int64_t count, uint16_t* K, uint16_t* V, void* stream);
+
+/*
+ * Causal attention of the step's queries over the cache (after the step's
+ * append): new token i of sequence b, query head h, sees the keys and values
+ * of kv head h / (q_heads / kv_heads) at positions up to its own,
+ *   Y = fp16( sum_j softmax_j(scale q . k_j) v_j ).
+ * Keys and values are what glowq_kv_read gives before its rounding to fp16.
+ * Scores, softmax statistics and sums are fp32; weights are rounded to fp16
+ * for the product with the values.  A row that sees nothing (kv_len below its
+ * sequence's new tokens) is zero.  A key, value or page scale that is not
+ * finite makes NaN of the rows that see it, and of no other.
+ *   Q  device fp16, rows x q_heads D (pitch ldQ); q_heads % kv_heads == 0
+ *   Y  device fp16, rows x q_heads D (pitch ldY); may not overlap Q
+ *   workspace  glowq_kv_attention_workspace_bytes bytes: its first 65536 must
+ *              be zero before the first call that uses it and are zero after
+ *              every call that completes; no other byte's value matters.
+ *              Calls that may overlap need separate workspaces.
+ */
+GLOWQ_API size_t glowq_kv_attention_workspace_bytes(const glowq_kv_cache* cache, const glowq_kv_batch* batch,
+                                                    int32_t q_heads);
+GLOWQ_API glowq_status glowq_kv_attention(const glowq_kv_cache* cache, const glowq_kv_batch* batch,
+                                          const uint16_t* Q, int64_t ldQ, int32_t q_heads, float scale, uint16_t* Y,
+                                          int64_t ldY, void* workspace, size_t workspace_bytes, void* stream);
+
 /* Reads and clears this device's status word (GLOWQ_OK, GLOWQ_ERR_TIMEOUT,
-   GLOWQ_ERR_NUMERIC, or GLOWQ_ERR_ALIGN if a decode kernel found its shared
+   GLOWQ_ERR_NUMERIC, GLOWQ_ERR_INDEX, or GLOWQ_ERR_ALIGN if a decode kernel found its shared
    memory base not 1 KB-aligned and skipped its work); synchronises `stream`
    first. */
 GLOWQ_API glowq_status glowq_get_device_status(void* stream);

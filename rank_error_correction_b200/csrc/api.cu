@@ -7,6 +7,7 @@
 
 #include "common.cuh"
 #include "internal.cuh"
+#include "kvcache.cuh"
 
 namespace glowq {
 
@@ -245,6 +246,39 @@ static glowq_status w8a8_impl(const glowq_int8_module* mods, int32_t m, int64_t 
     return GLOWQ_OK;
 }
 
+// Checks of a cache and a batch, and their device views.
+static glowq_status kv_views(const glowq_kv_cache* c, const glowq_kv_batch* b, KvCacheView* cv, KvBatchView* bv) {
+    if (!c || !b || c->pages < 0 || c->slots < 0 || c->kv_heads < 1 || b->n_seq < 0 || b->max_pages < 0 || b->rows < 0 ||
+        b->max_new < 0)
+        return GLOWQ_ERR_ARG;
+    if (c->head_dim != 64 && c->head_dim != 128) return GLOWQ_ERR_SHAPE;
+    if (c->kv_heads > 65536 || b->n_seq > (1 << 24) || b->max_pages > (1 << 24) || b->rows > ((int64_t)1 << 30) ||
+        c->pages > ((int64_t)1 << 31) - 1 || c->slots > ((int64_t)1 << 31) - 1)
+        return GLOWQ_ERR_SHAPE;
+    if (c->pages > 0 && (!c->k_codes || !c->v_codes || !c->k_scales || !c->v_scales)) return GLOWQ_ERR_ARG;
+    if (c->slots > 0 && (!c->k_tail || !c->v_tail)) return GLOWQ_ERR_ARG;
+    if (b->n_seq > 0 && (!b->q_start || !b->kv_len || !b->slot || (b->max_pages > 0 && !b->page_table)))
+        return GLOWQ_ERR_ARG;
+    if (!aligned16(c->k_codes) || !aligned16(c->v_codes) || !aligned16(c->k_tail) || !aligned16(c->v_tail))
+        return GLOWQ_ERR_ALIGN;
+    const uintptr_t words = reinterpret_cast<uintptr_t>(c->k_scales) | reinterpret_cast<uintptr_t>(c->v_scales) |
+                            reinterpret_cast<uintptr_t>(b->q_start) | reinterpret_cast<uintptr_t>(b->kv_len) |
+                            reinterpret_cast<uintptr_t>(b->page_table) | reinterpret_cast<uintptr_t>(b->slot);
+    if (words & 3u) return GLOWQ_ERR_ALIGN;
+    *cv = {c->k_codes, c->v_codes, c->k_scales, c->v_scales, c->k_tail, c->v_tail, c->pages, c->slots, c->kv_heads,
+           c->head_dim};
+    const int64_t most = b->max_new < b->rows ? b->max_new : b->rows;
+    *bv = {b->q_start, b->kv_len, b->page_table, b->slot, b->n_seq, b->max_pages, (int)b->rows, (int)most};
+    return GLOWQ_OK;
+}
+// A token-major fp16 array of `heads` heads: pitch at least its width, 16-byte rows.
+static glowq_status kv_array(const uint16_t* p, int64_t ld, int64_t heads, int head_dim) {
+    if (!p) return GLOWQ_ERR_ARG;
+    if (!aligned16(p) || ld < heads * head_dim || ld % 8 != 0) return GLOWQ_ERR_ALIGN;
+    return GLOWQ_OK;
+}
+static bool fits_grid(int64_t blocks) { return blocks <= INT32_MAX; }
+
 }  // namespace glowq
 
 using namespace glowq;
@@ -263,6 +297,7 @@ const char* glowq_status_string(glowq_status s) {
         case GLOWQ_ERR_TIMEOUT: return "a device-side bounded wait ran out";
         case GLOWQ_ERR_UNSUPPORTED: return "request outside this build's scope";
         case GLOWQ_ERR_NUMERIC: return "a factorisation met a non-positive pivot";
+        case GLOWQ_ERR_INDEX: return "a page, slot, length or row in device data is out of range";
     }
     return "unknown status";
 }
@@ -591,6 +626,88 @@ glowq_status glowq_solo_forward_w8a8(const glowq_int8_module* mod, int64_t d, co
                                      const uint16_t* X, int64_t T, void* workspace, size_t workspace_bytes,
                                      void* stream) {
     return w8a8_impl(mod, 1, d, B, r, X, T, nullptr, workspace, workspace_bytes, (cudaStream_t)stream, true);
+}
+
+glowq_status glowq_kv_append(const glowq_kv_cache* cache, const glowq_kv_batch* batch, const uint16_t* Q, int64_t ldQ,
+                             int32_t q_heads, const uint16_t* K, int64_t ldK, const uint16_t* V, int64_t ldV,
+                             const float* rope, int64_t rope_len, uint16_t* Q_out, int64_t ldQ_out, void* stream) {
+    KvCacheView c;
+    KvBatchView b;
+    glowq_status v = kv_views(cache, batch, &c, &b);
+    if (v != GLOWQ_OK) return v;
+    if (q_heads < 0 || rope_len < 0 || (!Q && q_heads > 0) || (rope_len > 0 && !rope)) return GLOWQ_ERR_ARG;
+    if (q_heads > 65536 || q_heads % c.kv_heads != 0) return GLOWQ_ERR_SHAPE;
+    if (b.n_seq == 0 || b.max_new == 0) return GLOWQ_OK;
+    if ((v = kv_array(K, ldK, c.kv_heads, c.head_dim)) != GLOWQ_OK) return v;
+    if ((v = kv_array(V, ldV, c.kv_heads, c.head_dim)) != GLOWQ_OK) return v;
+    if (Q && ((v = kv_array(Q, ldQ, q_heads, c.head_dim)) != GLOWQ_OK ||
+              (v = kv_array(Q_out, ldQ_out, q_heads, c.head_dim)) != GLOWQ_OK))
+        return v;
+    if (reinterpret_cast<uintptr_t>(rope) & 7u) return GLOWQ_ERR_ALIGN;
+    if (!fits_grid((int64_t)kv_touched_pages(b.max_new) * b.n_seq) ||
+        !fits_grid((int64_t)kv_touched_pages(b.max_new) * b.n_seq * c.kv_heads))
+        return GLOWQ_ERR_SHAPE;
+    const int len = rope_len > INT32_MAX ? INT32_MAX : (int)rope_len;
+    return launch_kv_append(c, b, Q, ldQ, q_heads, K, ldK, V, ldV, rope, len, Q_out, ldQ_out, (cudaStream_t)stream) ==
+                   cudaSuccess
+               ? GLOWQ_OK
+               : GLOWQ_ERR_CUDA;
+}
+
+glowq_status glowq_kv_read(const glowq_kv_cache* cache, const glowq_kv_batch* batch, const int32_t* first,
+                           int64_t count, uint16_t* K, uint16_t* V, void* stream) {
+    KvCacheView c;
+    KvBatchView b;
+    glowq_status v = kv_views(cache, batch, &c, &b);
+    if (v != GLOWQ_OK) return v;
+    if (count < 0) return GLOWQ_ERR_ARG;
+    if (count > kKvReadMax) return GLOWQ_ERR_SHAPE;
+    if (b.n_seq == 0 || count == 0) return GLOWQ_OK;
+    if (!K || !V) return GLOWQ_ERR_ARG;
+    if (!aligned16(K) || !aligned16(V) || (reinterpret_cast<uintptr_t>(first) & 3u)) return GLOWQ_ERR_ALIGN;
+    if (!fits_grid((int64_t)kv_touched_pages((int)count) * b.n_seq) ||
+        !fits_grid((int64_t)kv_touched_pages((int)count) * b.n_seq * c.kv_heads))
+        return GLOWQ_ERR_SHAPE;
+    return launch_kv_read(c, b, first, (int)count, K, V, (cudaStream_t)stream) == cudaSuccess ? GLOWQ_OK
+                                                                                            : GLOWQ_ERR_CUDA;
+}
+
+// Checks of an attention call's heads and sizes, shared with the workspace query.
+static glowq_status kv_attention_shape(const KvCacheView& c, const KvBatchView& b, int32_t q_heads) {
+    if (q_heads < 1) return GLOWQ_ERR_ARG;
+    if (q_heads > 65536 || q_heads % c.kv_heads != 0) return GLOWQ_ERR_SHAPE;
+    const int64_t rt = ((int64_t)b.max_new * (q_heads / c.kv_heads) + 15) / 16;
+    if (!fits_grid(rt * c.kv_heads) || !fits_grid(rt * c.kv_heads * b.n_seq)) return GLOWQ_ERR_SHAPE;
+    return GLOWQ_OK;
+}
+
+size_t glowq_kv_attention_workspace_bytes(const glowq_kv_cache* cache, const glowq_kv_batch* batch, int32_t q_heads) {
+    KvCacheView c;
+    KvBatchView b;
+    if (kv_views(cache, batch, &c, &b) != GLOWQ_OK || kv_attention_shape(c, b, q_heads) != GLOWQ_OK) return 0;
+    return kInt8ZeroBytes + plan_kv_attention(b, q_heads / c.kv_heads, c.kv_heads, c.head_dim, device_sm_count()).partial_bytes;
+}
+
+glowq_status glowq_kv_attention(const glowq_kv_cache* cache, const glowq_kv_batch* batch, const uint16_t* Q,
+                                int64_t ldQ, int32_t q_heads, float scale, uint16_t* Y, int64_t ldY, void* workspace,
+                                size_t workspace_bytes, void* stream) {
+    KvCacheView c;
+    KvBatchView b;
+    glowq_status v = kv_views(cache, batch, &c, &b);
+    if (v != GLOWQ_OK) return v;
+    if ((v = kv_attention_shape(c, b, q_heads)) != GLOWQ_OK) return v;
+    if (!(scale >= 0.f) || scale > 3.0e38f) return GLOWQ_ERR_ARG;
+    if (b.n_seq == 0 || b.max_new == 0) return GLOWQ_OK;
+    if ((v = kv_array(Q, ldQ, q_heads, c.head_dim)) != GLOWQ_OK) return v;
+    if ((v = kv_array(Y, ldY, q_heads, c.head_dim)) != GLOWQ_OK) return v;
+    const KvAttnPlan p = plan_kv_attention(b, q_heads / c.kv_heads, c.kv_heads, c.head_dim, device_sm_count());
+    if (!workspace || workspace_bytes < kInt8ZeroBytes + p.partial_bytes) return GLOWQ_ERR_ARG;
+    if (!aligned16(workspace)) return GLOWQ_ERR_ALIGN;
+    return launch_kv_attention(c, b, Q, ldQ, q_heads, scale, Y, ldY, reinterpret_cast<unsigned int*>(workspace),
+                               reinterpret_cast<float*>(static_cast<char*>(workspace) + kInt8ZeroBytes), p,
+                               (cudaStream_t)stream) == cudaSuccess
+               ? GLOWQ_OK
+               : GLOWQ_ERR_CUDA;
 }
 
 glowq_status glowq_selftest_wait_timeout(uint32_t polls, void* stream) {

@@ -505,7 +505,7 @@ cudaError_t launch_dequant_int8(const int8_t* codes, const float* scales, int64_
     dequant_int8_kernel<<<(unsigned)O, 256, 0, st>>>(codes, scales, d, reinterpret_cast<__half*>(out));
     return cudaGetLastError();
 }
-static cudaError_t launch_pdl(const void* fn, unsigned grid, unsigned block, size_t smem, cudaStream_t st, void** args) {
+cudaError_t launch_pdl(const void* fn, unsigned grid, unsigned block, size_t smem, cudaStream_t st, void** args) {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(grid);
     cfg.blockDim = dim3(block);

@@ -74,6 +74,10 @@ cudaError_t launch_pack_fp4(int fmt, const float* W, int64_t O, int64_t d, uint3
                             float* tensor_scale, cudaStream_t st);
 cudaError_t launch_dequant_fp4(int fmt, const uint32_t* codes, const uint8_t* scales, const float* tensor_scale,
                                int64_t O, int64_t d, uint16_t* out, cudaStream_t st);
+// A launch that may begin while the preceding kernel of the stream ends (the
+// kernel waits for it with pdl_wait before it touches anything it wrote).
+cudaError_t launch_pdl(const void* fn, unsigned grid, unsigned block, size_t smem, cudaStream_t st, void** args);
+
 // int8.cu: 8-bit integer weights and activations
 struct Int8ModuleView {
     const int8_t* q;     // codes [O][d]

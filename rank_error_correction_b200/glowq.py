@@ -20,6 +20,7 @@ LIB_PATH = os.path.join(_PKG, "libglowq.so")
 HEADER_PATH = os.path.join(os.path.dirname(_PKG), "include", "glowq.h")
 
 GROUP_SIZE = 128
+KV_PAGE = 64
 MAX_RANK = 256
 MAX_MODULES = 8
 
@@ -27,7 +28,8 @@ FMT_INT4, FMT_MXFP4, FMT_NVFP4 = 0, 1, 2
 FP4_BLOCK = {FMT_MXFP4: 32, FMT_NVFP4: 16}
 
 STATUS = {0: "GLOWQ_OK", 1: "GLOWQ_ERR_ARG", 2: "GLOWQ_ERR_SHAPE", 3: "GLOWQ_ERR_ALIGN",
-          4: "GLOWQ_ERR_CUDA", 5: "GLOWQ_ERR_TIMEOUT", 6: "GLOWQ_ERR_UNSUPPORTED", 7: "GLOWQ_ERR_NUMERIC"}
+          4: "GLOWQ_ERR_CUDA", 5: "GLOWQ_ERR_TIMEOUT", 6: "GLOWQ_ERR_UNSUPPORTED", 7: "GLOWQ_ERR_NUMERIC",
+          8: "GLOWQ_ERR_INDEX"}
 
 
 class GlowQError(RuntimeError):
@@ -54,6 +56,17 @@ class _Module(C.Structure):
 class _Int8Module(C.Structure):
     _fields_ = [("codes", C.c_void_p), ("scales", C.c_void_p), ("A", C.c_void_p), ("out_features", C.c_int64),
                 ("Y", C.c_void_p), ("ldY", C.c_int64)]
+
+
+class _KVCache(C.Structure):
+    _fields_ = [("k_codes", C.c_void_p), ("v_codes", C.c_void_p), ("k_scales", C.c_void_p), ("v_scales", C.c_void_p),
+                ("k_tail", C.c_void_p), ("v_tail", C.c_void_p), ("pages", C.c_int64), ("slots", C.c_int64),
+                ("kv_heads", C.c_int32), ("head_dim", C.c_int32)]
+
+
+class _KVBatch(C.Structure):
+    _fields_ = [("q_start", C.c_void_p), ("kv_len", C.c_void_p), ("page_table", C.c_void_p), ("slot", C.c_void_p),
+                ("n_seq", C.c_int32), ("max_pages", C.c_int32), ("rows", C.c_int64), ("max_new", C.c_int32)]
 
 
 _lib = None
@@ -95,6 +108,12 @@ def lib() -> C.CDLL:
         L.glowq_w8a8_workspace_bytes.restype = C.c_size_t
         L.glowq_group_forward_w8a8.argtypes = [C.POINTER(_Int8Module), i32, i64, p, i32, p, i64, p, p, C.c_size_t, p]
         L.glowq_solo_forward_w8a8.argtypes = [C.POINTER(_Int8Module), i64, p, i32, p, i64, p, C.c_size_t, p]
+        kc, kb = C.POINTER(_KVCache), C.POINTER(_KVBatch)
+        L.glowq_kv_append.argtypes = [kc, kb, p, i64, i32, p, i64, p, i64, p, i64, p, i64, p]
+        L.glowq_kv_read.argtypes = [kc, kb, p, i64, p, p, p]
+        L.glowq_kv_attention_workspace_bytes.argtypes = [kc, kb, i32]
+        L.glowq_kv_attention_workspace_bytes.restype = C.c_size_t
+        L.glowq_kv_attention.argtypes = [kc, kb, p, i64, i32, C.c_float, p, i64, p, C.c_size_t, p]
         L.glowq_solve_workspace_bytes.argtypes = [i64, i64, i32, i32]
         L.glowq_solve_workspace_bytes.restype = C.c_size_t
         L.glowq_group_solve.argtypes = [C.POINTER(_SolveModule), i32, i64, p, p, i32, i32, i32, p, p, p, p, p, p, p,
@@ -111,7 +130,8 @@ def lib() -> C.CDLL:
                   "glowq_select_restore", "glowq_select_restore_scores", "glowq_error_norms", "glowq_group_solve",
                   "glowq_quantize_act_e4m3", "glowq_group_forward_w4a8", "glowq_solo_forward_w4a8",
                   "glowq_pack_int8", "glowq_dequant_int8", "glowq_quantize_act_int8", "glowq_group_forward_w8a8",
-                  "glowq_solo_forward_w8a8", "glowq_get_device_status",
+                  "glowq_solo_forward_w8a8", "glowq_kv_append", "glowq_kv_read", "glowq_kv_attention",
+                  "glowq_get_device_status",
                   "glowq_selftest_wait_timeout"):
             getattr(L, f).restype = st
         _lib = L
@@ -715,6 +735,188 @@ def group_forward_w8a8(mods: Sequence[Int8Module], B, X, Ys=None, R_out=None, wo
 def solo_forward_w8a8(mod: Int8Module, B, X, Y=None, workspace=None, stream=None):
     with _on(stream):
         return Int8ForwardPlan([mod], B, X, None if Y is None else [Y], None, workspace, solo=True)(stream)[0]
+
+
+# ------------------------------------------------------- key/value cache ----
+
+class KVCache:
+    """A paged 8-bit key/value cache: complete pages of 64 tokens in int8 with
+    one scale per page and kv head (k_codes [pages, kv_heads, D/64, 64, 64],
+    v_codes [pages, kv_heads, D, 64], k_scales, v_scales float32 [pages,
+    kv_heads]), each sequence's incomplete last page in fp16 (k_tail, v_tail
+    [slots, kv_heads, 64, D]).  `alloc` makes one."""
+
+    def __init__(self, k_codes, v_codes, k_scales, v_scales, k_tail, v_tail):
+        import torch
+        dev = k_codes.device
+        _require(k_codes, "k_codes", torch.int8, dim=5)
+        P, H, panels, page, w = k_codes.shape
+        D = panels * 64
+        _require(v_codes, "v_codes", torch.int8, dev, 4)
+        _require(k_scales, "k_scales", torch.float32, dev, 2)
+        _require(v_scales, "v_scales", torch.float32, dev, 2)
+        _require(k_tail, "k_tail", torch.float16, dev, 4)
+        _require(v_tail, "v_tail", torch.float16, dev, 4)
+        S = k_tail.shape[0]
+        if (page, w) != (KV_PAGE, 64) or tuple(v_codes.shape) != (P, H, D, KV_PAGE):
+            raise ValueError("codes must be [pages, kv_heads, D/64, 64, 64] and [pages, kv_heads, D, 64]")
+        if tuple(k_scales.shape) != (P, H) or tuple(v_scales.shape) != (P, H):
+            raise ValueError("scales must be [pages, kv_heads]")
+        if tuple(k_tail.shape) != (S, H, KV_PAGE, D) or tuple(v_tail.shape) != (S, H, KV_PAGE, D):
+            raise ValueError("tails must be [slots, kv_heads, 64, D]")
+        self.k_codes, self.v_codes, self.k_scales, self.v_scales = k_codes, v_codes, k_scales, v_scales
+        self.k_tail, self.v_tail = k_tail, v_tail
+        self.pages, self.slots, self.kv_heads, self.head_dim, self.device = P, S, H, D, dev
+        self._c = _KVCache(_ptr(k_codes), _ptr(v_codes), _ptr(k_scales), _ptr(v_scales), _ptr(k_tail), _ptr(v_tail),
+                           P, S, H, D)
+
+    @classmethod
+    def alloc(cls, pages: int, slots: int, kv_heads: int, head_dim: int, device="cuda"):
+        import torch
+        if head_dim not in (64, 128):
+            raise ValueError("head_dim must be 64 or 128")
+        e = lambda *s, t: torch.empty(*s, dtype=t, device=device)
+        return cls(e(pages, kv_heads, head_dim // 64, KV_PAGE, 64, t=torch.int8),
+                   e(pages, kv_heads, head_dim, KV_PAGE, t=torch.int8), e(pages, kv_heads, t=torch.float32),
+                   e(pages, kv_heads, t=torch.float32), e(slots, kv_heads, KV_PAGE, head_dim, t=torch.float16),
+                   e(slots, kv_heads, KV_PAGE, head_dim, t=torch.float16))
+
+
+class KVBatch:
+    """One step's sequences (device int32): rows q_start[b] .. q_start[b+1] - 1
+    of the step's arrays are sequence b's new tokens, kv_len[b] its tokens with
+    them, page_table[b] its pages, slot[b] its tail; `rows` rows in all (the
+    rest is padding), no sequence with more than `max_new` new tokens."""
+
+    def __init__(self, q_start, kv_len, page_table, slot, rows: int, max_new: int):
+        import torch
+        dev = q_start.device
+        _require(q_start, "q_start", torch.int32, dim=1)
+        _require(kv_len, "kv_len", torch.int32, dev, 1)
+        _require(page_table, "page_table", torch.int32, dev, 2)
+        _require(slot, "slot", torch.int32, dev, 1)
+        n = int(kv_len.shape[0])
+        if q_start.shape[0] != n + 1 or page_table.shape[0] != n or slot.shape[0] != n:
+            raise ValueError("q_start has one more value than kv_len; page_table and slot one row per sequence")
+        self.n_seq, self.rows, self.max_new, self.device = n, int(rows), int(max_new), dev
+        self._keep = (q_start, kv_len, page_table, slot)
+        self._c = _KVBatch(_ptr(q_start), _ptr(kv_len), _ptr(page_table), _ptr(slot), n, int(page_table.shape[1]),
+                           int(rows), int(max_new))
+
+
+def _heads(t, name: str, rows: int, width: int, device):
+    """A rows x width fp16 array whose rows may lie apart (a column slice); its pitch."""
+    import torch
+    _require(t, name, torch.float16, device, 2, contiguous=False)
+    if t.shape[0] < rows or t.shape[1] != width or (t.stride(1) != 1 and width > 1):
+        raise ValueError(f"{name} must be {rows} x {width} with unit column stride")
+    return t.stride(0) if t.shape[0] > 1 else max(t.stride(0), width)
+
+
+class KVAppendPlan(_Call):
+    """kv_append with its arguments marshalled once; calling it returns Q_out."""
+
+    def __init__(self, cache: KVCache, batch: KVBatch, K, V, Q=None, Q_out=None, rope=None):
+        import torch
+        dev, D, n = cache.device, cache.head_dim, batch.rows
+        if batch.device != dev:
+            raise ValueError("cache and batch are on different devices")
+        ldK = _heads(K, "K", n, cache.kv_heads * D, dev)
+        ldV = _heads(V, "V", n, cache.kv_heads * D, dev)
+        ldQ = ldO = hq = 0
+        if Q is not None:
+            hq = int(Q.shape[1]) // D
+            ldQ = _heads(Q, "Q", n, hq * D, dev)
+            if Q_out is None:
+                Q_out = torch.empty((Q.shape[0], hq * D), dtype=torch.float16, device=dev)
+            ldO = _heads(Q_out, "Q_out", n, hq * D, dev)
+        if rope is not None:
+            _require(rope, "rope", torch.float32, dev, 2)
+            if rope.shape[1] != D:
+                raise ValueError("rope must be positions x D: cosines of the D/2 pairs, then sines")
+        args = (C.byref(cache._c), C.byref(batch._c), _ptr(Q), ldQ, hq, _ptr(K), ldK, _ptr(V), ldV, _ptr(rope),
+                0 if rope is None else int(rope.shape[0]), _ptr(Q_out), ldO)
+        super().__init__("glowq_kv_append", dev, args, Q_out, (cache, batch, K, V, Q, rope))
+
+
+def kv_append(cache: KVCache, batch: KVBatch, K, V, Q=None, Q_out=None, rope=None, stream=None):
+    """Append the step's keys and values (rows x kv_heads D fp16, e.g. column
+    slices of a Q/K/V group's output) to the cache, rotated by position with
+    `rope` (positions x D float32: cosines of the D/2 pairs, then sines).  Q,
+    if given, is rotated into Q_out (returned; Q_out=Q works in place)."""
+    with _on(stream):
+        return KVAppendPlan(cache, batch, K, V, Q, Q_out, rope)(stream)
+
+
+class KVReadPlan(_Call):
+    """kv_read with its arguments marshalled once; calling it returns (K, V)."""
+
+    def __init__(self, cache: KVCache, batch: KVBatch, count: int, first=None, K=None, V=None):
+        import torch
+        dev, width = cache.device, cache.kv_heads * cache.head_dim
+        if batch.device != dev:
+            raise ValueError("cache and batch are on different devices")
+        if first is not None:
+            _require(first, "first", torch.int32, dev, 1)
+            if first.shape[0] != batch.n_seq:
+                raise ValueError("first must have one value per sequence")
+        shape = (batch.n_seq, int(count), width)
+        out = []
+        for t, name in ((K, "K"), (V, "V")):
+            if t is None:
+                t = torch.empty(shape, dtype=torch.float16, device=dev)
+            _require(t, name, torch.float16, dev, 3)
+            if tuple(t.shape) != shape:
+                raise ValueError(f"{name} must be n_seq x count x kv_heads D")
+            out.append(t)
+        args = (C.byref(cache._c), C.byref(batch._c), _ptr(first), int(count), _ptr(out[0]), _ptr(out[1]))
+        super().__init__("glowq_kv_read", dev, args, tuple(out), (cache, batch, first))
+
+
+def kv_read(cache: KVCache, batch: KVBatch, count: int, first=None, K=None, V=None, stream=None):
+    """What the cache holds at positions first[b] .. first[b] + count - 1 of every
+    sequence: (K, V) fp16 [n_seq, count, kv_heads D], zero from kv_len on."""
+    with _on(stream):
+        return KVReadPlan(cache, batch, count, first, K, V)(stream)
+
+
+def kv_attention_workspace(cache: KVCache, batch: KVBatch, q_heads: int):
+    """Zero-filled (the tickets at its start must begin at zero; every call leaves them so)."""
+    import torch
+    n = int(lib().glowq_kv_attention_workspace_bytes(C.byref(cache._c), C.byref(batch._c), int(q_heads)))
+    return torch.zeros(max(n, 16), dtype=torch.uint8, device=cache.device)
+
+
+class KVAttentionPlan(_Call):
+    """kv_attention with its arguments marshalled once; calling it returns Y.  A
+    workspace made here is zeroed on the stream that is current at that moment:
+    calls on another stream have to be ordered behind it."""
+
+    def __init__(self, cache: KVCache, batch: KVBatch, Q, scale: Optional[float] = None, Y=None, workspace=None):
+        import torch
+        dev, D = cache.device, cache.head_dim
+        if batch.device != dev:
+            raise ValueError("cache and batch are on different devices")
+        hq = int(Q.shape[1]) // D if Q.dim() == 2 else 0
+        ldQ = _heads(Q, "Q", batch.rows, hq * D, dev)
+        if Y is None:
+            Y = torch.empty((Q.shape[0], hq * D), dtype=torch.float16, device=dev)
+        ldY = _heads(Y, "Y", batch.rows, hq * D, dev)
+        if workspace is None:
+            workspace = kv_attention_workspace(cache, batch, hq)
+        _require(workspace, "workspace", torch.uint8, dev)
+        args = (C.byref(cache._c), C.byref(batch._c), _ptr(Q), ldQ, hq, D ** -0.5 if scale is None else float(scale),
+                _ptr(Y), ldY, _ptr(workspace), workspace.numel())
+        super().__init__("glowq_kv_attention", dev, args, Y, (cache, batch, Q, workspace))
+
+
+def kv_attention(cache: KVCache, batch: KVBatch, Q, scale: Optional[float] = None, Y=None, workspace=None,
+                 stream=None):
+    """Causal attention of the step's queries (rows x q_heads D fp16) over the
+    cache, after the step's append; scale defaults to D^-1/2.  Returns Y (rows x
+    q_heads D fp16), the input of o_proj."""
+    with _on(stream):
+        return KVAttentionPlan(cache, batch, Q, scale, Y, workspace)(stream)
 
 
 # ---------------------------------------------------------- offline solve ----

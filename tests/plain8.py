@@ -49,3 +49,89 @@ def within(got, ref, bound):
     assert np.array_equal(np.isnan(got), np.isnan(ref))
     ok = ~np.isnan(ref)
     return float(np.max(np.abs(got - ref)[ok] / bound[ok], initial=0.0))
+
+
+# ------------------------------------------------------- key/value cache ----
+
+PAGE = 64
+
+
+def rope_table(positions, D, theta=10000.0):
+    """Cosines of the D/2 pairs, then sines, by position (fp32)."""
+    inv = theta ** (-np.arange(0, D, 2) / D)
+    ang = np.arange(positions)[:, None] * inv
+    return np.concatenate([np.cos(ang), np.sin(ang)], 1).astype(np.float32)
+
+
+def rotate(x, cs):
+    """x (n x heads x D fp16), cs (n x D fp32): two fp32 products and a sum, unfused, rounded to fp16 -- the
+    operator's definition, so stored values can be compared bit by bit."""
+    half = x.shape[-1] // 2
+    a, b = x[..., :half].astype(np.float32), x[..., half:].astype(np.float32)
+    c, s = cs[:, None, :half], cs[:, None, half:]
+    with np.errstate(over="ignore", invalid="ignore"):
+        return np.concatenate([(a * c - b * s).astype(np.float16), (b * c + a * s).astype(np.float16)], -1)
+
+
+def quantize_page(x):
+    """One page and head (64 x D fp16) -> (codes, scale)."""
+    x = x.astype(np.float32)
+    if not np.isfinite(x).all():
+        return np.zeros(x.shape, np.int8), np.float32(np.nan)
+    s = np.float32(max(np.abs(x).max(), np.float32(2.0 ** -24))) / np.float32(127)
+    return np.clip(np.rint(x / s), -127, 127).astype(np.int8), s
+
+
+class Sequence:
+    """The keys and values of one sequence as the cache defines them: fp16 (keys rotated), whole pages quantised."""
+
+    def __init__(self, H, D):
+        self.k, self.v = np.zeros((0, H, D), np.float16), np.zeros((0, H, D), np.float16)
+
+    def append(self, k, v):
+        self.k, self.v = np.concatenate([self.k, k]), np.concatenate([self.v, v])
+
+    def held(self):
+        """(keys, values) in 64 bits, len x H x D."""
+        out = []
+        for x in (self.k, self.v):
+            y = x.astype(np.float64)
+            for p in range(len(x) // PAGE):
+                for h in range(x.shape[1]):
+                    q, s = quantize_page(x[p * PAGE:(p + 1) * PAGE, h])
+                    y[p * PAGE:(p + 1) * PAGE, h] = q.astype(np.float64) * np.float64(s)
+            out.append(y)
+        return out
+
+
+def attention(Q, k, v, start, scale):
+    """Q (n x Hq x D fp16) at positions start .. over k, v (len x H x D, 64 bits).  Returns (Y, bound)."""
+    n, Hq, D = Q.shape
+    L, H = k.shape[:2]
+    G = Hq // H
+    Y, bound = np.zeros((n, Hq, D)), np.full((n, Hq, D), 2.0 ** -25)
+    u16, u32 = 2.0 ** -11, 2.0 ** -23
+    for i in range(n):
+        m = min(L, start + i + 1)
+        if m <= 0:
+            continue
+        for h in range(Hq):
+            with np.errstate(over="ignore", invalid="ignore"):
+                q, kk, vv = Q[i, h].astype(np.float64), k[:m, h // G], v[:m, h // G]
+                s = kk @ q * scale
+                w = np.exp(s - s.max())
+                p = w / w.sum()
+                y = p @ vv
+                # fp32 scores: D products summed, the scales and log2 e applied, in a range of |s| and of the maximum's
+                ds = (D + 6) * u32 * (np.abs(kk) @ np.abs(q)) * scale + 4 * u32 * (np.abs(s) + abs(s.max()))
+                # weights: that error in the exponent, exp2's own (2^-22), fp16 rounding; below fp16's normals an absolute 2^-33
+                dw = 2 * ds + 2.0 ** -22 + u16
+                # sums over m terms in fp32: each weight and product, and the rescalings of one per page
+                acc = (m + 8) * u32
+                spread = p @ (np.abs(vv) * (dw[:, None] + acc)) + np.abs(y) * (p @ (dw - u16) + acc)
+                # a weight below fp16's normals is off by 2^-33 of the largest weighted value's unit, and values
+                # are at most 128 units of their page (64 .. 128 in a tail)
+                spread += 2.0 ** -33 * 2 * m * np.abs(vv).max(initial=0.0) / w.sum()
+            Y[i, h] = y
+            bound[i, h] += spread + u16 * (np.abs(y) + spread)
+    return Y, bound
