@@ -169,30 +169,40 @@ static glowq_status fp4_views(glowq_format fmt, const glowq_fp4_module* mods, in
 
 // W8A8 workspace: [zero region: tickets][codes][token scales][solo R][R partials][k-split sums]
 struct W8A8Layout {
-    size_t codes, scales, R, partial, slots, total;
+    bool small;          // the weight-streaming product, else the tensor-core GEMM
     Int8GemvPlan gemv;
-    int64_t chunk;       // tokens per pass
+    I8GemmPlan gemm;
+    size_t codes, scales, R, partial, slots, total;
 };
-static W8A8Layout w8a8_layout(int64_t T, int64_t d, int32_t r, int64_t tiles) {
+static W8A8Layout w8a8_layout(int64_t T, int64_t d, int32_t r, const int64_t* outs, int32_t m) {
     W8A8Layout L;
-    L.chunk = T < kInt8SmallTokens ? T : kInt8SmallTokens;
-    const int64_t tok = int8_small_tokens(L.chunk);
-    L.gemv = plan_int8_gemv(L.chunk, d, tiles, r, device_sm_count());
+    int64_t tiles = 0, mtiles = 0;
+    for (int i = 0; i < m; ++i) {
+        tiles += outs[i] / 16;
+        mtiles += (outs[i] + 255) / 256;
+    }
+    L.small = false;
+    int64_t rows = T;
+    if (T <= kInt8SmallTokens) {
+        L.gemv = plan_int8_gemv(T, d, tiles, r, device_sm_count());
+        L.small = L.gemv.ok;
+        if (L.small) rows = int8_small_tokens(T);
+    }
+    if (!L.small) L.gemm = plan_int8_gemm(T, d, mtiles, r, device_sm_count());
     L.codes = kInt8ZeroBytes;
-    L.scales = L.codes + align_up((size_t)tok * d, 256);
-    L.R = L.scales + align_up((size_t)tok * 4, 256);
+    L.scales = L.codes + align_up((size_t)rows * d, 256);
+    L.R = L.scales + align_up((size_t)rows * 4, 256);
     L.partial = L.R + align_up((size_t)T * r * 2, 256);
-    L.slots = L.partial;
-    L.total = L.slots + L.gemv.slot_bytes;
+    L.slots = L.partial + (L.small || r == 0 ? 0 : align_up(prefill_partial_bytes(T, r), 256));
+    L.total = L.slots + (L.small ? L.gemv.slot_bytes : L.gemm.slot_bytes);
     return L;
 }
 
 // Validation of 8-bit integer modules and their conversion to module views.
 static glowq_status int8_views(const glowq_int8_module* mods, int32_t m, int64_t d, const uint16_t* B, int32_t r,
-                               const uint16_t* X, int64_t T, Int8ModuleView* hm, int64_t* tiles) {
+                               const uint16_t* X, int64_t T, Int8ModuleView* hm, int64_t* outs) {
     if (!mods || m < 1 || m > GLOWQ_MAX_MODULES) return GLOWQ_ERR_ARG;
     glowq_module tmp[GLOWQ_MAX_MODULES];
-    *tiles = 0;
     for (int i = 0; i < m; ++i) {
         const glowq_int8_module& f = mods[i];
         if (!f.scales) return GLOWQ_ERR_ARG;
@@ -207,7 +217,7 @@ static glowq_status int8_views(const glowq_int8_module* mods, int32_t m, int64_t
     for (int i = 0; i < m; ++i) {
         hm[i] = {mods[i].codes, mods[i].scales, (r > 0) ? mods[i].A : nullptr, mods[i].Y, mods[i].ldY,
                  mods[i].out_features};
-        *tiles += mods[i].out_features / 16;
+        outs[i] = mods[i].out_features;
     }
     return GLOWQ_OK;
 }
@@ -216,34 +226,36 @@ static glowq_status w8a8_impl(const glowq_int8_module* mods, int32_t m, int64_t 
                               const uint16_t* X, int64_t T, uint16_t* R_out, void* workspace, size_t workspace_bytes,
                               cudaStream_t st, bool solo) {
     Int8ModuleView hm[GLOWQ_MAX_MODULES];
-    int64_t tiles = 0;
-    glowq_status v = int8_views(mods, m, d, B, r, X, T, hm, &tiles);
+    int64_t outs[GLOWQ_MAX_MODULES];
+    glowq_status v = int8_views(mods, m, d, B, r, X, T, hm, outs);
     if (v != GLOWQ_OK) return v;
     if (T == 0) return GLOWQ_OK;
     if (!solo && r > 0) {
         if (!R_out) return GLOWQ_ERR_ARG;
         if (!aligned16(R_out)) return GLOWQ_ERR_ALIGN;
     }
-    const W8A8Layout L = w8a8_layout(T, d, r, tiles);
+    const W8A8Layout L = w8a8_layout(T, d, r, outs, m);
     if (!workspace || workspace_bytes < L.total) return GLOWQ_ERR_ARG;
     if (!aligned16(workspace)) return GLOWQ_ERR_ALIGN;
-    if (!L.gemv.ok) return GLOWQ_ERR_UNSUPPORTED;
     char* ws = static_cast<char*>(workspace);
+    unsigned int* tickets = reinterpret_cast<unsigned int*>(ws);
+    int8_t* codes = reinterpret_cast<int8_t*>(ws + L.codes);
+    float* scales = reinterpret_cast<float*>(ws + L.scales);
     uint16_t* R = solo ? reinterpret_cast<uint16_t*>(ws + L.R) : R_out;
-    for (int64_t t0 = 0; t0 < T; t0 += L.chunk) {
-        const int64_t n = T - t0 < L.chunk ? T - t0 : L.chunk;
-        const Int8GemvPlan p = plan_int8_gemv(L.chunk, d, tiles, r, device_sm_count());
-        Int8ModuleView cm[GLOWQ_MAX_MODULES];
-        for (int i = 0; i < m; ++i) {
-            cm[i] = hm[i];
-            cm[i].Y += t0 * hm[i].ldY;
-        }
-        if (launch_int8_small(cm, m, (int)d, (int)n, (int)L.chunk, r, X + t0 * d, B, R ? R + t0 * r : nullptr,
-                              reinterpret_cast<int8_t*>(ws + L.codes), reinterpret_cast<float*>(ws + L.scales),
-                              reinterpret_cast<unsigned int*>(ws), reinterpret_cast<int*>(ws + L.slots), p, st) != cudaSuccess)
-            return GLOWQ_ERR_CUDA;
+    cudaError_t e;
+    if (L.small) {
+        e = launch_int8_small(hm, m, (int)d, (int)T, r, X, B, R, codes, scales, tickets,
+                              reinterpret_cast<int*>(ws + L.slots), L.gemv, st);
+    } else {
+        if (!encode_fn()) return GLOWQ_ERR_CUDA;
+        e = r > 0 ? launch_rproj_prefill(X, B, T, (int)d, r, R, reinterpret_cast<float*>(ws + L.partial),
+                                         device_sm_count(), st, nullptr, nullptr)
+                  : cudaSuccess;
+        if (e == cudaSuccess) e = launch_quantize_act_int8(X, T, d, codes, scales, st, r > 0);
+        if (e == cudaSuccess)
+            e = launch_int8_gemm(hm, m, (int)d, T, r, codes, scales, R, tickets, ws + L.slots, L.gemm, device_sm_count(), st);
     }
-    return GLOWQ_OK;
+    return e == cudaSuccess ? GLOWQ_OK : GLOWQ_ERR_CUDA;
 }
 
 // Checks of a cache and a batch, and their device views.
@@ -608,12 +620,9 @@ size_t glowq_w8a8_workspace_bytes(int64_t T, int64_t d, int32_t r, const int64_t
     if (T <= 0 || T > ((int64_t)1 << 30) || d <= 0 || d % GLOWQ_GROUP_SIZE != 0 || d > kInt8MaxD || r < 0 ||
         r > GLOWQ_MAX_RANK || r % 8 != 0 || !out_features || m < 1 || m > GLOWQ_MAX_MODULES)
         return 0;
-    int64_t tiles = 0;
-    for (int i = 0; i < m; ++i) {
+    for (int i = 0; i < m; ++i)
         if (out_features[i] <= 0 || out_features[i] % 16 != 0 || out_features[i] > ((int64_t)1 << 30)) return 0;
-        tiles += out_features[i] / 16;
-    }
-    return w8a8_layout(T, d, r, tiles).total;
+    return w8a8_layout(T, d, r, out_features, m).total;
 }
 
 glowq_status glowq_group_forward_w8a8(const glowq_int8_module* mods, int32_t m, int64_t d, const uint16_t* B,

@@ -135,15 +135,19 @@ __device__ __forceinline__ void quantize_token(const uint16_t* __restrict__ X, i
     for (int i = threadIdx.x + kKeep * kQuantThreads; i < n8; i += kQuantThreads) code(i, ldcg_128(x + i));
 }
 
-// One token per block, codes row-major [T][d].
+// One token per block, codes row-major [T][d].  BESIDE: launched behind kernels
+// of the same call that have already waited for X (the projection R), so it
+// runs beside them and waits for their end at its own.
+template <bool BESIDE>
 __global__ void __launch_bounds__(kQuantThreads) quantize_act_int8_kernel(const uint16_t* __restrict__ X, int64_t d,
                                                                           int8_t* __restrict__ codes,
                                                                           float* __restrict__ scales) {
-    pdl_wait();
+    if (!BESIDE) pdl_wait();
     pdl_launch_dependents();
     const int64_t t = blockIdx.x;
     uint2* out = reinterpret_cast<uint2*>(codes + t * d);
     quantize_token(X, t, d, scales, [&](int i, uint2 q) { out[i] = q; });
+    if (BESIDE) pdl_wait();
 }
 
 // ---------------------------------------------------------------------------
@@ -519,9 +523,10 @@ cudaError_t launch_pdl(const void* fn, unsigned grid, unsigned block, size_t sme
     return cudaLaunchKernelExC(&cfg, fn, args);
 }
 cudaError_t launch_quantize_act_int8(const uint16_t* X, int64_t T, int64_t d, int8_t* codes, float* scales,
-                                     cudaStream_t st) {
+                                     cudaStream_t st, bool beside) {
     void* args[] = {(void*)&X, (void*)&d, (void*)&codes, (void*)&scales};
-    return launch_pdl((const void*)quantize_act_int8_kernel, (unsigned)T, kQuantThreads, 0, st, args);
+    return launch_pdl(beside ? (const void*)quantize_act_int8_kernel<true> : (const void*)quantize_act_int8_kernel<false>,
+                      (unsigned)T, kQuantThreads, 0, st, args);
 }
 
 // Token width (a multiple of 8) of the small-T kernels.
@@ -558,10 +563,10 @@ static cudaError_t launch_int8_gemv_t(const Int8GemvArgs& a, const Int8GemvPlan&
     return launch_pdl((const void*)int8_gemv_kernel<NT>, (unsigned)p.grid, kGemvWarps * 32, (size_t)p.smem, st, args);
 }
 
-cudaError_t launch_int8_small(const Int8ModuleView* mods, int m, int d, int T, int width, int r, const uint16_t* X,
+cudaError_t launch_int8_small(const Int8ModuleView* mods, int m, int d, int T, int r, const uint16_t* X,
                               const uint16_t* B, uint16_t* R, int8_t* xq, float* xs, unsigned int* tickets, int* slots,
                               const Int8GemvPlan& p, cudaStream_t st) {
-    const int tok = int8_small_tokens(width);    // the width that the plan and the workspace are made for
+    const int tok = int8_small_tokens(T);
     Int8PrepArgs pa = {X, B, xq, xs, reinterpret_cast<__half*>(R), d, T, tok, r};
     void* pargs[] = {(void*)&pa};
     const unsigned rblocks = r > 0 ? (unsigned)(r / kPrepRows * ((T + kPrepTokens - 1) / kPrepTokens)) : 0u;

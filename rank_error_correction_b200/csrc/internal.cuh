@@ -103,10 +103,24 @@ cudaError_t launch_pack_int8(const float* W, int64_t O, int64_t d, int8_t* codes
 cudaError_t launch_dequant_int8(const int8_t* codes, const float* scales, int64_t O, int64_t d, uint16_t* out,
                                 cudaStream_t st);
 cudaError_t launch_quantize_act_int8(const uint16_t* X, int64_t T, int64_t d, int8_t* codes, float* scales,
-                                     cudaStream_t st);
-cudaError_t launch_int8_small(const Int8ModuleView* mods, int m, int d, int T, int width, int r, const uint16_t* X,
+                                     cudaStream_t st, bool beside = false);
+cudaError_t launch_int8_small(const Int8ModuleView* mods, int m, int d, int T, int r, const uint16_t* X,
                               const uint16_t* B, uint16_t* R, int8_t* xq, float* xs, unsigned int* tickets, int* slots,
                               const Int8GemvPlan& p, cudaStream_t st);
+// int8_gemm.cu: larger T on the tensor cores
+struct I8GemmPlan {
+    int bn, S, kbs;      // tokens per pair tile, parts per tile, k-blocks per part
+    int64_t tiles;
+    size_t slot_bytes;   // partial sums (S > 1)
+};
+I8GemmPlan plan_int8_gemm(int64_t T, int64_t d, int64_t mtiles, int r, int num_sms);
+cudaError_t launch_int8_gemm(const Int8ModuleView* mods, int m, int d, int64_t T, int r, const int8_t* xq,
+                             const float* xs, const uint16_t* R, unsigned int* tickets, void* slots,
+                             const I8GemmPlan& p, int num_sms, cudaStream_t st);
+// prefill.cu: R = X B^T on the tensor cores (scratch of prefill_partial_bytes(T, r))
+cudaError_t launch_rproj_prefill(const uint16_t* X, const uint16_t* B, int64_t T, int d, int r, uint16_t* R,
+                                 float* partial, int num_sms, cudaStream_t st, const float* tok_scale,
+                                 uint16_t* R_scaled);
 // solve.cu: the offline group solve (float64)
 struct SolveModule {
     const float* W;      // O x d fp32 weights
