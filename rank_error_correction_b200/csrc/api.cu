@@ -188,7 +188,7 @@ static W8A8Layout w8a8_layout(int64_t T, int64_t d, int32_t r, const int64_t* ou
         L.small = L.gemv.ok;
         if (L.small) rows = int8_small_tokens(T);
     }
-    if (!L.small) L.gemm = plan_int8_gemm(T, d, mtiles, r, device_sm_count());
+    if (!L.small) L.gemm = plan_int8_gemm(T, d, mtiles, device_sm_count());
     L.codes = kInt8ZeroBytes;
     L.scales = L.codes + align_up((size_t)rows * d, 256);
     L.R = L.scales + align_up((size_t)rows * 4, 256);
@@ -253,7 +253,7 @@ static glowq_status w8a8_impl(const glowq_int8_module* mods, int32_t m, int64_t 
                   : cudaSuccess;
         if (e == cudaSuccess) e = launch_quantize_act_int8(X, T, d, codes, scales, st, r > 0);
         if (e == cudaSuccess)
-            e = launch_int8_gemm(hm, m, (int)d, T, r, codes, scales, R, tickets, ws + L.slots, L.gemm, device_sm_count(), st);
+            e = launch_int8_gemm(hm, m, (int)d, T, r, codes, scales, R, reinterpret_cast<int*>(ws + L.slots), L.gemm, st);
     }
     return e == cudaSuccess ? GLOWQ_OK : GLOWQ_ERR_CUDA;
 }

@@ -530,7 +530,7 @@ cudaError_t launch_quantize_act_int8(const uint16_t* X, int64_t T, int64_t d, in
 }
 
 // Token width (a multiple of 8) of the small-T kernels.
-int int8_small_tokens(int64_t T) { return T <= 8 ? 8 : T <= 16 ? 16 : T <= 32 ? 32 : 64; }
+int int8_small_tokens(int64_t T) { return T <= 8 ? 8 : 16; }
 
 // Decomposition of the small-T product.
 Int8GemvPlan plan_int8_gemv(int64_t T, int64_t d, int64_t tiles, int r, int num_sms) {
@@ -594,9 +594,7 @@ cudaError_t launch_int8_small(const Int8ModuleView* mods, int m, int d, int T, i
     a.status = device_status_ptr();
     switch (tok) {
         case 8: return launch_int8_gemv_t<1>(a, p, st);
-        case 16: return launch_int8_gemv_t<2>(a, p, st);
-        case 32: return launch_int8_gemv_t<4>(a, p, st);
-        default: return launch_int8_gemv_t<8>(a, p, st);
+        default: return launch_int8_gemv_t<2>(a, p, st);
     }
 }
 

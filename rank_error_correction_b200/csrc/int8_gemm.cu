@@ -1,4 +1,4 @@
-// int8_gemm.cu -- W8A8 for larger T on the 5th-generation tensor cores:
+// int8_gemm.cu -- W8A8 for T > 16 on the 5th-generation tensor cores:
 // tcgen05.mma kind::i8 on CTA pairs, int32 accumulators in TMEM.
 //
 //   y[t][o] = s_t s_o sum_k c[t][k] q[o][k] + sum_j R[t][j] A[o][j]
@@ -6,15 +6,22 @@
 // A cluster of two CTAs computes 256 rows of W x BN tokens: CTA p stages rows
 // [128 p, +128) of the codes and half of the tokens' codes (128-byte rows, one
 // swizzle atom, by TMA), the leader's MMA thread issues M = 256, N = BN, K = 32
-// per step, and each CTA's TMEM receives the int32 sums of its 128 rows.  The
-// correction is K = 64 slabs of fp16 (A_i and R by TMA, zero beyond r) into
-// fp32 columns of their own beside the sums, because one accumulator cannot
-// hold both; the epilogue joins them in fp32 and rounds once.  Both are double
-// buffered, so a tile's drain overlaps the next tile's products.
-// When the tiles alone would not occupy every pair, the k of each tile is
-// split into parts: every part stores its sums, and the part that counts last
-// on the tile's ticket adds them (integers: the order does not matter).
+// per step, and each CTA's TMEM receives the int32 sums of its 128 rows, double
+// buffered so that a tile's drain overlaps the next tile's products.  A k-block
+// of 128 (four steps) takes 565-610 clocks for every BN from 64 to 256 (the
+// rows of W set the pace), so BN is the widest that T fills.
+//
+// Whole tiles: the epilogue turns the sums into s_t s_o sum in fp32 in place,
+// the correction's K = 64 slabs of fp16 (A_i and R by TMA, zero beyond r) are
+// added to them by the tensor core in the middle of the next tile's products,
+// and the epilogue stores y, rounded once.
+// Split tiles: what does not make a full round of tiles for every pair (all of
+// it when T is small) is one run of k-blocks cut evenly among the pairs, so
+// that each streams the same share of W; every segment of a tile stores its
+// sums, and int8_join_kernel adds a tile's segments (integers: exact in any
+// order), the correction by warp MMA, and stores y.
 #include <cstring>
+#include <type_traits>
 
 #include "internal.cuh"
 #include "tc.cuh"
@@ -28,17 +35,18 @@ constexpr int kI8Threads = 256;          // producer, MMA, forwarder, (idle), 4 
 constexpr int kI8Chunk = 32;             // tokens per epilogue step
 constexpr int kI8EpiBytes = kI8Chunk * kI8Rows * 2;
 constexpr int kI8SmemMax = 227 * 1024;
+constexpr int kI8MaxStages = 9;
 
 template <int BN>
 struct I8Tile {
     static constexpr int kHalf = BN / 2;
     static constexpr int kXBytes = kHalf * kI8Block;
     static constexpr int kStageBytes = kI8WBytes + kXBytes;
-    static constexpr int kStages = BN == 256 ? 6 : BN == 128 ? 8 : 9;
-    static constexpr int kCols = 4 * BN <= 512 ? 4 * BN : 512;   // two int32 and two fp32 accumulators
+    static constexpr int kStages = BN == 256 ? 6 : BN == 192 ? 7 : BN == 128 ? 8 : 9;
+    static constexpr int kCols = BN == 64 ? 128 : BN == 128 ? 256 : 512;   // two accumulators, a power of two
     static constexpr int kSmem = kStages * kStageBytes + 2 * kI8EpiBytes + 2 * BN * 4 + 512 + 1024;
-    static_assert(BN % 64 == 0 && 4 * BN <= 512, "two accumulators of each kind in TMEM");
-    static_assert(kSmem <= kI8SmemMax, "shared memory per CTA");
+    static_assert(BN % 64 == 0 && BN <= 256, "MMA N and TMEM columns");
+    static_assert(kStages <= kI8MaxStages && kSmem <= kI8SmemMax, "shared memory per CTA");
 };
 
 struct I8GemmModule {
@@ -56,21 +64,21 @@ struct I8GemmArgs {
     I8GemmModule mod[GLOWQ_MAX_MODULES];
     const float* xs;
     int m, d, T, r;
-    int ntiles_n, nunits;
-    int S, kbs;                            // parts per tile, k-blocks per part
-    int4* slots;                           // [tile][2 CTAs][S sums (+ 1 correction)][BN / 4][128 rows]
-    unsigned int* tickets;                 // [tile][2 CTAs], zero between calls
+    int ntiles_n;
+    I8Split split;
+    int* slots;                            // [pair][segment][2 CTAs][BN tokens][128 rows]
     unsigned int* status;
 };
 
 struct __align__(8) I8Barriers {
-    uint64_t full[9];          // per CTA: its TMA bytes landed
-    uint64_t ready[9];         // leader: both CTAs' bytes landed (one arrival from each)
-    uint64_t empty[9];         // per CTA: the pair's MMAs that read the stage completed
-    uint64_t acc_full[2];      // per CTA: accumulators complete
-    uint64_t acc_empty[2];     // leader: both CTAs drained them (one arrival per epilogue warp)
+    uint64_t full[kI8MaxStages];   // per CTA: its TMA bytes landed
+    uint64_t ready[kI8MaxStages];  // leader: both CTAs' bytes landed (one arrival from each)
+    uint64_t empty[kI8MaxStages];  // per CTA: the pair's MMAs that read the stage completed
+    uint64_t acc_full[2];          // per CTA: sums complete
+    uint64_t conv[2];              // leader: both CTAs turned them into fp32 (one arrival per epilogue warp)
+    uint64_t slab_full[2];         // per CTA: correction added
+    uint64_t acc_empty[2];         // leader: both CTAs drained them (one arrival per epilogue warp)
     uint32_t tmem_base;
-    uint32_t last_part;
 };
 
 // Instruction descriptor, kind::i8: signed int8 A and B, int32 accumulator, both K-major, shape M x N.
@@ -79,25 +87,63 @@ __host__ __device__ constexpr uint32_t i8_idesc(int M, int N) {
 }
 
 struct I8Unit {
-    int mi, m0, n0, tile, part;
+    int mi, m0, n0;
     int kb0, nkb, nslab;
+    int slot;            // slot of a segment, -1: a whole tile
 };
-template <int BN>
-__device__ __forceinline__ I8Unit i8_unit(const I8GemmArgs& a, int u) {
+__device__ __forceinline__ I8Unit i8_unit(const I8GemmArgs& a, int bn, int tile, int kb0, int nkb, int slot) {
     I8Unit c;
-    c.tile = u / a.S;
-    c.part = u - c.tile * a.S;
-    const int mt = c.tile / a.ntiles_n, nt = c.tile - mt * a.ntiles_n;
+    const int mt = tile / a.ntiles_n, nt = tile - mt * a.ntiles_n;
     c.mi = 0;
     for (int i = 1; i < a.m; ++i)
         if (mt >= a.mod[i].mtile_begin) c.mi = i;
     c.m0 = (mt - a.mod[c.mi].mtile_begin) * 2 * kI8Rows;
-    c.n0 = nt * BN;
-    const int all = a.d / kI8Block;
-    c.kb0 = c.part * a.kbs;
-    c.nkb = min(a.kbs, all - c.kb0);
-    c.nslab = (c.part == 0 && a.r > 0 && a.mod[c.mi].has_A) ? (a.r + 63) / 64 : 0;
+    c.n0 = nt * bn;
+    c.kb0 = kb0;
+    c.nkb = nkb;
+    c.slot = slot;
+    c.nslab = (slot < 0 && a.r > 0 && a.mod[c.mi].has_A) ? (a.r + 63) / 64 : 0;
     return c;
+}
+// The stages of a pair in order, the same for every role: the k-blocks of each
+// unit, and the slabs of the unit before it in their midst (its sums are turned
+// to fp32 meanwhile, and its buffer is drained before the unit after needs it).
+//   begin(unit, n), block(unit, n, i), end(unit, n), slab(unit, n, j); n: units so far
+template <class Begin, class Block, class End, class Slab>
+__device__ __forceinline__ void i8_walk(const I8GemmArgs& a, int bn, int pair, Begin begin, Block block, End end, Slab slab) {
+    I8Unit prev;
+    prev.nslab = 0;
+    int n = 0, round = 0, seg = 0;
+    int64_t pos = i8_share(a.split, pair);
+    const int64_t stop = i8_share(a.split, pair + 1);
+    while (true) {
+        I8Unit c;
+        if (round < a.split.rounds) {
+            const int64_t tile = (int64_t)round * a.split.pairs + pair;
+            ++round;
+            if (tile >= a.split.whole) continue;
+            c = i8_unit(a, bn, (int)tile, 0, a.split.nkb, -1);
+        } else if (pos < stop) {
+            const int t = (int)(pos / a.split.nkb), kb0 = (int)(pos - (int64_t)t * a.split.nkb);
+            const int nkb = (int)min((int64_t)(a.split.nkb - kb0), stop - pos);
+            pos += nkb;
+            c = i8_unit(a, bn, a.split.rounds * a.split.pairs + t, kb0, nkb, pair * a.split.segments + seg);
+            ++seg;
+        } else {
+            break;
+        }
+        begin(c, n);
+        const int mid = min(8, (c.nkb + 1) / 2);
+        for (int i = 0; i < c.nkb; ++i) {
+            block(c, n, i);
+            if (i + 1 == mid)
+                for (int j = 0; j < prev.nslab; ++j) slab(prev, n - 1, j);
+        }
+        end(c, n);
+        prev = c;
+        ++n;
+    }
+    for (int j = 0; j < prev.nslab; ++j) slab(prev, n - 1, j);
 }
 
 // Four MMAs of one stage (32 bytes of k each), the commits that free it in both
@@ -147,7 +193,7 @@ __global__ void __launch_bounds__(kI8Threads, 1) int8_gemm_kernel(const __grid_c
     I8Barriers* bars = reinterpret_cast<I8Barriers*>(tok + 2 * BN);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const uint32_t crank = cluster_ctarank();                              // 0 = leader (issues the MMAs)
-    const int first = (int)cluster_id_x(), step = (int)cluster_count_x();
+    const int pair = (int)cluster_id_x();
     const int row_off = (int)crank * kI8Rows, tok_off = (int)crank * TL::kHalf;
 
     if (threadIdx.x == 32) {
@@ -167,6 +213,8 @@ __global__ void __launch_bounds__(kI8Threads, 1) int8_gemm_kernel(const __grid_c
         }
         for (int b = 0; b < 2; ++b) {
             mbar_init(&bars->acc_full[b], 1);
+            mbar_init(&bars->conv[b], 8);
+            mbar_init(&bars->slab_full[b], 1);
             mbar_init(&bars->acc_empty[b], 8);
         }
         fence_mbar_init();
@@ -181,38 +229,43 @@ __global__ void __launch_bounds__(kI8Threads, 1) int8_gemm_kernel(const __grid_c
 
     if (warp == 0) {
         // ---------------- producer (both CTAs) ----------------
-        // The codes of W are static: the first ring of them is fetched before
-        // the kernels that quantise X and compute R are known to be complete.
         if (lane == 0) {
             bool ok = true;
             int g = 0, early = 0;
-            for (int pass = 0; pass < 2; ++pass) {
-                g = 0;
-                for (int unit = first; unit < a.nunits; unit += step) {
-                    const I8Unit c = i8_unit<BN>(a, unit);
-                    for (int i = 0; i < c.nkb + c.nslab; ++i, ++g) {
-                        if (pass == 0 && (g >= kStages || i >= c.nkb)) goto stop;   // (slab stages are not static)
-                        const int s = g % kStages;
-                        if (g >= kStages && ok) ok = mbar_wait(&bars->empty[s], ((g / kStages) - 1) & 1, a.status);
-                        const uint32_t ws = smem_u32(sm + s * TL::kStageBytes), xs = ws + kI8WBytes;
-                        if (i < c.nkb) {
-                            if (pass == 0 || g >= early) {
-                                mbar_arrive_expect_tx(&bars->full[s], TL::kStageBytes);
-                                tma_load_2d(ws, &a.tmW[c.mi], &bars->full[s], (c.kb0 + i) * kI8Block, c.m0 + row_off);
-                            }
-                            if (pass == 0) early = g + 1;
-                            else tma_load_2d(xs, &a.tmX, &bars->full[s], (c.kb0 + i) * kI8Block, c.n0 + tok_off);
-                        } else {
-                            const int j = i - c.nkb;
-                            mbar_arrive_expect_tx(&bars->full[s], TL::kStageBytes);
-                            tma_load_2d(ws, &a.tmA[c.mi], &bars->full[s], j * 64, c.m0 + row_off);
-                            tma_load_2d(xs, &a.tmR, &bars->full[s], j * 64, c.n0 + tok_off);
-                        }
+            auto at = [&](int g) { return smem_u32(sm + (g % kStages) * TL::kStageBytes); };
+            auto load_w = [&](const I8Unit& c, int i, int g) {
+                mbar_arrive_expect_tx(&bars->full[g % kStages], TL::kStageBytes);
+                tma_load_2d(at(g), &a.tmW[c.mi], &bars->full[g % kStages], (c.kb0 + i) * kI8Block, c.m0 + row_off);
+            };
+            auto room = [&]() {
+                if (g >= kStages && ok) ok = mbar_wait(&bars->empty[g % kStages], ((g / kStages) - 1) & 1, a.status);
+            };
+            i8_walk(
+                a, BN, pair,
+                [&](const I8Unit& c, int n) {
+                    if (n > 0) return;
+                    // the codes of W are static: the first of them are fetched before the
+                    // kernels that quantise X and compute R are known to be complete
+                    early = min(kStages, c.nkb);
+                    for (int i = 0; i < early; ++i) load_w(c, i, i);
+                    pdl_wait();
+                },
+                [&](const I8Unit& c, int n, int i) {
+                    if (g >= early) {
+                        room();
+                        load_w(c, i, g);
                     }
-                }
-            stop:
-                if (pass == 0) pdl_wait();
-            }
+                    tma_load_2d(at(g) + kI8WBytes, &a.tmX, &bars->full[g % kStages], (c.kb0 + i) * kI8Block, c.n0 + tok_off);
+                    ++g;
+                },
+                [&](const I8Unit&, int) {},
+                [&](const I8Unit& c, int n, int j) {
+                    room();
+                    mbar_arrive_expect_tx(&bars->full[g % kStages], TL::kStageBytes);
+                    tma_load_2d(at(g), &a.tmA[c.mi], &bars->full[g % kStages], j * 64, c.m0 + row_off);
+                    tma_load_2d(at(g) + kI8WBytes, &a.tmR, &bars->full[g % kStages], j * 64, c.n0 + tok_off);
+                    ++g;
+                });
             // the leader's commits for the last stages land here before this CTA may exit
             for (int p = (g > kStages ? g - kStages : 0); p < g && ok; ++p)
                 ok = mbar_wait(&bars->empty[p % kStages], (p / kStages) & 1, a.status);
@@ -223,14 +276,14 @@ __global__ void __launch_bounds__(kI8Threads, 1) int8_gemm_kernel(const __grid_c
             bool ok = true;
             int g = 0;
             pdl_wait();                                   // (bounded waits begin when the codes of X can come)
-            for (int unit = first; unit < a.nunits; unit += step) {
-                const I8Unit c = i8_unit<BN>(a, unit);
-                for (int i = 0; i < c.nkb + c.nslab; ++i, ++g) {
-                    const int s = g % kStages;
-                    if (ok) ok = mbar_wait(&bars->full[s], (g / kStages) & 1, a.status);
-                    mbar_arrive_remote(cluster_addr(&bars->ready[s], 0));
-                }
-            }
+            auto forward = [&]() {
+                if (ok) ok = mbar_wait(&bars->full[g % kStages], (g / kStages) & 1, a.status);
+                mbar_arrive_remote(cluster_addr(&bars->ready[g % kStages], 0));
+                ++g;
+            };
+            i8_walk(
+                a, BN, pair, [&](const I8Unit&, int) {}, [&](const I8Unit&, int, int) { forward(); },
+                [&](const I8Unit&, int) {}, [&](const I8Unit&, int, int) { forward(); });
         }
     } else if (warp == 1) {
         // ---------------- MMA issuer (leader CTA) ----------------
@@ -241,162 +294,137 @@ __global__ void __launch_bounds__(kI8Threads, 1) int8_gemm_kernel(const __grid_c
             const uint32_t empty_l = smem_u32(&bars->empty[0]), empty_p = cluster_addr(&bars->empty[0], 1);
             const uint32_t ready0 = smem_u32(&bars->ready[0]);
             bool ok = true, next_ready = false;
+            int s = 0;
+            uint32_t ph = 0, convs[2] = {0, 0};
             pdl_wait();
-            int tl = 0, s = 0;
-            uint32_t ph = 0;
-            for (int unit = first; unit < a.nunits; unit += step, ++tl) {
-                const I8Unit c = i8_unit<BN>(a, unit);
-                const int buf = tl & 1;
-                if (tl >= 2 && ok) ok = mbar_wait_cluster(&bars->acc_empty[buf], ((tl >> 1) - 1) & 1, a.status);
+            auto stage = [&](auto integer, uint32_t acc, uint32_t accumulate) {
+                if (!next_ready && ok) ok = mbar_wait_cluster(&bars->ready[s], ph, a.status);
                 tc_fence_after();
-                const uint32_t iacc = tmem + (uint32_t)(buf * BN), facc = tmem + (uint32_t)((2 + buf) * BN);
-                for (int i = 0; i < c.nkb + c.nslab; ++i) {
-                    if (!next_ready && ok) ok = mbar_wait_cluster(&bars->ready[s], ph, a.status);
+                const int sn = (s + 1 == kStages) ? 0 : s + 1;
+                const uint32_t phn = (s + 1 == kStages) ? (ph ^ 1u) : ph;
+                constexpr bool kInt = decltype(integer)::value;
+                next_ready = i8_stage_mma<kInt>(acc, wdesc + (uint64_t)s * kStageDesc, xdesc + (uint64_t)s * kStageDesc,
+                                                kInt ? i8_idesc(2 * kI8Rows, BN) : f16_idesc(2 * kI8Rows, BN), accumulate,
+                                                empty_l + 8u * (uint32_t)s, empty_p + 8u * (uint32_t)s,
+                                                ready0 + 8u * (uint32_t)sn, phn) != 0;
+                s = sn;
+                ph = phn;
+            };
+            int units = 0;
+            i8_walk(
+                a, BN, pair,
+                [&](const I8Unit&, int n) {
+                    if (n >= 2 && ok) ok = mbar_wait_cluster(&bars->acc_empty[n & 1], ((n >> 1) - 1) & 1, a.status);
                     tc_fence_after();
-                    const int sn = (s + 1 == kStages) ? 0 : s + 1;
-                    const uint32_t phn = (s + 1 == kStages) ? (ph ^ 1u) : ph;
-                    const uint64_t ad = wdesc + (uint64_t)s * kStageDesc, bd = xdesc + (uint64_t)s * kStageDesc;
-                    const uint32_t el = empty_l + 8u * (uint32_t)s, ep = empty_p + 8u * (uint32_t)s;
-                    const uint32_t pb = ready0 + 8u * (uint32_t)sn;
-                    if (i < c.nkb)
-                        next_ready = i8_stage_mma<true>(iacc, ad, bd, i8_idesc(2 * kI8Rows, BN), i > 0, el, ep, pb, phn) != 0;
-                    else
-                        next_ready = i8_stage_mma<false>(facc, ad, bd, f16_idesc(2 * kI8Rows, BN), i > c.nkb, el, ep, pb, phn) != 0;
-                    s = sn;
-                    ph = phn;
-                }
-                umma_commit_pair(smem_u32(&bars->acc_full[buf]));
-                umma_commit_pair(cluster_addr(&bars->acc_full[buf], 1));
-            }
-            for (int t = (tl > 2 ? tl - 2 : 0); t < tl && ok; ++t)
-                ok = mbar_wait_cluster(&bars->acc_empty[t & 1], (t >> 1) & 1, a.status);
+                    units = n + 1;
+                },
+                [&](const I8Unit&, int n, int i) {
+                    stage(std::integral_constant<bool, true>{}, tmem + (uint32_t)((n & 1) * BN), i > 0 ? 1u : 0u);
+                },
+                [&](const I8Unit&, int n) {
+                    umma_commit_pair(smem_u32(&bars->acc_full[n & 1]));
+                    umma_commit_pair(cluster_addr(&bars->acc_full[n & 1], 1));
+                },
+                [&](const I8Unit& c, int n, int j) {
+                    const int b = n & 1;
+                    if (j == 0) {
+                        if (ok) ok = mbar_wait_cluster(&bars->conv[b], convs[b] & 1, a.status);
+                        ++convs[b];
+                    }
+                    stage(std::integral_constant<bool, false>{}, tmem + (uint32_t)(b * BN), 1u);
+                    if (j + 1 == c.nslab) {
+                        umma_commit_pair(smem_u32(&bars->slab_full[b]));
+                        umma_commit_pair(cluster_addr(&bars->slab_full[b], 1));
+                    }
+                });
+            for (int n = (units > 2 ? units - 2 : 0); n < units && ok; ++n)
+                ok = mbar_wait_cluster(&bars->acc_empty[n & 1], (n >> 1) & 1, a.status);
         }
     } else if (warp >= 4) {
         // ---------------- epilogue (warps 4..7, both CTAs), one thread per row ----------------
         const int quarter = warp & 3, row = quarter * 32 + lane, et = threadIdx.x - 128;
         const bool leader = et == 0;
+        const uint32_t lanes = (uint32_t)(quarter * 32) << 16;
         bool ok = true;
-        int tl = 0, chunk = 0;
+        int chunk = 0;
+        uint32_t slabs[2] = {0, 0};
         pdl_wait();                                       // the token scales are complete
-        for (int unit = first; unit < a.nunits; unit += step, ++tl) {
-            const I8Unit c = i8_unit<BN>(a, unit);
-            const int buf = tl & 1;
-            const int orow = c.m0 + row_off + row;
-            const float so = orow < a.mod[c.mi].O ? __ldg(a.mod[c.mi].s + orow) : 0.f;
-            float* ts = tok + buf * BN;                   // (the previous tile's readers passed this tile's first barrier)
-            for (int i = et; i < BN; i += 128) ts[i] = c.n0 + i < a.T ? ldcg_f32(a.xs + c.n0 + i) : 0.f;
-            if (ok) ok = mbar_wait(&bars->acc_full[buf], (tl >> 1) & 1, a.status);
-            tc_fence_after();
-            named_barrier_sync(1, 128);                   // token scales staged
-            const uint32_t lanes = (uint32_t)(quarter * 32) << 16;
-            const uint32_t iacc = tmem + lanes + (uint32_t)(buf * BN), facc = tmem + lanes + (uint32_t)((2 + buf) * BN);
-            const bool slab_tile = a.r > 0 && a.mod[c.mi].has_A;
-            // y of one chunk from its sums and correction
-            auto store_chunk = [&](const uint32_t (&v)[32], const float (&f)[32], int ch) {
-                unsigned char* sb = epi + (chunk & 1) * kI8EpiBytes;
-                ++chunk;
-                if (leader) bulk_wait_read<1>();
-                named_barrier_sync(1, 128);
-                __half* col = reinterpret_cast<__half*>(sb) + row;
-#pragma unroll
-                for (int j = 0; j < 32; ++j)
-                    col[j * kI8Rows] = __float2half_rn(fmaf((float)(int)v[j] * ts[ch * kI8Chunk + j], so, f[j]));
-                fence_proxy_async_smem();
-                named_barrier_sync(1, 128);
-                const int o0 = c.m0 + row_off, t0 = c.n0 + ch * kI8Chunk;
-                if (leader) {
-                    if (o0 < a.mod[c.mi].O && t0 < a.T) tma_store_2d(&a.tmY[c.mi], smem_u32(sb), o0, t0);
-                    bulk_commit();
-                }
-            };
-            if (a.S == 1) {
+        i8_walk(
+            a, BN, pair, [&](const I8Unit&, int) {}, [&](const I8Unit&, int, int) {},
+            [&](const I8Unit& c, int n) {
+                const int buf = n & 1;
+                const uint32_t acc = tmem + lanes + (uint32_t)(buf * BN);
+                if (c.slot >= 0) {
+                    // a segment of a split tile: its sums to its slot
+                    if (ok) ok = mbar_wait(&bars->acc_full[buf], (n >> 1) & 1, a.status);
+                    tc_fence_after();
+                    int* dst = a.slots + ((int64_t)c.slot * 2 + crank) * (BN * kI8Rows) + row;
+                    const int ntok = min(BN, a.T - c.n0);
 #pragma unroll 1
-                for (int ch = 0; ch < BN / kI8Chunk; ++ch) {
-                    uint32_t v[32];
-                    float f[32];
-                    tmem_ld32(iacc + ch * kI8Chunk, v);
-                    if (slab_tile) {
-                        uint32_t w[32];
-                        tmem_ld32(facc + ch * kI8Chunk, w);
+                    for (int ch = 0; ch < BN / kI8Chunk; ++ch) {
+                        uint32_t v[32];
+                        tmem_ld32(acc + ch * kI8Chunk, v);
 #pragma unroll
-                        for (int j = 0; j < 32; ++j) f[j] = __uint_as_float(w[j]);
-                    } else {
-#pragma unroll
-                        for (int j = 0; j < 32; ++j) f[j] = 0.f;
+                        for (int j = 0; j < 32; ++j)
+                            if (ch * kI8Chunk + j < ntok) __stcg(dst + (ch * kI8Chunk + j) * kI8Rows, (int)v[j]);
                     }
-                    store_chunk(v, f, ch);
+                } else {
+                    const int orow = c.m0 + row_off + row;
+                    const float so = orow < a.mod[c.mi].O ? __ldg(a.mod[c.mi].s + orow) : 0.f;
+                    float* ts = tok + buf * BN;           // (its last readers passed the previous unit's first barrier)
+                    for (int i = et; i < BN; i += 128) ts[i] = c.n0 + i < a.T ? ldcg_f32(a.xs + c.n0 + i) : 0.f;
+                    if (ok) ok = mbar_wait(&bars->acc_full[buf], (n >> 1) & 1, a.status);
+                    tc_fence_after();
+                    named_barrier_sync(1, 128);           // token scales staged
+                    if (c.nslab > 0) {
+#pragma unroll 1
+                        for (int ch = 0; ch < BN / kI8Chunk; ++ch) {
+                            uint32_t v[32];
+                            tmem_ld32(acc + ch * kI8Chunk, v);
+#pragma unroll
+                            for (int j = 0; j < 32; ++j)
+                                v[j] = __float_as_uint((float)(int)v[j] * ts[ch * kI8Chunk + j] * so);
+                            tmem_st32(acc + ch * kI8Chunk, v);
+                        }
+                        tc_fence_before();
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive_remote(cluster_addr(&bars->conv[buf], 0));
+                        if (ok) ok = mbar_wait(&bars->slab_full[buf], slabs[buf] & 1, a.status);
+                        ++slabs[buf];
+                        tc_fence_after();
+                    }
+#pragma unroll 1
+                    for (int ch = 0; ch < BN / kI8Chunk; ++ch) {
+                        const int o0 = c.m0 + row_off, t0 = c.n0 + ch * kI8Chunk;
+                        if (t0 >= a.T) break;
+                        uint32_t v[32];
+                        tmem_ld32(acc + ch * kI8Chunk, v);
+                        unsigned char* sb = epi + (chunk & 1) * kI8EpiBytes;
+                        ++chunk;
+                        if (leader) bulk_wait_read<1>();
+                        named_barrier_sync(1, 128);
+                        __half* col = reinterpret_cast<__half*>(sb) + row;
+                        if (c.nslab > 0) {
+#pragma unroll
+                            for (int j = 0; j < 32; ++j) col[j * kI8Rows] = __float2half_rn(__uint_as_float(v[j]));
+                        } else {
+#pragma unroll
+                            for (int j = 0; j < 32; ++j)
+                                col[j * kI8Rows] = __float2half_rn((float)(int)v[j] * ts[ch * kI8Chunk + j] * so);
+                        }
+                        fence_proxy_async_smem();
+                        named_barrier_sync(1, 128);
+                        if (leader) {
+                            if (o0 < a.mod[c.mi].O) tma_store_2d(&a.tmY[c.mi], smem_u32(sb), o0, t0);
+                            bulk_commit();
+                        }
+                    }
                 }
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) mbar_arrive_remote(cluster_addr(&bars->acc_empty[buf], 0));
-                continue;
-            }
-            // a part of a split tile: its sums to its slot ([token / 4][row] of 16 bytes), part 0's correction behind them
-            const int per = a.S + (a.r > 0 ? 1 : 0);
-            int4* slots = a.slots + ((int64_t)c.tile * 2 + crank) * per * (BN / 4 * kI8Rows) + row;
-            auto to_slot = [&](uint32_t acc, int p) {
-#pragma unroll 1
-                for (int ch = 0; ch < BN / kI8Chunk; ++ch) {
-                    uint32_t v[32];
-                    tmem_ld32(acc + ch * kI8Chunk, v);
-                    int4* dst = slots + ((int64_t)p * (BN / 4) + ch * 8) * kI8Rows;
-#pragma unroll
-                    for (int q = 0; q < 8; ++q)
-                        __stcg(dst + q * kI8Rows, make_int4((int)v[4 * q], (int)v[4 * q + 1], (int)v[4 * q + 2], (int)v[4 * q + 3]));
-                }
-            };
-            to_slot(iacc, c.part);
-            if (c.nslab > 0) to_slot(facc, a.S);
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive_remote(cluster_addr(&bars->acc_empty[buf], 0));
-            __threadfence();
-            named_barrier_sync(1, 128);
-            if (leader) {
-                unsigned int* tk = a.tickets + c.tile * 2 + crank;
-                unsigned int prev;
-                asm volatile("atom.acq_rel.gpu.global.add.u32 %0, [%1], 1;" : "=r"(prev) : "l"(tk) : "memory");
-                const uint32_t last = prev == (unsigned)(a.S - 1) ? 1u : 0u;
-                if (last) atomicExch(tk, 0u);             // every part has counted: ready for the next call
-                *reinterpret_cast<volatile uint32_t*>(&bars->last_part) = last;
-            }
-            named_barrier_sync(1, 128);
-            if (*reinterpret_cast<volatile uint32_t*>(&bars->last_part) == 0u) continue;
-            __threadfence();
-#pragma unroll 1
-            for (int ch = 0; ch < BN / kI8Chunk; ++ch) {
-                uint32_t v[32];
-                float f[32];
-#pragma unroll
-                for (int j = 0; j < 32; ++j) v[j] = 0u, f[j] = 0.f;
-#pragma unroll 1
-                for (int p = 0; p < a.S; ++p) {
-                    const int4* src = slots + ((int64_t)p * (BN / 4) + ch * 8) * kI8Rows;
-                    int4 x[8];
-#pragma unroll
-                    for (int q = 0; q < 8; ++q) x[q] = __ldcg(src + q * kI8Rows);
-#pragma unroll
-                    for (int q = 0; q < 8; ++q) {
-                        v[4 * q] += (uint32_t)x[q].x;
-                        v[4 * q + 1] += (uint32_t)x[q].y;
-                        v[4 * q + 2] += (uint32_t)x[q].z;
-                        v[4 * q + 3] += (uint32_t)x[q].w;
-                    }
-                }
-                if (slab_tile) {
-                    const int4* src = slots + ((int64_t)a.S * (BN / 4) + ch * 8) * kI8Rows;
-#pragma unroll
-                    for (int q = 0; q < 8; ++q) {
-                        const int4 x = __ldcg(src + q * kI8Rows);
-                        f[4 * q] = __int_as_float(x.x);
-                        f[4 * q + 1] = __int_as_float(x.y);
-                        f[4 * q + 2] = __int_as_float(x.z);
-                        f[4 * q + 3] = __int_as_float(x.w);
-                    }
-                }
-                store_chunk(v, f, ch);
-            }
-        }
+            },
+            [&](const I8Unit&, int, int) {});
         if (leader) bulk_wait_all();
     }
     pdl_wait();                                           // every thread: this grid's end implies the preceding ones'
@@ -407,34 +435,148 @@ __global__ void __launch_bounds__(kI8Threads, 1) int8_gemm_kernel(const __grid_c
 }
 
 // ---------------------------------------------------------------------------
-// Host side
+// Split tiles: one block per 128 rows x 32 tokens of a tile.  A warp has 16
+// rows: lane (g, t) the rows g and g + 8 of tokens 2 t, 2 t + 1 of each 8.
 // ---------------------------------------------------------------------------
-// Token width and parts per tile: the busiest pair's time in tensor-core
-// clocks, a k-block of a tile costing its MMAs (2 BN) but not less than its
-// codes' way from memory, a unit a fixed drain, a split its partial sums.
-I8GemmPlan plan_int8_gemm(int64_t T, int64_t d, int64_t mtiles, int r, int num_sms) {
-    I8GemmPlan best = {};
-    const int64_t pairs = num_sms / 2 > 0 ? num_sms / 2 : 1, nkb = d / kI8Block;
-    double least = 0;
-    for (int bn = 64; bn <= 128; bn += 64) {
-        const int64_t nt = (T + bn - 1) / bn, tiles = mtiles * nt;
-        for (int S = 1; S <= 8; ++S) {
-            const int64_t kbs = (nkb + S - 1) / S;
-            if (S > 1 && (kbs < 4 || (S - 1) * kbs >= nkb || tiles * 2 > kInt8MaxTickets || tiles >= pairs)) break;
-            const double block = bn == 64 ? 300 : 2.2 * bn, drain = 1500 + 10.0 * bn;
-            const double cost = (double)((tiles * S + pairs - 1) / pairs) * ((double)kbs * block + drain) +
-                                (S > 1 ? 1500.0 + 12.0 * bn * S : 0.0);
-            if (best.bn == 0 || cost < least) {
-                least = cost;
-                best.bn = bn;
-                best.S = S;
-                best.kbs = (int)kbs;
-                best.tiles = tiles;
-                best.slot_bytes = S > 1 ? (size_t)tiles * 2 * (S + (r > 0 ? 1 : 0)) * bn * kI8Rows * 4 : 0;
+struct I8JoinModule {
+    const float* s;
+    const __half* A;
+    __half* Y;
+    int64_t ldY;
+    int O, mtile_begin;
+};
+struct I8JoinArgs {
+    I8JoinModule mod[GLOWQ_MAX_MODULES];
+    const float* xs;
+    const __half* R;
+    const int* slots;
+    I8Split split;
+    int m, T, r, bn, ntiles_n;
+};
+
+__global__ void __launch_bounds__(256) int8_join_kernel(const __grid_constant__ I8JoinArgs a) {
+    pdl_launch_dependents();
+    const int chunks = a.bn / 32;
+    const int ch = blockIdx.x % chunks, half = (blockIdx.x / chunks) & 1, rel = blockIdx.x / chunks / 2;
+    const int tile = a.split.rounds * a.split.pairs + rel;
+    const int mt = tile / a.ntiles_n, nt = tile - mt * a.ntiles_n;
+    int mi = 0;
+    for (int i = 1; i < a.m; ++i)
+        if (mt >= a.mod[i].mtile_begin) mi = i;
+    const I8JoinModule& md = a.mod[mi];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+    const int wrow = warp * 16, row0 = (mt - md.mtile_begin) * 2 * kI8Rows + half * kI8Rows + wrow;
+    const int t0 = nt * a.bn + ch * 32;
+    if (t0 >= a.T || row0 >= md.O) {                      // (O % 16 == 0: a warp's rows are all there or none)
+        pdl_wait();
+        return;
+    }
+    // A and the scales are static; R, the sums and the token scales come from the preceding kernels
+    const float s0 = __ldg(md.s + row0 + g), s1 = __ldg(md.s + row0 + g + 8);
+    const bool corrects = a.r > 0 && md.A;
+    uint4 af[4] = {};
+    auto load_a = [&](int j0) {
+        const __half* A = md.A + (int64_t)(row0 + g) * a.r + j0 + 16 * t;
+#pragma unroll
+        for (int p = 0; p < 2; ++p) {
+            af[p] = af[2 + p] = make_uint4(0, 0, 0, 0);
+            if (j0 + 16 * t + 8 * p < a.r) {
+                af[p] = ldg_128(A + 8 * p);
+                af[2 + p] = ldg_128(A + 8 * p + (int64_t)8 * a.r);
+            }
+        }
+    };
+    if (corrects) load_a(0);
+    pdl_wait();
+    // the segments that hold the tile's k-blocks [rel nkb, (rel + 1) nkb): pairs p0 .. p1
+    const int64_t lo = (int64_t)rel * a.split.nkb, hi = lo + a.split.nkb;
+    int p = (int)(lo * a.split.pairs / a.split.blocks);
+    while (i8_share(a.split, p + 1) <= lo) ++p;
+    while (i8_share(a.split, p) > lo) --p;
+    int v[4][4] = {};
+    for (; p < a.split.pairs && i8_share(a.split, p) < hi; ++p) {
+        const int64_t begin = i8_share(a.split, p);
+        if (begin == i8_share(a.split, p + 1)) continue;  // no share (fewer blocks than pairs)
+        const int seg = (int)(rel - begin / a.split.nkb); // the pair's segments are one per tile, in order
+        const int* src = a.slots + (((int64_t)p * a.split.segments + seg) * 2 + half) * ((int64_t)a.bn * kI8Rows) +
+                         (int64_t)ch * 32 * kI8Rows + wrow + g;
+#pragma unroll
+        for (int n = 0; n < 4; ++n)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                const int tok = n * 8 + 2 * t + e;
+                if (t0 + tok < a.T) {
+                    v[n][e] += __ldcg(src + tok * kI8Rows);
+                    v[n][2 + e] += __ldcg(src + tok * kI8Rows + 8);
+                }
+            }
+    }
+    float c[4][4] = {};
+    if (corrects) {
+        for (int j0 = 0; j0 < a.r; j0 += 64) {
+            if (j0 > 0) load_a(j0);
+#pragma unroll
+            for (int n = 0; n < 4; ++n) {
+                const int tok = t0 + n * 8 + g;
+#pragma unroll
+                for (int q = 0; q < 2; ++q) {
+                    const int j = j0 + 16 * t + 8 * q;
+                    uint4 x = make_uint4(0, 0, 0, 0);
+                    if (tok < a.T && j < a.r) x = ldcg_128(a.R + (int64_t)tok * a.r + j);
+                    const uint32_t a1[4] = {af[q].x, af[2 + q].x, af[q].y, af[2 + q].y}, b1[2] = {x.x, x.y};
+                    const uint32_t a2[4] = {af[q].z, af[2 + q].z, af[q].w, af[2 + q].w}, b2[2] = {x.z, x.w};
+                    mma_16816(c[n], a1, b1);
+                    mma_16816(c[n], a2, b2);
+                }
             }
         }
     }
-    return best;
+#pragma unroll
+    for (int n = 0; n < 4; ++n)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+            const int tok = t0 + n * 8 + 2 * t + e;
+            if (tok < a.T) {
+                const float st = ldcg_f32(a.xs + tok);
+                __half* y = md.Y + (int64_t)tok * md.ldY + row0 + g;
+                y[0] = __float2half_rn(fmaf((float)v[n][e] * st, s0, c[n][e]));
+                y[8] = __float2half_rn(fmaf((float)v[n][2 + e] * st, s1, c[n][2 + e]));
+            }
+        }
+}
+
+// ---------------------------------------------------------------------------
+// Host side
+// ---------------------------------------------------------------------------
+// Token width: the fewest token tiles, then the narrowest that holds T in them.
+// Whole rounds of tiles for every pair, and the rest split, unless a last round
+// of whole tiles ends sooner: in clocks, a k-block 600, a split the stores of
+// its sums and the join (about 2 us, and the sums' way at 5 TB/s).
+I8GemmPlan plan_int8_gemm(int64_t T, int64_t d, int64_t mtiles, int num_sms) {
+    I8GemmPlan p;
+    const int64_t pairs = gemm_max_pairs(num_sms), nkb = d / kI8Block;
+    const int64_t nt = (T + 255) / 256;
+    p.bn = (int)(((T + nt - 1) / nt + 63) / 64 * 64);
+    const int64_t tiles = mtiles * nt;
+    int64_t rounds = tiles / pairs, rest = tiles - rounds * pairs;
+    const double blocks = (double)rest * nkb;
+    const double split = blocks / pairs * 600 + 4000 + (double)rest * 256 * p.bn * 8 / 2600.0;
+    p.split.pairs = (int)(tiles < pairs && rest > 0 && nkb * 600.0 < split ? tiles : pairs);
+    if (rest > 0 && nkb * 600.0 < split) {
+        // the last round is one of whole tiles: pairs without a tile in it have none
+        p.split.whole = tiles;
+        rest = 0;
+        rounds = (tiles + p.split.pairs - 1) / p.split.pairs;
+    } else {
+        p.split.whole = rounds * pairs;
+    }
+    p.split.rounds = (int)rounds;
+    p.split.nkb = (int)nkb;
+    p.split.blocks = rest * nkb;
+    p.split.segments = (int)((p.split.blocks + pairs - 1) / pairs / nkb + 2);
+    p.rest = rest;
+    p.slot_bytes = rest > 0 ? (size_t)pairs * p.split.segments * 2 * kI8Rows * p.bn * 4 : 0;
+    return p;
 }
 
 template <int BN>
@@ -461,8 +603,7 @@ static cudaError_t launch_int8_gemm_t(const I8GemmArgs& a, int pairs, cudaStream
 }
 
 cudaError_t launch_int8_gemm(const Int8ModuleView* mods, int m, int d, int64_t T, int r, const int8_t* xq,
-                             const float* xs, const uint16_t* R, unsigned int* tickets, void* slots,
-                             const I8GemmPlan& p, int num_sms, cudaStream_t st) {
+                             const float* xs, const uint16_t* R, int* slots, const I8GemmPlan& p, cudaStream_t st) {
     I8GemmArgs a;
     std::memset(&a, 0, sizeof(a));
     const uint32_t half = (uint32_t)(p.bn / 2);
@@ -492,14 +633,30 @@ cudaError_t launch_int8_gemm(const Int8ModuleView* mods, int m, int d, int64_t T
     a.T = (int)T;
     a.r = r;
     a.ntiles_n = (int)((T + p.bn - 1) / p.bn);
-    a.nunits = (int)(p.tiles * p.S);
-    a.S = p.S;
-    a.kbs = p.kbs;
-    a.slots = static_cast<int4*>(slots);
-    a.tickets = tickets;
+    a.split = p.split;
+    a.slots = slots;
     a.status = device_status_ptr();
-    const int most = gemm_max_pairs(num_sms), pairs = a.nunits < most ? a.nunits : most;
-    return p.bn == 64 ? launch_int8_gemm_t<64>(a, pairs, st) : launch_int8_gemm_t<128>(a, pairs, st);
+    const int pairs = p.split.pairs;
+    cudaError_t e = p.bn == 64    ? launch_int8_gemm_t<64>(a, pairs, st)
+                    : p.bn == 128 ? launch_int8_gemm_t<128>(a, pairs, st)
+                    : p.bn == 192 ? launch_int8_gemm_t<192>(a, pairs, st)
+                                  : launch_int8_gemm_t<256>(a, pairs, st);
+    if (e != cudaSuccess || p.rest == 0) return e;
+    I8JoinArgs j = {};
+    for (int i = 0; i < m; ++i)
+        j.mod[i] = {mods[i].s, r > 0 ? reinterpret_cast<const __half*>(mods[i].A) : nullptr, reinterpret_cast<__half*>(mods[i].Y),
+                    mods[i].ldY, (int)mods[i].O, a.mod[i].mtile_begin};
+    j.xs = xs;
+    j.R = reinterpret_cast<const __half*>(R);
+    j.slots = slots;
+    j.split = p.split;
+    j.m = m;
+    j.T = (int)T;
+    j.r = r;
+    j.bn = p.bn;
+    j.ntiles_n = a.ntiles_n;
+    void* args[] = {(void*)&j};
+    return launch_pdl((const void*)int8_join_kernel, (unsigned)(p.rest * 2 * (p.bn / 32)), 256, 0, st, args);
 }
 
 }  // namespace glowq

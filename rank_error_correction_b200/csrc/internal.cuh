@@ -88,7 +88,7 @@ struct Int8ModuleView {
     int64_t O;
 };
 constexpr int64_t kInt8MaxD = 131072;          // 127^2 d < 2^31
-constexpr int kInt8SmallTokens = 64;           // tokens up to which the weight-streaming product runs
+constexpr int kInt8SmallTokens = 16;           // tokens up to which the weight-streaming product runs
 constexpr int kInt8ZeroBytes = 65536;          // tickets at the workspace's start
 constexpr int kInt8MaxTickets = kInt8ZeroBytes / 4;
 // Decomposition of the small-T product: S CTAs share a tile's k, wk warps of a CTA.
@@ -107,16 +107,23 @@ cudaError_t launch_quantize_act_int8(const uint16_t* X, int64_t T, int64_t d, in
 cudaError_t launch_int8_small(const Int8ModuleView* mods, int m, int d, int T, int r, const uint16_t* X,
                               const uint16_t* B, uint16_t* R, int8_t* xq, float* xs, unsigned int* tickets, int* slots,
                               const Int8GemvPlan& p, cudaStream_t st);
-// int8_gemm.cu: larger T on the tensor cores
-struct I8GemmPlan {
-    int bn, S, kbs;      // tokens per pair tile, parts per tile, k-blocks per part
-    int64_t tiles;
-    size_t slot_bytes;   // partial sums (S > 1)
+// int8_gemm.cu: T > 16 on the tensor cores.  `rounds` whole tiles per pair
+// (tiles [0, whole)), then the other tiles' k-blocks as one run of `blocks` cut
+// evenly among the pairs; a pair's share has at most `segments` tiles' segments.
+struct I8Split {
+    int pairs, rounds, nkb, segments;
+    int64_t whole, blocks;
 };
-I8GemmPlan plan_int8_gemm(int64_t T, int64_t d, int64_t mtiles, int r, int num_sms);
+__host__ __device__ inline int64_t i8_share(const I8Split& s, int pair) { return s.blocks * pair / s.pairs; }
+struct I8GemmPlan {
+    int bn;              // tokens per pair tile
+    I8Split split;
+    int64_t rest;        // split tiles
+    size_t slot_bytes;   // their partial sums
+};
+I8GemmPlan plan_int8_gemm(int64_t T, int64_t d, int64_t mtiles, int num_sms);
 cudaError_t launch_int8_gemm(const Int8ModuleView* mods, int m, int d, int64_t T, int r, const int8_t* xq,
-                             const float* xs, const uint16_t* R, unsigned int* tickets, void* slots,
-                             const I8GemmPlan& p, int num_sms, cudaStream_t st);
+                             const float* xs, const uint16_t* R, int* slots, const I8GemmPlan& p, cudaStream_t st);
 // prefill.cu: R = X B^T on the tensor cores (scratch of prefill_partial_bytes(T, r))
 cudaError_t launch_rproj_prefill(const uint16_t* X, const uint16_t* B, int64_t T, int d, int r, uint16_t* R,
                                  float* partial, int num_sms, cudaStream_t st, const float* tok_scale,

@@ -88,6 +88,9 @@ SHAPES = [
     (31, 2176, [272], 128), (33, 5120, [160, 32], 256), (64, 4096, [1024], 64), (64, 13824, [80], 16),
     (65, 256, [304], 64), (100, 4096, [64], 0), (129, 896, [528, 16], 8), (257, 1152, [272, 400], 64),
     (300, 768, [256, 48, 144], 40), (520, 2048, [1040], 256), (1000, 384, [2064], 64),
+    # more tiles than CTA pairs: whole tiles, a rest that is split or not, short k, several slabs
+    (2000, 256, [2560, 272], 72), (1500, 128, [5120], 8), (2500, 640, [4096], 0), (1030, 1152, [10000], 256),
+    (4000, 128, [512, 16, 4112], 200), (300, 256, [18944], 64),
 ]
 
 
