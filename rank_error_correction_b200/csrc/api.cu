@@ -167,12 +167,12 @@ static glowq_status fp4_views(glowq_format fmt, const glowq_fp4_module* mods, in
     return GLOWQ_OK;
 }
 
-// W8A8 workspace: [zero region: tickets][codes][token scales][solo R][R partials][k-split sums]
+// W8A8 workspace: [zero region: tickets][codes][token scales][solo R][k-split sums]
 struct W8A8Layout {
     bool small;          // the weight-streaming product, else the tensor-core GEMM
     Int8GemvPlan gemv;
     I8GemmPlan gemm;
-    size_t codes, scales, R, partial, slots, total;
+    size_t codes, scales, R, slots, total;
 };
 static W8A8Layout w8a8_layout(int64_t T, int64_t d, int32_t r, const int64_t* outs, int32_t m) {
     W8A8Layout L;
@@ -192,8 +192,7 @@ static W8A8Layout w8a8_layout(int64_t T, int64_t d, int32_t r, const int64_t* ou
     L.codes = kInt8ZeroBytes;
     L.scales = L.codes + align_up((size_t)rows * d, 256);
     L.R = L.scales + align_up((size_t)rows * 4, 256);
-    L.partial = L.R + align_up((size_t)T * r * 2, 256);
-    L.slots = L.partial + (L.small || r == 0 ? 0 : align_up(prefill_partial_bytes(T, r), 256));
+    L.slots = L.R + align_up((size_t)T * r * 2, 256);
     L.total = L.slots + (L.small ? L.gemv.slot_bytes : L.gemm.slot_bytes);
     return L;
 }
@@ -242,18 +241,16 @@ static glowq_status w8a8_impl(const glowq_int8_module* mods, int32_t m, int64_t 
     int8_t* codes = reinterpret_cast<int8_t*>(ws + L.codes);
     float* scales = reinterpret_cast<float*>(ws + L.scales);
     uint16_t* R = solo ? reinterpret_cast<uint16_t*>(ws + L.R) : R_out;
-    cudaError_t e;
+    int* slots = reinterpret_cast<int*>(ws + L.slots);
+    cudaError_t e = cudaSuccess;
     if (L.small) {
-        e = launch_int8_small(hm, m, (int)d, (int)T, r, X, B, R, codes, scales, tickets,
-                              reinterpret_cast<int*>(ws + L.slots), L.gemv, st);
+        e = launch_int8_small(hm, m, (int)d, (int)T, r, X, B, R, codes, scales, tickets, slots, L.gemv, st);
     } else {
         if (!encode_fn()) return GLOWQ_ERR_CUDA;
-        e = r > 0 ? launch_rproj_prefill(X, B, T, (int)d, r, R, reinterpret_cast<float*>(ws + L.partial),
-                                         device_sm_count(), st, nullptr, nullptr)
-                  : cudaSuccess;
-        if (e == cudaSuccess) e = launch_quantize_act_int8(X, T, d, codes, scales, st, r > 0);
+        if (r > 0) e = launch_int8_project(X, B, T, (int)d, r, R, st);
         if (e == cudaSuccess)
-            e = launch_int8_gemm(hm, m, (int)d, T, r, codes, scales, R, reinterpret_cast<int*>(ws + L.slots), L.gemm, st);
+            e = r > 0 ? launch_quantize_beside(X, T, d, codes, scales, st) : launch_quantize_act_int8(X, T, d, codes, scales, st);
+        if (e == cudaSuccess) e = launch_int8_gemm(hm, m, (int)d, T, r, codes, scales, R, slots, L.gemm, st);
     }
     return e == cudaSuccess ? GLOWQ_OK : GLOWQ_ERR_CUDA;
 }

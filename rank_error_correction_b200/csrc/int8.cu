@@ -34,6 +34,22 @@ __device__ __forceinline__ uint32_t int8_pack4(float a, float b, float c, float 
     return (uint32_t)(int8_code(a, s) & 255) | ((uint32_t)(int8_code(b, s) & 255) << 8) |
            ((uint32_t)(int8_code(c, s) & 255) << 16) | ((uint32_t)(int8_code(d, s) & 255) << 24);
 }
+// The same code from p = x * fp32(1 / s), and without a division unless p is
+// within 1e-4 of a half-integer: |p| < 128 and p is off the quotient by 2^-22
+// relative at most (3.1e-5), so elsewhere both round to the same integer.  (An
+// IEEE division per element made the quantiser ALU-bound: 12 us instead of 5
+// at T = 2048, d = 4096.)  Adding 1.5 2^23 rounds to even and leaves the
+// integer in the low bits.  s >= 2^-24 / 127, as for fp16 rows.
+__device__ __forceinline__ uint32_t int8_code_fast(float x, float s, float inv) {
+    const float p = x * inv, m = p + 12582912.f;
+    if (fabsf(fabsf(p - (m - 12582912.f)) - 0.5f) < 1e-4f) return (uint32_t)int8_code(x, s);
+    return __float_as_uint(m);
+}
+__device__ __forceinline__ uint32_t int8_pack4_fast(float a, float b, float c, float d, float s, float inv) {
+    const uint32_t lo = __byte_perm(int8_code_fast(a, s, inv), int8_code_fast(b, s, inv), 0x0040);
+    const uint32_t hi = __byte_perm(int8_code_fast(c, s, inv), int8_code_fast(d, s, inv), 0x0040);
+    return __byte_perm(lo, hi, 0x5410);
+}
 // Maximum of |x| and whether every x is finite, over the block; the result in every thread.
 __device__ __forceinline__ void block_amax(float& amax, bool& finite) {
     __shared__ float red[kQuantThreads / 32];
@@ -117,13 +133,14 @@ __device__ __forceinline__ void quantize_token(const uint16_t* __restrict__ X, i
     block_amax(amax, finite);
     const float s = int8_row_scale(amax, finite);
     if (threadIdx.x == 0) scales[t] = s;
+    const float inv = __fdiv_rn(1.f, s);
     auto code = [&](int i, const uint4& u) {
         const float2 a = __half22float2(u32_as_h2(u.x)), b = __half22float2(u32_as_h2(u.y));
         const float2 c = __half22float2(u32_as_h2(u.z)), e = __half22float2(u32_as_h2(u.w));
         uint2 q = make_uint2(0u, 0u);
         if (finite) {
-            q.x = int8_pack4(a.x, a.y, b.x, b.y, s);
-            q.y = int8_pack4(c.x, c.y, e.x, e.y, s);
+            q.x = int8_pack4_fast(a.x, a.y, b.x, b.y, s, inv);
+            q.y = int8_pack4_fast(c.x, c.y, e.x, e.y, s, inv);
         }
         codes8(i, q);
     };
@@ -135,9 +152,9 @@ __device__ __forceinline__ void quantize_token(const uint16_t* __restrict__ X, i
     for (int i = threadIdx.x + kKeep * kQuantThreads; i < n8; i += kQuantThreads) code(i, ldcg_128(x + i));
 }
 
-// One token per block, codes row-major [T][d].  BESIDE: launched behind kernels
-// of the same call that have already waited for X (the projection R), so it
-// runs beside them and waits for their end at its own.
+// One token per block, codes row-major [T][d].  BESIDE: launched behind the
+// projection of the same call, which has waited for X: it runs beside it and
+// waits for its end at its own, so that its end implies both.
 template <bool BESIDE>
 __global__ void __launch_bounds__(kQuantThreads) quantize_act_int8_kernel(const uint16_t* __restrict__ X, int64_t d,
                                                                           int8_t* __restrict__ codes,
@@ -151,10 +168,13 @@ __global__ void __launch_bounds__(kQuantThreads) quantize_act_int8_kernel(const 
 }
 
 // ---------------------------------------------------------------------------
-// Small T (<= 64), first launch: blocks [0, TOK) quantise a token each into
-// the layout the product stages with one bulk copy, [d/64][TOK][64] (tokens
-// past T are zero); the others compute R = X B^T, two rows of B for up to 16
-// tokens per block, fp32 sums in a fixed order, rounded to fp16.
+// Small T (<= 16), first launch.  The first blocks compute R = X B^T, two rows
+// of B for all tokens per block, fp32 sums in a fixed order, rounded to fp16
+// (splitting d over blocks as well costs more in joining the parts than it
+// saves: 8.0 us against 4.9 at T = 1, d = 4096).  The others (only when the
+// product does not quantise by itself) quantise a token each into the layout
+// that the product stages with one bulk copy, [d/64][TOK][64]; tokens past T
+// are zero.
 // ---------------------------------------------------------------------------
 constexpr int kPrepRows = 2, kPrepTokens = 16;
 
@@ -167,26 +187,10 @@ struct Int8PrepArgs {
     int d, T, tok, r;
 };
 
-__global__ void __launch_bounds__(kQuantThreads) int8_prep_kernel(const Int8PrepArgs a) {
-    pdl_launch_dependents();
-    pdl_wait();                                  // X is final; the previous call's readers of xq, xs, R are done
-    if ((int)blockIdx.x < a.tok) {
-        const int t = blockIdx.x;
-        auto at = [&](int i) {                   // element 8 i of token t
-            return reinterpret_cast<uint2*>(a.xq + ((int64_t)(i >> 3) * a.tok + t) * 64 + (i & 7) * 8);
-        };
-        if (t < a.T) {
-            quantize_token(a.X, t, a.d, a.xs, [&](int i, uint2 q) { *at(i) = q; });
-        } else {
-            for (int i = threadIdx.x; i < a.d / 8; i += kQuantThreads) *at(i) = make_uint2(0u, 0u);
-            if (threadIdx.x == 0) a.xs[t] = 0.f;
-        }
-        return;
-    }
-    const int b = blockIdx.x - a.tok, nrow = a.r / kPrepRows;
-    const int j0 = (b % nrow) * kPrepRows, t0 = (b / nrow) * kPrepTokens;
-    const int nt = min(kPrepTokens, a.T - t0);
-    float acc[kPrepTokens][kPrepRows] = {};
+template <int TOK>
+__device__ __forceinline__ void prep_rows(const Int8PrepArgs& a) {
+    const int j0 = blockIdx.x * kPrepRows;
+    float acc[TOK][kPrepRows] = {};
     for (int i = threadIdx.x; i < a.d / 8; i += kQuantThreads) {
         float w[kPrepRows][8];
 #pragma unroll
@@ -201,9 +205,9 @@ __global__ void __launch_bounds__(kQuantThreads) int8_prep_kernel(const Int8Prep
             }
         }
 #pragma unroll
-        for (int t = 0; t < kPrepTokens; ++t) {
-            if (t >= nt) break;
-            const uint4 u = ldcg_128(a.X + (int64_t)(t0 + t) * a.d + 8 * i);
+        for (int t = 0; t < TOK; ++t) {
+            if (t >= a.T) break;
+            const uint4 u = ldcg_128(a.X + (int64_t)t * a.d + 8 * i);
             const uint32_t v[4] = {u.x, u.y, u.z, u.w};
 #pragma unroll
             for (int q = 0; q < 4; ++q) {
@@ -214,11 +218,11 @@ __global__ void __launch_bounds__(kQuantThreads) int8_prep_kernel(const Int8Prep
             }
         }
     }
-    __shared__ float red[kQuantThreads / 32][kPrepTokens * kPrepRows];
+    __shared__ float red[kQuantThreads / 32][TOK * kPrepRows];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 #pragma unroll
-    for (int t = 0; t < kPrepTokens; ++t) {
-        if (t >= nt) break;
+    for (int t = 0; t < TOK; ++t) {
+        if (t >= a.T) break;
 #pragma unroll
         for (int j = 0; j < kPrepRows; ++j) {
             float v = acc[t][j];
@@ -227,24 +231,49 @@ __global__ void __launch_bounds__(kQuantThreads) int8_prep_kernel(const Int8Prep
         }
     }
     __syncthreads();
-    if ((int)threadIdx.x < nt * kPrepRows) {
+    if ((int)threadIdx.x < min(a.T, TOK) * kPrepRows) {
         float v = 0.f;
         for (int w = 0; w < kQuantThreads / 32; ++w) v += red[w][threadIdx.x];
-        a.R[(int64_t)(t0 + threadIdx.x / kPrepRows) * a.r + j0 + threadIdx.x % kPrepRows] = __float2half_rn(v);
+        a.R[(int64_t)(threadIdx.x / kPrepRows) * a.r + j0 + threadIdx.x % kPrepRows] = __float2half_rn(v);
+    }
+}
+
+__global__ void __launch_bounds__(kQuantThreads) int8_prep_kernel(const Int8PrepArgs a) {
+    pdl_wait();                                  // X is final; the previous call's readers of xq, xs, R are done
+    pdl_launch_dependents();                     // (only now: the product may read X without waiting for this kernel)
+    if ((int)blockIdx.x < a.r / kPrepRows) {
+        if (a.T <= 4) prep_rows<4>(a);
+        else prep_rows<kPrepTokens>(a);
+        return;
+    }
+    const int t = (int)blockIdx.x - a.r / kPrepRows;
+    auto at = [&](int i) {                       // elements 8 i .. + 7 of token t
+        return reinterpret_cast<uint2*>(a.xq + ((int64_t)(i >> 3) * a.tok + t) * 64 + (i & 7) * 8);
+    };
+    if (t < a.T) {
+        quantize_token(a.X, t, a.d, a.xs, [&](int i, uint2 q) { *at(i) = q; });
+    } else {
+        for (int i = threadIdx.x; i < a.d / 8; i += kQuantThreads) *at(i) = make_uint2(0u, 0u);
+        if (threadIdx.x == 0) a.xs[t] = 0.f;
     }
 }
 
 // ---------------------------------------------------------------------------
-// Small T: the product.  Weight streaming; each warp owns a 16-row tile of one
-// module and a share of its k, read as blocks of 16 rows x 128 k (2 KB) into a
-// private ring in shared memory with cp.async: a lane copies exactly the bytes
-// that it later feeds to the MMA, so no barrier stands between copy and use.
-// mma.m16n8k32 takes k in any order as long as both operands agree: lane
-// (g, t) holds the 16 bytes k = 64 h + 16 t .. + 15 of rows g and g + 8, and of
-// token g of the staged activations.
+// Small T: the product.  Weight streaming; a block's eight warps share a 16-row
+// tile of one module, each a share of its k, read as blocks of 16 rows x 128 k
+// (2 KB) into a private ring in shared memory with cp.async: a lane copies
+// exactly the bytes that it later feeds to the MMA, so no barrier stands
+// between copy and use.  mma.m16n8k32 takes k in any order as long as both
+// operands agree: lane (g, t) holds the 16 bytes k = 64 h + 16 t .. + 15 of
+// rows g and g + 8, and of token g of the staged activations.
+// SELF: the block quantises the tokens itself (few of them: each block reads
+// all of X), which needs no kernel to wait for; the projection of R runs beside
+// and is waited for before the first output.
 // ---------------------------------------------------------------------------
 constexpr int kGemvWarps = 8;
+constexpr int kGemvStages = 4;
 constexpr int kBlockBytes = 2048;                // 16 rows x 128 k
+constexpr int kSelfElements = 16384;             // T d up to which SELF is used
 
 struct Int8GemvModule {
     const int8_t* q;
@@ -256,14 +285,14 @@ struct Int8GemvModule {
 };
 struct Int8GemvArgs {
     Int8GemvModule mod[GLOWQ_MAX_MODULES];
-    const int8_t* xq;       // [d/64][TOK][64]
+    const uint16_t* X;      // SELF: [T][d]
+    const int8_t* xq;       // else: [d/64][TOK][64] and
     const float* xs;        // [TOK]
     const __half* R;        // [T][r]
     int* slots;             // [tile][NT][S][4][32] partial sums (S > 1)
     unsigned int* tickets;  // [tile][NT], zero between calls
     int m, d, T, r, tiles;
-    int S;                  // CTAs that share a tile's k
-    int wk;                 // warps of a CTA that share a tile's k
+    int S;                  // blocks that share a tile's k
     unsigned int* status;
 };
 
@@ -282,41 +311,100 @@ __device__ __forceinline__ void mma_s8(int c[4], uint32_t a0, uint32_t a1, uint3
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
-// Shared memory: [X codes TOK x krange][ring][R TOK x r][sums 2 x 8 x NT x 512][barrier]
+// Shared memory: [codes of X, TOK x k range][rings][R, TOK x r][sums 2 x 8 x NT x 512][token scales][barrier]
 struct Int8GemvSmem {
-    int ring, rt, red, bar, total;
+    int ring, rt, red, xs, bar, total;
 };
-__host__ __device__ inline Int8GemvSmem int8_gemv_smem(int nt, int kblocks, int stages, int wk, int r) {
+__host__ __device__ inline Int8GemvSmem int8_gemv_smem(int nt, int kblocks, int r) {
     Int8GemvSmem s;
     s.ring = nt * 8 * kblocks * 128;
-    s.rt = s.ring + kGemvWarps * stages * kBlockBytes;
+    s.rt = s.ring + kGemvWarps * kGemvStages * kBlockBytes;
     s.red = (s.rt + nt * 8 * r * 2 + 127) / 128 * 128;
-    s.bar = s.red + (wk > 1 ? 2 * kGemvWarps * nt * 512 : 0);
+    s.xs = s.red + 2 * kGemvWarps * nt * 512;
+    s.bar = s.xs + nt * 8 * 4;
     s.total = s.bar + 16;
     return s;
 }
 
-constexpr int kGemvStages = 4;
+// Codes (of k blocks [kb0, kb1)) and scales of all tokens into shared memory:
+// a token by 8 / P warps, P = T rounded up to a power of two.
+template <int TOK>
+__device__ __forceinline__ void self_quantize(const Int8GemvArgs& a, unsigned char* codes, float* xs, float* red, int kb0,
+                                              int kb1) {
+    static_assert(TOK == 8, "a warp or more per token");
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int per = a.T > 4 ? 1 : a.T > 2 ? 2 : a.T > 1 ? 4 : 8;         // warps per token
+    const int t = warp / per, first = (warp % per) * 32 + lane, step = per * 32, n8 = a.d / 8;
+    const uint4* x = reinterpret_cast<const uint4*>(a.X + (int64_t)t * a.d);
+    constexpr int kKeep = 8;
+    uint4 keep[kKeep];
+    float amax = 0.f;
+    bool finite = true;
+    auto see = [&](const uint4& u) {
+        const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const float2 f = __half22float2(u32_as_h2(w[j]));
+            amax = fmaxf(amax, fmaxf(fabsf(f.x), fabsf(f.y)));
+            finite &= fabsf(f.x) <= FLT_MAX && fabsf(f.y) <= FLT_MAX;
+        }
+    };
+    if (t < a.T) {
+#pragma unroll
+        for (int j = 0; j < kKeep; ++j)
+            if (first + j * step < n8) keep[j] = ldcg_128(x + first + j * step);
+#pragma unroll
+        for (int j = 0; j < kKeep; ++j)
+            if (first + j * step < n8) see(keep[j]);
+        for (int i = first + kKeep * step; i < n8; i += step) see(ldcg_128(x + i));
+    }
+    for (int o = 16; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(~0u, amax, o));
+    if (__any_sync(~0u, !finite)) amax = INFINITY;                       // carries "not finite" through the maximum
+    if (lane == 0) red[warp] = amax;
+    __syncthreads();
+    for (int w = 0; w < per; ++w) amax = fmaxf(amax, red[t * per + w]);
+    finite = amax <= FLT_MAX;
+    const float s = int8_row_scale(amax, finite), inv = __fdiv_rn(1.f, s);
+    if (warp % per == 0 && lane == 0) xs[t] = s;
+    auto code = [&](int i, const uint4& u) {
+        if (i < kb0 * 16 || i >= kb1 * 16) return;
+        const float2 a0 = __half22float2(u32_as_h2(u.x)), b = __half22float2(u32_as_h2(u.y));
+        const float2 c = __half22float2(u32_as_h2(u.z)), e = __half22float2(u32_as_h2(u.w));
+        uint2 q = make_uint2(0u, 0u);
+        if (finite) {
+            q.x = int8_pack4_fast(a0.x, a0.y, b.x, b.y, s, inv);
+            q.y = int8_pack4_fast(c.x, c.y, e.x, e.y, s, inv);
+        }
+        *reinterpret_cast<uint2*>(codes + ((i >> 3) - 2 * kb0) * (TOK * 64) + t * 64 + (i & 7) * 8) = q;
+    };
+    if (t < a.T) {
+#pragma unroll
+        for (int j = 0; j < kKeep; ++j)
+            if (first + j * step < n8) code(first + j * step, keep[j]);
+        for (int i = first + kKeep * step; i < n8; i += step) code(i, ldcg_128(x + i));
+    }
+    // tokens past T: their sums are not stored, but the codes must be numbers that are written
+    for (int i = threadIdx.x; i < (kb1 - kb0) * 2 * (TOK - a.T) * 4; i += kGemvWarps * 32) {
+        const int c = i & 3, rest = i >> 2, tok = a.T + rest % (TOK - a.T), kb = rest / (TOK - a.T);
+        *reinterpret_cast<uint4*>(codes + (kb * TOK + tok) * 64 + c * 16) = make_uint4(0, 0, 0, 0);
+    }
+}
 
-template <int NT>
+template <int NT, bool SELF>
 __global__ void __launch_bounds__(kGemvWarps * 32) int8_gemv_kernel(const __grid_constant__ Int8GemvArgs a) {
     extern __shared__ __align__(128) unsigned char sm[];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
-    const int wk = a.wk, wr = kGemvWarps / wk;
-    const int kw = warp % wk, rw = warp / wk;            // this warp's share of k, its tile within the CTA's step
-    const int ks = blockIdx.x % a.S, cx = blockIdx.x / a.S, nx = gridDim.x / a.S;
+    const int ks = blockIdx.x % a.S, tile0 = blockIdx.x / a.S, step = gridDim.x / a.S;
     const int nkb = a.d / 128;
     const int kb0 = (int)((int64_t)ks * nkb / a.S), kb1 = (int)((int64_t)(ks + 1) * nkb / a.S);
-    const int kmax = (nkb + a.S - 1) / a.S;              // blocks that shared memory is laid out for
-    const Int8GemvSmem L = int8_gemv_smem(NT, kmax, kGemvStages, wk, a.r);
+    const Int8GemvSmem L = int8_gemv_smem(NT, (nkb + a.S - 1) / a.S, a.r);
     const uint32_t base = smem_u32(sm);
     const uint32_t ring = base + L.ring + warp * kGemvStages * kBlockBytes + lane * 16;
+    float* xs = reinterpret_cast<float*>(sm + L.xs);
     uint64_t* bar = reinterpret_cast<uint64_t*>(sm + L.bar);
-    const int nsteps = (kb1 - kb0 + wk - 1) / wk;        // ring blocks per tile (the last may be absent)
-    const int step_tiles = nx * wr;
-    const int tile0 = cx * wr;                           // the CTA's first step: tiles tile0 .. tile0 + wr - 1
+    const int nsteps = (kb1 - kb0 + kGemvWarps - 1) / kGemvWarps;      // ring blocks per tile (the last may be absent)
     const uint64_t policy = l2_policy_evict_first();
-    if (threadIdx.x == 0) {
+    if (!SELF && threadIdx.x == 0) {
         mbar_init(bar, 1);
         fence_mbar_init();
     }
@@ -326,30 +414,28 @@ __global__ void __launch_bounds__(kGemvWarps * 32) int8_gemv_kernel(const __grid
             if (tile >= a.mod[i].tile_begin) mi = i;
         return mi;
     };
-    // the next block to copy: block pi of this warp's tile in the step at pb, into ring stage ps
-    int pb = tile0, pi = 0, ps = 0;
+    // the next block to copy: block pi of tile pt, into ring stage ps
+    int pt = tile0, pi = 0, ps = 0;
     const int8_t* psrc = nullptr;                        // row g of the tile, byte 16 t
     auto prefetch = [&]() {
-        if (pb < a.tiles) {
-            const int tile = pb + rw, kb = kb0 + pi * wk + kw;
-            if (tile < a.tiles) {
-                if (pi == 0) {
-                    const Int8GemvModule& md = a.mod[module_of(tile)];
-                    psrc = md.q + ((int64_t)(tile - md.tile_begin) * 16 + g) * a.d + 16 * t;
-                }
-                if (kb < kb1) {
-                    const int8_t* src = psrc + (int64_t)kb * 128;
-                    const uint32_t dst = ring + ps * kBlockBytes;
+        if (pt < a.tiles) {
+            const int kb = kb0 + pi * kGemvWarps + warp;
+            if (pi == 0) {
+                const Int8GemvModule& md = a.mod[module_of(pt)];
+                psrc = md.q + ((int64_t)(pt - md.tile_begin) * 16 + g) * a.d + 16 * t;
+            }
+            if (kb < kb1) {
+                const int8_t* src = psrc + (int64_t)kb * 128;
+                const uint32_t dst = ring + ps * kBlockBytes;
 #pragma unroll
-                    for (int h = 0; h < 2; ++h) {
-                        cp_async16(dst + h * 1024, src + h * 64, policy);
-                        cp_async16(dst + h * 1024 + 512, src + h * 64 + (int64_t)8 * a.d, policy);
-                    }
+                for (int h = 0; h < 2; ++h) {
+                    cp_async16(dst + h * 1024, src + h * 64, policy);
+                    cp_async16(dst + h * 1024 + 512, src + h * 64 + (int64_t)8 * a.d, policy);
                 }
             }
             if (++pi == nsteps) {
                 pi = 0;
-                pb += step_tiles;
+                pt += step;
             }
         }
         if (++ps == kGemvStages) ps = 0;
@@ -369,37 +455,47 @@ __global__ void __launch_bounds__(kGemvWarps * 32) int8_gemv_kernel(const __grid
             }
         }
     };
+    auto stage_r = [&]() {
+        for (int i = threadIdx.x; i < NT * a.r; i += kGemvWarps * 32) {   // 8 halves each
+            uint4 v = make_uint4(0, 0, 0, 0);
+            if (i * 8 / a.r < a.T) v = ldcg_128(a.R + i * 8);
+            *reinterpret_cast<uint4*>(sm + L.rt + i * 16) = v;
+        }
+    };
     for (int i = 0; i < kGemvStages - 1; ++i) prefetch();
-    __syncthreads();                                     // the barrier is initialised
-    pdl_wait();                                          // codes, scales and R of this call are complete
-    pdl_launch_dependents();
-    if (threadIdx.x == 0) {
-        const uint32_t bytes = (uint32_t)(NT * 8 * 128) * (uint32_t)(kb1 - kb0);
-        fence_proxy_async_smem();
-        mbar_arrive_expect_tx(bar, bytes);
-        bulk_g2s(base, a.xq + (int64_t)kb0 * (NT * 8 * 128), bytes, bar);
+    if constexpr (SELF) {
+        // launched behind the projection, which has waited for X (r > 0), or first in the call
+        if (a.r == 0) pdl_wait();
+        pdl_launch_dependents();
+        self_quantize<8>(a, sm, xs, reinterpret_cast<float*>(sm + L.red), kb0, kb1);
+    } else {
+        __syncthreads();                                 // the barrier is initialised
+        pdl_wait();                                      // codes, scales and R of this call are complete
+        pdl_launch_dependents();
+        if (threadIdx.x == 0) {
+            const uint32_t bytes = (uint32_t)(NT * 8 * 128) * (uint32_t)(kb1 - kb0);
+            fence_proxy_async_smem();
+            mbar_arrive_expect_tx(bar, bytes);
+            bulk_g2s(base, a.xq + (int64_t)kb0 * (NT * 8 * 128), bytes, bar);
+        }
+        for (int i = threadIdx.x; i < NT * 8; i += kGemvWarps * 32) xs[i] = ldcg_f32(a.xs + i);
+        stage_r();
+        mbar_wait(bar, 0, a.status);
     }
-    for (int i = threadIdx.x; i < NT * a.r; i += kGemvWarps * 32) {   // 8 halves each
-        const int tok = i * 8 / a.r;
-        uint4 v = make_uint4(0, 0, 0, 0);
-        if (tok < a.T) v = ldcg_128(a.R + i * 8);
-        *reinterpret_cast<uint4*>(sm + L.rt + i * 16) = v;
-    }
-    mbar_wait(bar, 0, a.status);
     __syncthreads();
     int cs = 0, par = 0;
-    for (int tb = tile0; tb < a.tiles; tb += step_tiles, par ^= 1) {
-        const int tile = tb + rw;
+    for (int tile = tile0; tile < a.tiles; tile += step, par ^= 1) {
         int acc[NT][4] = {};
-        // the tile's first 64 columns of A, loaded ahead by the warps that will apply them (fragments below)
+        // the tile's first 64 columns of A, loaded ahead by the warps that will apply them
         uint4 af[4];
-        const bool corrects = tile < a.tiles && a.r > 0 && kw < NT && a.mod[module_of(tile)].A;
+        const int mi = module_of(tile);
+        const bool corrects = a.r > 0 && warp < NT && a.mod[mi].A;
         if (corrects) load_a(tile, 0, af);
         for (int i = 0; i < nsteps; ++i) {
             prefetch();
             cp_async_wait<kGemvStages - 1>();
-            const int kb = i * wk + kw;                  // within this CTA's k range
-            if (tile < a.tiles && kb0 + kb < kb1) {
+            const int kb = i * kGemvWarps + warp;        // within this block's k range
+            if (kb0 + kb < kb1) {
                 const unsigned char* src = sm + L.ring + (warp * kGemvStages + cs) * kBlockBytes + lane * 16;
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
@@ -416,81 +512,75 @@ __global__ void __launch_bounds__(kGemvWarps * 32) int8_gemv_kernel(const __grid
             }
             if (++cs == kGemvStages) cs = 0;
         }
-        // sums of the warps that share the tile, in shared memory
-        int4* red = reinterpret_cast<int4*>(sm + L.red + par * kGemvWarps * NT * 512);
-        if (wk > 1) {
-#pragma unroll
-            for (int n = 0; n < NT; ++n) red[(warp * NT + n) * 32 + lane] = make_int4(acc[n][0], acc[n][1], acc[n][2], acc[n][3]);
-            __syncthreads();                             // also: the tile's rows of A, copied by these warps, are in place
-        } else {
-            __syncwarp();
+        if (SELF && tile == tile0 && a.r > 0) {
+            pdl_wait();                                  // R is complete
+            stage_r();
         }
-        if (tile >= a.tiles) continue;
-        const int mi = module_of(tile);
+        // the warps' sums meet in shared memory (double buffered: one barrier per tile)
+        int4* red = reinterpret_cast<int4*>(sm + L.red + par * kGemvWarps * NT * 512);
+#pragma unroll
+        for (int n = 0; n < NT; ++n) red[(warp * NT + n) * 32 + lane] = make_int4(acc[n][0], acc[n][1], acc[n][2], acc[n][3]);
+        __syncthreads();
+        if (warp >= NT) continue;                        // warp n finishes tokens 8 n .. 8 n + 7
+        const int n = warp;
         const Int8GemvModule& md = a.mod[mi];
         const int row0 = (tile - md.tile_begin) * 16;
+        int v[4] = {0, 0, 0, 0};
 #pragma unroll
-        for (int n = 0; n < NT; ++n) {
-            if (wk > 1 && n % wk != kw) continue;
-            int v[4] = {acc[n][0], acc[n][1], acc[n][2], acc[n][3]};
-            if (wk > 1) {
-                v[0] = v[1] = v[2] = v[3] = 0;
-                for (int w = 0; w < wk; ++w) {
-                    const int4 p = red[((rw * wk + w) * NT + n) * 32 + lane];
-                    v[0] += p.x, v[1] += p.y, v[2] += p.z, v[3] += p.w;
+        for (int w = 0; w < kGemvWarps; ++w) {
+            const int4 p = red[(w * NT + n) * 32 + lane];
+            v[0] += p.x, v[1] += p.y, v[2] += p.z, v[3] += p.w;
+        }
+        if (a.S > 1) {
+            // this block's share of k to its slot; the share that counts last adds them all (integers: any order)
+            int* slot = a.slots + (((int64_t)tile * NT + n) * a.S) * 128 + lane;
+#pragma unroll
+            for (int q = 0; q < 4; ++q) __stcg(slot + ks * 128 + q * 32, v[q]);
+            __threadfence();
+            __syncwarp();
+            unsigned int prev = 0;
+            unsigned int* tk = a.tickets + tile * NT + n;
+            if (lane == 0)
+                asm volatile("atom.acq_rel.gpu.global.add.u32 %0, [%1], 1;" : "=r"(prev) : "l"(tk) : "memory");
+            prev = __shfl_sync(~0u, prev, 0);
+            if (prev != (unsigned)(a.S - 1)) continue;
+            if (lane == 0) atomicExch(tk, 0u);           // every share has counted: ready for the next call
+            __threadfence();
+            for (int s = 0; s < a.S; ++s) {
+                if (s == ks) continue;
+#pragma unroll
+                for (int q = 0; q < 4; ++q) v[q] += __ldcg(slot + s * 128 + q * 32);
+            }
+        }
+        float c[4] = {0.f, 0.f, 0.f, 0.f};
+        if (corrects) {
+            for (int j0 = 0; j0 < a.r; j0 += 64) {
+                if (j0 > 0) load_a(tile, j0, af);
+                uint4 x[2];
+#pragma unroll
+                for (int p = 0; p < 2; ++p) {
+                    const int j = j0 + 16 * t + 8 * p;
+                    x[p] = make_uint4(0, 0, 0, 0);
+                    if (j < a.r) x[p] = *reinterpret_cast<const uint4*>(sm + L.rt + ((n * 8 + g) * a.r + j) * 2);
+                }
+#pragma unroll
+                for (int p = 0; p < 2; ++p) {
+                    const uint32_t a1[4] = {af[p].x, af[2 + p].x, af[p].y, af[2 + p].y}, b1[2] = {x[p].x, x[p].y};
+                    const uint32_t a2[4] = {af[p].z, af[2 + p].z, af[p].w, af[2 + p].w}, b2[2] = {x[p].z, x[p].w};
+                    mma_16816(c, a1, b1);
+                    mma_16816(c, a2, b2);
                 }
             }
-            if (a.S > 1) {
-                // this CTA's share of k to its slot; the share that counts last adds them all (integers: any order)
-                int* slot = a.slots + (((int64_t)tile * NT + n) * a.S) * 128 + lane;
+        }
+        const float s0 = __ldg(md.s + row0 + g), s1 = __ldg(md.s + row0 + g + 8);
 #pragma unroll
-                for (int q = 0; q < 4; ++q) __stcg(slot + ks * 128 + q * 32, v[q]);
-                __threadfence();
-                __syncwarp();
-                unsigned int prev = 0;
-                unsigned int* tk = a.tickets + tile * NT + n;
-                if (lane == 0)
-                    asm volatile("atom.acq_rel.gpu.global.add.u32 %0, [%1], 1;" : "=r"(prev) : "l"(tk) : "memory");
-                prev = __shfl_sync(~0u, prev, 0);
-                if (prev != (unsigned)(a.S - 1)) continue;
-                if (lane == 0) atomicExch(tk, 0u);       // every share has counted: ready for the next call
-                __threadfence();
-                for (int s = 0; s < a.S; ++s) {
-                    if (s == ks) continue;
-#pragma unroll
-                    for (int q = 0; q < 4; ++q) v[q] += __ldcg(slot + s * 128 + q * 32);
-                }
-            }
-            float c[4] = {0.f, 0.f, 0.f, 0.f};
-            if (corrects) {
-                for (int j0 = 0; j0 < a.r; j0 += 64) {
-                    if (j0 > 0 || (a.r > 64 && n != kw)) load_a(tile, j0, af);   // else still held from the tile's start
-                    uint4 x[2];
-#pragma unroll
-                    for (int p = 0; p < 2; ++p) {
-                        const int j = j0 + 16 * t + 8 * p;
-                        x[p] = make_uint4(0, 0, 0, 0);
-                        if (j < a.r) x[p] = *reinterpret_cast<const uint4*>(sm + L.rt + ((n * 8 + g) * a.r + j) * 2);
-                    }
-#pragma unroll
-                    for (int p = 0; p < 2; ++p) {
-                        const uint32_t a1[4] = {af[p].x, af[2 + p].x, af[p].y, af[2 + p].y}, b1[2] = {x[p].x, x[p].y};
-                        const uint32_t a2[4] = {af[p].z, af[2 + p].z, af[p].w, af[2 + p].w}, b2[2] = {x[p].z, x[p].w};
-                        mma_16816(c, a1, b1);
-                        mma_16816(c, a2, b2);
-                    }
-                }
-            }
-            const float s0 = __ldg(md.s + row0 + g), s1 = __ldg(md.s + row0 + g + 8);
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-                const int tok = n * 8 + 2 * t + e;
-                if (tok < a.T) {
-                    const float st = ldcg_f32(a.xs + tok);
-                    __half* y = md.Y + (int64_t)tok * md.ldY + row0 + g;
-                    y[0] = __float2half_rn(fmaf((float)v[e] * st, s0, c[e]));
-                    y[8] = __float2half_rn(fmaf((float)v[2 + e] * st, s1, c[2 + e]));
-                }
+        for (int e = 0; e < 2; ++e) {
+            const int tok = n * 8 + 2 * t + e;
+            if (tok < a.T) {
+                const float st = xs[tok];
+                __half* y = md.Y + (int64_t)tok * md.ldY + row0 + g;
+                y[0] = __float2half_rn(fmaf((float)v[e] * st, s0, c[e]));
+                y[8] = __float2half_rn(fmaf((float)v[2 + e] * st, s1, c[2 + e]));
             }
         }
     }
@@ -523,44 +613,46 @@ cudaError_t launch_pdl(const void* fn, unsigned grid, unsigned block, size_t sme
     return cudaLaunchKernelExC(&cfg, fn, args);
 }
 cudaError_t launch_quantize_act_int8(const uint16_t* X, int64_t T, int64_t d, int8_t* codes, float* scales,
-                                     cudaStream_t st, bool beside) {
+                                     cudaStream_t st) {
     void* args[] = {(void*)&X, (void*)&d, (void*)&codes, (void*)&scales};
-    return launch_pdl(beside ? (const void*)quantize_act_int8_kernel<true> : (const void*)quantize_act_int8_kernel<false>,
-                      (unsigned)T, kQuantThreads, 0, st, args);
+    return launch_pdl((const void*)quantize_act_int8_kernel<false>, (unsigned)T, kQuantThreads, 0, st, args);
+}
+
+cudaError_t launch_quantize_beside(const uint16_t* X, int64_t T, int64_t d, int8_t* codes, float* scales,
+                                   cudaStream_t st) {
+    void* args[] = {(void*)&X, (void*)&d, (void*)&codes, (void*)&scales};
+    return launch_pdl((const void*)quantize_act_int8_kernel<true>, (unsigned)T, kQuantThreads, 0, st, args);
 }
 
 // Token width (a multiple of 8) of the small-T kernels.
 int int8_small_tokens(int64_t T) { return T <= 8 ? 8 : 16; }
 
-// Decomposition of the small-T product.
+// Decomposition of the small-T product: the fewest shares of k that leave two
+// blocks an SM (or one, if the staged activations need the room) and a tile or
+// more for each, or whose shares are down to two blocks per warp.
 Int8GemvPlan plan_int8_gemv(int64_t T, int64_t d, int64_t tiles, int r, int num_sms) {
     Int8GemvPlan p;
     const int nt = int8_small_tokens(T) / 8, nkb = (int)(d / 128);
-    p.wk = nt <= 2 ? kGemvWarps : nt == 4 ? 2 : 1;
-    const int wr = kGemvWarps / p.wk;
     for (p.S = 1; p.S < nkb; ++p.S) {
-        const int smem = int8_gemv_smem(nt, (nkb + p.S - 1) / p.S, kGemvStages, p.wk, r).total;
-        if (smem > 227 * 1024) continue;
-        const int64_t steps = (tiles + wr - 1) / wr;
-        if (steps * p.S >= num_sms || (nkb + p.S) / (p.S + 1) < 2 * p.wk) break;
+        if (int8_gemv_smem(nt, (nkb + p.S - 1) / p.S, r).total > 227 * 1024) continue;
+        if (tiles * p.S >= num_sms || (nkb + p.S) / (p.S + 1) < 2 * kGemvWarps) break;
     }
-    p.smem = int8_gemv_smem(nt, (nkb + p.S - 1) / p.S, kGemvStages, p.wk, r).total;
+    p.smem = int8_gemv_smem(nt, (nkb + p.S - 1) / p.S, r).total;
     p.ok = p.smem <= 227 * 1024 && (p.S == 1 || tiles * nt <= kInt8MaxTickets) && tiles < (1 << 24);
-    const int per_sm = p.smem <= 113 * 1024 ? 2 : 1;
-    const int64_t steps = (tiles + wr - 1) / wr;
-    const int64_t slots = (int64_t)num_sms * per_sm / p.S;
-    p.grid = (int)(steps < slots ? steps : (slots < 1 ? 1 : slots)) * p.S;
+    p.self = T <= 8 && T * d <= kSelfElements;
+    const int64_t slots = (int64_t)num_sms * (p.smem <= 113 * 1024 ? 2 : 1) / p.S;
+    p.grid = (int)(tiles < slots ? tiles : (slots < 1 ? 1 : slots)) * p.S;
     p.slot_bytes = p.S > 1 ? (size_t)tiles * nt * p.S * 512 : 0;
     return p;
 }
 
-template <int NT>
+template <int NT, bool SELF>
 static cudaError_t launch_int8_gemv_t(const Int8GemvArgs& a, const Int8GemvPlan& p, cudaStream_t st) {
-    cudaError_t e = cudaFuncSetAttribute((const void*)int8_gemv_kernel<NT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                         227 * 1024);
+    const void* fn = (const void*)int8_gemv_kernel<NT, SELF>;
+    cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, 227 * 1024);
     if (e != cudaSuccess) return e;
     void* args[] = {(void*)&a};
-    return launch_pdl((const void*)int8_gemv_kernel<NT>, (unsigned)p.grid, kGemvWarps * 32, (size_t)p.smem, st, args);
+    return launch_pdl(fn, (unsigned)p.grid, kGemvWarps * 32, (size_t)p.smem, st, args);
 }
 
 cudaError_t launch_int8_small(const Int8ModuleView* mods, int m, int d, int T, int r, const uint16_t* X,
@@ -569,9 +661,11 @@ cudaError_t launch_int8_small(const Int8ModuleView* mods, int m, int d, int T, i
     const int tok = int8_small_tokens(T);
     Int8PrepArgs pa = {X, B, xq, xs, reinterpret_cast<__half*>(R), d, T, tok, r};
     void* pargs[] = {(void*)&pa};
-    const unsigned rblocks = r > 0 ? (unsigned)(r / kPrepRows * ((T + kPrepTokens - 1) / kPrepTokens)) : 0u;
-    cudaError_t e = launch_pdl((const void*)int8_prep_kernel, (unsigned)tok + rblocks, kQuantThreads, 0, st, pargs);
-    if (e != cudaSuccess) return e;
+    const unsigned blocks = (unsigned)(r / kPrepRows + (p.self ? 0 : tok));
+    if (blocks > 0) {
+        cudaError_t e = launch_pdl((const void*)int8_prep_kernel, blocks, kQuantThreads, 0, st, pargs);
+        if (e != cudaSuccess) return e;
+    }
     Int8GemvArgs a = {};
     int tile = 0;
     for (int i = 0; i < m; ++i) {
@@ -579,6 +673,7 @@ cudaError_t launch_int8_small(const Int8ModuleView* mods, int m, int d, int T, i
                     mods[i].ldY, tile};
         tile += (int)(mods[i].O / 16);
     }
+    a.X = X;
     a.xq = xq;
     a.xs = xs;
     a.R = reinterpret_cast<const __half*>(R);
@@ -590,12 +685,9 @@ cudaError_t launch_int8_small(const Int8ModuleView* mods, int m, int d, int T, i
     a.r = r;
     a.tiles = tile;
     a.S = p.S;
-    a.wk = p.wk;
     a.status = device_status_ptr();
-    switch (tok) {
-        case 8: return launch_int8_gemv_t<1>(a, p, st);
-        default: return launch_int8_gemv_t<2>(a, p, st);
-    }
+    if (p.self) return launch_int8_gemv_t<1, true>(a, p, st);
+    return T <= 8 ? launch_int8_gemv_t<1, false>(a, p, st) : launch_int8_gemv_t<2, false>(a, p, st);
 }
 
 }  // namespace glowq

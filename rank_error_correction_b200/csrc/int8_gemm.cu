@@ -7,9 +7,9 @@
 // [128 p, +128) of the codes and half of the tokens' codes (128-byte rows, one
 // swizzle atom, by TMA), the leader's MMA thread issues M = 256, N = BN, K = 32
 // per step, and each CTA's TMEM receives the int32 sums of its 128 rows, double
-// buffered so that a tile's drain overlaps the next tile's products.  A k-block
-// of 128 (four steps) takes 565-610 clocks for every BN from 64 to 256 (the
-// rows of W set the pace), so BN is the widest that T fills.
+// buffered so that a tile's drain overlaps the next tile's products.  BN is as
+// wide as T fills, up to 256, where a k-block of 128 (four steps) takes the
+// tensor cores 512 clocks: 3.09 POPS measured at T = 2048, d = O = 16384.
 //
 // Whole tiles: the epilogue turns the sums into s_t s_o sum in fp32 in place,
 // the correction's K = 64 slabs of fp16 (A_i and R by TMA, zero beyond r) are
@@ -31,7 +31,7 @@ namespace glowq {
 constexpr int kI8Rows = 128;             // W rows per CTA (TMEM lanes)
 constexpr int kI8Block = 128;            // k per stage: one 128-byte swizzle atom of int8
 constexpr int kI8WBytes = kI8Rows * kI8Block;
-constexpr int kI8Threads = 256;          // producer, MMA, forwarder, (idle), 4 epilogue warps
+constexpr int kI8Threads = 192;          // producer, MMA, 4 epilogue warps
 constexpr int kI8Chunk = 32;             // tokens per epilogue step
 constexpr int kI8EpiBytes = kI8Chunk * kI8Rows * 2;
 constexpr int kI8SmemMax = 227 * 1024;
@@ -71,8 +71,7 @@ struct I8GemmArgs {
 };
 
 struct __align__(8) I8Barriers {
-    uint64_t full[kI8MaxStages];   // per CTA: its TMA bytes landed
-    uint64_t ready[kI8MaxStages];  // leader: both CTAs' bytes landed (one arrival from each)
+    uint64_t full[kI8MaxStages];   // leader: both CTAs' TMA bytes landed
     uint64_t empty[kI8MaxStages];  // per CTA: the pair's MMAs that read the stage completed
     uint64_t acc_full[2];          // per CTA: sums complete
     uint64_t conv[2];              // leader: both CTAs turned them into fp32 (one arrival per epilogue warp)
@@ -114,8 +113,8 @@ __device__ __forceinline__ void i8_walk(const I8GemmArgs& a, int bn, int pair, B
     I8Unit prev;
     prev.nslab = 0;
     int n = 0, round = 0, seg = 0;
-    int64_t pos = i8_share(a.split, pair);
-    const int64_t stop = i8_share(a.split, pair + 1);
+    int pos = i8_share(a.split, pair);
+    const int stop = i8_share(a.split, pair + 1);
     while (true) {
         I8Unit c;
         if (round < a.split.rounds) {
@@ -124,8 +123,8 @@ __device__ __forceinline__ void i8_walk(const I8GemmArgs& a, int bn, int pair, B
             if (tile >= a.split.whole) continue;
             c = i8_unit(a, bn, (int)tile, 0, a.split.nkb, -1);
         } else if (pos < stop) {
-            const int t = (int)(pos / a.split.nkb), kb0 = (int)(pos - (int64_t)t * a.split.nkb);
-            const int nkb = (int)min((int64_t)(a.split.nkb - kb0), stop - pos);
+            const int t = pos / a.split.nkb, kb0 = pos - t * a.split.nkb;
+            const int nkb = min(a.split.nkb - kb0, stop - pos);
             pos += nkb;
             c = i8_unit(a, bn, a.split.rounds * a.split.pairs + t, kb0, nkb, pair * a.split.segments + seg);
             ++seg;
@@ -146,32 +145,29 @@ __device__ __forceinline__ void i8_walk(const I8GemmArgs& a, int bn, int pair, B
     for (int j = 0; j < prev.nslab; ++j) slab(prev, n - 1, j);
 }
 
-// Four MMAs of one stage (32 bytes of k each), the commits that free it in both
-// CTAs, and a non-blocking probe of the next stage's barrier whose round trip
-// the issue hides.
+// Four MMAs of one stage (32 bytes of k each) and the commit that frees it in
+// both CTAs, issued by one lane of a warp that runs the loop as a whole: the
+// descriptors are then warp-uniform values.  (Inside an `if (lane == 0)` each
+// MMA took about 140 clocks to issue whatever its N, most of it moving
+// descriptors into uniform registers.)
 template <bool INT>
-__device__ __forceinline__ uint32_t i8_stage_mma(uint32_t dacc, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
-                                                 uint32_t accumulate, uint32_t empty_local, uint32_t empty_peer,
-                                                 uint32_t probe_bar, uint32_t probe_parity) {
-    uint32_t ready;
+__device__ __forceinline__ void i8_stage_mma(uint32_t dacc, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
+                                             uint32_t accumulate, uint32_t empty) {
 #define GLOWQ_STAGE_MMA(KIND)                                                                             \
     asm volatile(                                                                                         \
-        "{\n\t.reg .pred pr, pa, pt;\n\t.reg .b64 a1, a2, a3, b1, b2, b3;\n\t"                             \
-        "mbarrier.test_wait.parity.shared::cta.b64 pr, [%6], %7;\n\t"                                     \
-        "setp.ne.b32 pa, %3, 0;\n\t"                                                                      \
-        "setp.eq.b32 pt, %3, %3;\n\t"                                                                     \
-        "add.s64 a1, %8, 2;\n\tadd.s64 a2, %8, 4;\n\tadd.s64 a3, %8, 6;\n\t"                              \
-        "add.s64 b1, %9, 2;\n\tadd.s64 b2, %9, 4;\n\tadd.s64 b3, %9, 6;\n\t"                              \
-        "tcgen05.mma.cta_group::2.kind::" KIND " [%1], %8, %9, %2, pa;\n\t"                               \
-        "tcgen05.mma.cta_group::2.kind::" KIND " [%1], a1, b1, %2, pt;\n\t"                               \
-        "tcgen05.mma.cta_group::2.kind::" KIND " [%1], a2, b2, %2, pt;\n\t"                               \
-        "tcgen05.mma.cta_group::2.kind::" KIND " [%1], a3, b3, %2, pt;\n\t"                               \
-        "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.b64 [%4];\n\t"                 \
-        "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.b64 [%5];\n\t"                 \
-        "selp.u32 %0, 1, 0, pr;\n\t}"                                                                     \
-        : "=r"(ready)                                                                                     \
-        : "r"(dacc), "r"(idesc), "r"(accumulate), "r"(empty_local), "r"(empty_peer), "r"(probe_bar),      \
-          "r"(probe_parity), "l"(adesc), "l"(bdesc)                                                       \
+        "{\n\t.reg .pred pe, pa, pt;\n\t.reg .b64 a1, a2, a3, b1, b2, b3;\n\t.reg .b16 both;\n\t"      \
+        "elect.sync _|pe, 0xffffffff;\n\t"                                                               \
+        "setp.ne.b32 pa, %2, 0;\n\t"                                                                     \
+        "setp.eq.b32 pt, %2, %2;\n\t"                                                                    \
+        "mov.b16 both, 3;\n\t"                                                                           \
+        "add.s64 a1, %4, 2;\n\tadd.s64 a2, %4, 4;\n\tadd.s64 a3, %4, 6;\n\t"                           \
+        "add.s64 b1, %5, 2;\n\tadd.s64 b2, %5, 4;\n\tadd.s64 b3, %5, 6;\n\t"                           \
+        "@pe tcgen05.mma.cta_group::2.kind::" KIND " [%0], %4, %5, %1, pa;\n\t"                          \
+        "@pe tcgen05.mma.cta_group::2.kind::" KIND " [%0], a1, b1, %1, pt;\n\t"                          \
+        "@pe tcgen05.mma.cta_group::2.kind::" KIND " [%0], a2, b2, %1, pt;\n\t"                          \
+        "@pe tcgen05.mma.cta_group::2.kind::" KIND " [%0], a3, b3, %1, pt;\n\t"                          \
+        "@pe tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%3], both;\n\t}" \
+        ::"r"(dacc), "r"(idesc), "r"(accumulate), "r"(empty), "l"(adesc), "l"(bdesc)                      \
         : "memory")
     if constexpr (INT) {
         GLOWQ_STAGE_MMA("i8");
@@ -179,7 +175,14 @@ __device__ __forceinline__ uint32_t i8_stage_mma(uint32_t dacc, uint64_t adesc, 
         GLOWQ_STAGE_MMA("f16");
     }
 #undef GLOWQ_STAGE_MMA
-    return ready;
+}
+// Arrive on the barrier at this offset in both CTAs of the pair once the MMAs issued so far complete (one lane).
+__device__ __forceinline__ void i8_commit_both(uint32_t bar) {
+    asm volatile(
+        "{\n\t.reg .pred pe;\n\t.reg .b16 both;\n\t"
+        "elect.sync _|pe, 0xffffffff;\n\tmov.b16 both, 3;\n\t"
+        "@pe tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], both;\n\t}" ::"r"(bar)
+        : "memory");
 }
 
 template <int BN>
@@ -208,7 +211,6 @@ __global__ void __launch_bounds__(kI8Threads, 1) int8_gemm_kernel(const __grid_c
     if (threadIdx.x == 0) {
         for (int s = 0; s < kStages; ++s) {
             mbar_init(&bars->full[s], 1);
-            mbar_init(&bars->ready[s], 2);
             mbar_init(&bars->empty[s], 1);
         }
         for (int b = 0; b < 2; ++b) {
@@ -228,126 +230,116 @@ __global__ void __launch_bounds__(kI8Threads, 1) int8_gemm_kernel(const __grid_c
     pdl_launch_dependents();
 
     if (warp == 0) {
-        // ---------------- producer (both CTAs) ----------------
-        if (lane == 0) {
-            bool ok = true;
-            int g = 0, early = 0;
-            auto at = [&](int g) { return smem_u32(sm + (g % kStages) * TL::kStageBytes); };
-            auto load_w = [&](const I8Unit& c, int i, int g) {
-                mbar_arrive_expect_tx(&bars->full[g % kStages], TL::kStageBytes);
-                tma_load_2d(at(g), &a.tmW[c.mi], &bars->full[g % kStages], (c.kb0 + i) * kI8Block, c.m0 + row_off);
-            };
-            auto room = [&]() {
-                if (g >= kStages && ok) ok = mbar_wait(&bars->empty[g % kStages], ((g / kStages) - 1) & 1, a.status);
-            };
-            i8_walk(
-                a, BN, pair,
-                [&](const I8Unit& c, int n) {
-                    if (n > 0) return;
-                    // the codes of W are static: the first of them are fetched before the
-                    // kernels that quantise X and compute R are known to be complete
-                    early = min(kStages, c.nkb);
-                    for (int i = 0; i < early; ++i) load_w(c, i, i);
-                    pdl_wait();
-                },
-                [&](const I8Unit& c, int n, int i) {
-                    if (g >= early) {
-                        room();
-                        load_w(c, i, g);
-                    }
-                    tma_load_2d(at(g) + kI8WBytes, &a.tmX, &bars->full[g % kStages], (c.kb0 + i) * kI8Block, c.n0 + tok_off);
-                    ++g;
-                },
-                [&](const I8Unit&, int) {},
-                [&](const I8Unit& c, int n, int j) {
+        // ---------------- producer (both CTAs, the whole warp) ----------------
+        bool ok = true;
+        int g = 0, s = 0, early = 0;                       // stages so far, ring stage, stages whose W is fetched ahead
+        uint32_t ph = 1;                                   // parity of empty[s] that frees the stage (the first use: free)
+        const uint32_t base = smem_u32(sm), empty0 = smem_u32(&bars->empty[0]), full0 = smem_u32(&bars->full[0]);
+        const uint32_t lead0 = cluster_addr(&bars->full[0], 0);
+        // stage `st` is free: announce both CTAs' bytes on the leader's barrier
+        auto announce = [&](int st) {
+            if (crank == 0) expect_tx_elect(full0 + 8u * (uint32_t)st, 2 * TL::kStageBytes);
+        };
+        auto load = [&](uint32_t off, const CUtensorMap* map, int st, int x, int y) {
+            tma_load_2d_pair(base + (uint32_t)(st * TL::kStageBytes) + off, map, lead0 + 8u * (uint32_t)st, x, y);
+        };
+        auto room = [&]() {
+            if (g >= kStages && ok) ok = mbar_wait_warp(empty0 + 8u * (uint32_t)s, ph, a.status);
+        };
+        auto advance = [&]() {
+            ++g;
+            if (++s == kStages) {
+                s = 0;
+                ph ^= 1u;
+            }
+        };
+        i8_walk(
+            a, BN, pair,
+            [&](const I8Unit& c, int n) {
+                if (n > 0) return;
+                // the codes of W are static: the first of them are fetched before the
+                // kernels that quantise X and compute R are known to be complete
+                early = min(kStages, c.nkb);
+                for (int i = 0; i < early; ++i) {
+                    announce(i);
+                    load(0, &a.tmW[c.mi], i, (c.kb0 + i) * kI8Block, c.m0 + row_off);
+                }
+                pdl_wait();
+            },
+            [&](const I8Unit& c, int n, int i) {
+                if (g >= early) {
                     room();
-                    mbar_arrive_expect_tx(&bars->full[g % kStages], TL::kStageBytes);
-                    tma_load_2d(at(g), &a.tmA[c.mi], &bars->full[g % kStages], j * 64, c.m0 + row_off);
-                    tma_load_2d(at(g) + kI8WBytes, &a.tmR, &bars->full[g % kStages], j * 64, c.n0 + tok_off);
-                    ++g;
-                });
-            // the leader's commits for the last stages land here before this CTA may exit
-            for (int p = (g > kStages ? g - kStages : 0); p < g && ok; ++p)
-                ok = mbar_wait(&bars->empty[p % kStages], (p / kStages) & 1, a.status);
-        }
-    } else if (warp == 2) {
-        // ---------------- forwarder (both CTAs): own bytes landed -> the leader's barrier ----------------
-        if (lane == 0) {
-            bool ok = true;
-            int g = 0;
-            pdl_wait();                                   // (bounded waits begin when the codes of X can come)
-            auto forward = [&]() {
-                if (ok) ok = mbar_wait(&bars->full[g % kStages], (g / kStages) & 1, a.status);
-                mbar_arrive_remote(cluster_addr(&bars->ready[g % kStages], 0));
-                ++g;
-            };
-            i8_walk(
-                a, BN, pair, [&](const I8Unit&, int) {}, [&](const I8Unit&, int, int) { forward(); },
-                [&](const I8Unit&, int) {}, [&](const I8Unit&, int, int) { forward(); });
-        }
+                    announce(s);
+                    load(0, &a.tmW[c.mi], s, (c.kb0 + i) * kI8Block, c.m0 + row_off);
+                }
+                load(kI8WBytes, &a.tmX, s, (c.kb0 + i) * kI8Block, c.n0 + tok_off);
+                advance();
+            },
+            [&](const I8Unit&, int) {},
+            [&](const I8Unit& c, int n, int j) {
+                room();
+                announce(s);
+                load(0, &a.tmA[c.mi], s, j * 64, c.m0 + row_off);
+                load(kI8WBytes, &a.tmR, s, j * 64, c.n0 + tok_off);
+                advance();
+            });
+        // the leader's commits for the last stages land here before this CTA may exit
+        for (int p = (g > kStages ? g - kStages : 0); p < g && ok; ++p)
+            ok = mbar_wait_warp(empty0 + 8u * (uint32_t)(p % kStages), (uint32_t)(p / kStages) & 1u, a.status);
     } else if (warp == 1) {
-        // ---------------- MMA issuer (leader CTA) ----------------
-        if (crank == 0 && lane == 0) {
+        // ---------------- MMA issuer (leader CTA, the whole warp) ----------------
+        if (crank == 0) {
             constexpr uint64_t kStageDesc = (uint64_t)(TL::kStageBytes >> 4);
             const uint64_t wdesc = sw128_kmajor_desc(smem_u32(sm));
             const uint64_t xdesc = sw128_kmajor_desc(smem_u32(sm) + kI8WBytes);
-            const uint32_t empty_l = smem_u32(&bars->empty[0]), empty_p = cluster_addr(&bars->empty[0], 1);
-            const uint32_t ready0 = smem_u32(&bars->ready[0]);
-            bool ok = true, next_ready = false;
-            int s = 0;
-            uint32_t ph = 0, convs[2] = {0, 0};
+            const uint32_t empty0 = smem_u32(&bars->empty[0]), full0 = smem_u32(&bars->full[0]);
+            bool ok = true;
+            int s = 0, units = 0;
+            uint32_t ph = 0, convs = 0;                    // convs: bit b: parity of conv[b]
             pdl_wait();
             auto stage = [&](auto integer, uint32_t acc, uint32_t accumulate) {
-                if (!next_ready && ok) ok = mbar_wait_cluster(&bars->ready[s], ph, a.status);
+                if (ok) ok = mbar_wait_warp(full0 + 8u * (uint32_t)s, ph, a.status);
                 tc_fence_after();
-                const int sn = (s + 1 == kStages) ? 0 : s + 1;
-                const uint32_t phn = (s + 1 == kStages) ? (ph ^ 1u) : ph;
                 constexpr bool kInt = decltype(integer)::value;
-                next_ready = i8_stage_mma<kInt>(acc, wdesc + (uint64_t)s * kStageDesc, xdesc + (uint64_t)s * kStageDesc,
-                                                kInt ? i8_idesc(2 * kI8Rows, BN) : f16_idesc(2 * kI8Rows, BN), accumulate,
-                                                empty_l + 8u * (uint32_t)s, empty_p + 8u * (uint32_t)s,
-                                                ready0 + 8u * (uint32_t)sn, phn) != 0;
-                s = sn;
-                ph = phn;
+                i8_stage_mma<kInt>(acc, wdesc + (uint64_t)s * kStageDesc, xdesc + (uint64_t)s * kStageDesc,
+                                   kInt ? i8_idesc(2 * kI8Rows, BN) : f16_idesc(2 * kI8Rows, BN), accumulate,
+                                   empty0 + 8u * (uint32_t)s);
+                if (++s == kStages) {
+                    s = 0;
+                    ph ^= 1u;
+                }
             };
-            int units = 0;
             i8_walk(
                 a, BN, pair,
                 [&](const I8Unit&, int n) {
-                    if (n >= 2 && ok) ok = mbar_wait_cluster(&bars->acc_empty[n & 1], ((n >> 1) - 1) & 1, a.status);
+                    if (n >= 2 && ok) ok = mbar_wait_warp(smem_u32(&bars->acc_empty[n & 1]), ((n >> 1) - 1) & 1, a.status);
                     tc_fence_after();
                     units = n + 1;
                 },
                 [&](const I8Unit&, int n, int i) {
                     stage(std::integral_constant<bool, true>{}, tmem + (uint32_t)((n & 1) * BN), i > 0 ? 1u : 0u);
                 },
-                [&](const I8Unit&, int n) {
-                    umma_commit_pair(smem_u32(&bars->acc_full[n & 1]));
-                    umma_commit_pair(cluster_addr(&bars->acc_full[n & 1], 1));
-                },
+                [&](const I8Unit&, int n) { i8_commit_both(smem_u32(&bars->acc_full[n & 1])); },
                 [&](const I8Unit& c, int n, int j) {
-                    const int b = n & 1;
+                    const uint32_t b = (uint32_t)(n & 1);
                     if (j == 0) {
-                        if (ok) ok = mbar_wait_cluster(&bars->conv[b], convs[b] & 1, a.status);
-                        ++convs[b];
+                        if (ok) ok = mbar_wait_warp(smem_u32(&bars->conv[b]), (convs >> b) & 1u, a.status);
+                        convs ^= 1u << b;
                     }
-                    stage(std::integral_constant<bool, false>{}, tmem + (uint32_t)(b * BN), 1u);
-                    if (j + 1 == c.nslab) {
-                        umma_commit_pair(smem_u32(&bars->slab_full[b]));
-                        umma_commit_pair(cluster_addr(&bars->slab_full[b], 1));
-                    }
+                    stage(std::integral_constant<bool, false>{}, tmem + b * BN, 1u);
+                    if (j + 1 == c.nslab) i8_commit_both(smem_u32(&bars->slab_full[b]));
                 });
             for (int n = (units > 2 ? units - 2 : 0); n < units && ok; ++n)
-                ok = mbar_wait_cluster(&bars->acc_empty[n & 1], (n >> 1) & 1, a.status);
+                ok = mbar_wait_warp(smem_u32(&bars->acc_empty[n & 1]), (n >> 1) & 1, a.status);
         }
-    } else if (warp >= 4) {
-        // ---------------- epilogue (warps 4..7, both CTAs), one thread per row ----------------
-        const int quarter = warp & 3, row = quarter * 32 + lane, et = threadIdx.x - 128;
+    } else {
+        // ---------------- epilogue (warps 2..5, both CTAs), one thread per row ----------------
+        const int quarter = warp & 3, row = quarter * 32 + lane, et = threadIdx.x - 64;
         const bool leader = et == 0;
         const uint32_t lanes = (uint32_t)(quarter * 32) << 16;
         bool ok = true;
         int chunk = 0;
-        uint32_t slabs[2] = {0, 0};
+        uint32_t slabs = 0;                               // bit b: parity of slab_full[b]
         pdl_wait();                                       // the token scales are complete
         i8_walk(
             a, BN, pair, [&](const I8Unit&, int) {}, [&](const I8Unit&, int, int) {},
@@ -389,8 +381,8 @@ __global__ void __launch_bounds__(kI8Threads, 1) int8_gemm_kernel(const __grid_c
                         tc_fence_before();
                         __syncwarp();
                         if (lane == 0) mbar_arrive_remote(cluster_addr(&bars->conv[buf], 0));
-                        if (ok) ok = mbar_wait(&bars->slab_full[buf], slabs[buf] & 1, a.status);
-                        ++slabs[buf];
+                        if (ok) ok = mbar_wait(&bars->slab_full[buf], (slabs >> buf) & 1, a.status);
+                        slabs ^= 1u << buf;
                         tc_fence_after();
                     }
 #pragma unroll 1
@@ -435,9 +427,139 @@ __global__ void __launch_bounds__(kI8Threads, 1) int8_gemm_kernel(const __grid_c
 }
 
 // ---------------------------------------------------------------------------
-// Split tiles: one block per 128 rows x 32 tokens of a tile.  A warp has 16
-// rows: lane (g, t) the rows g and g + 8 of tokens 2 t, 2 t + 1 of each 8.
+// R = X B^T ahead of the product: a cluster of eight blocks takes 128 tokens,
+// block c the c-th eighth of d (tcgen05, M = 128 tokens, N = r, both operands by
+// TMA, fp32 in TMEM).  The eight parts meet in distributed shared memory: block
+// c adds the parts of tokens 16 c .. + 15 in block order and rounds R to fp16.
 // ---------------------------------------------------------------------------
+constexpr int kProjParts = 8, kProjThreads = 192, kProjStages = 8;
+
+struct I8ProjArgs {
+    CUtensorMap tmX;      // X [T][d] fp16, box {64, 128}, SW128
+    CUtensorMap tmB;      // B [r][d] fp16, box {64, rn}, SW128
+    __half* R;
+    int d, T, r, rn, stages;
+    unsigned int* status;
+};
+__host__ __device__ inline int proj_stage_bytes(int rn) { return 128 * 128 + rn * 128; }
+__host__ __device__ inline int proj_pitch(int rn) { return rn + 4; }     // floats
+static size_t proj_ring_bytes(int rn, int stages) {
+    const size_t ring = (size_t)stages * proj_stage_bytes(rn), sums = (size_t)128 * proj_pitch(rn) * 4;
+    return ((ring > sums ? ring : sums) + 1023) / 1024 * 1024;
+}
+
+__global__ void __launch_bounds__(kProjThreads, 1) int8_project_kernel(const __grid_constant__ I8ProjArgs a, uint32_t ring_bytes) {
+    extern __shared__ __align__(1024) unsigned char raw[];
+    unsigned char* sm = reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~uintptr_t(1023));
+    struct Bars {
+        uint64_t full[kProjStages], empty[kProjStages], acc;
+        uint32_t tmem;
+    };
+    Bars* bars = reinterpret_cast<Bars*>(sm + ring_bytes);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const uint32_t part = cluster_ctarank();
+    const int t0 = (int)(blockIdx.x / kProjParts) * 128;
+    const int nkb = a.d / 64, kb0 = (int)part * nkb / kProjParts, n = (int)(part + 1) * nkb / kProjParts - kb0;
+    const int sbytes = proj_stage_bytes(a.rn);
+    uint32_t ncols = 32;
+    while (ncols < (uint32_t)a.rn) ncols <<= 1;
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < a.stages; ++s) {
+            mbar_init(&bars->full[s], 1);
+            mbar_init(&bars->empty[s], 1);
+        }
+        mbar_init(&bars->acc, 1);
+        fence_mbar_init();
+    }
+    if (warp == 1) tmem_alloc(&bars->tmem, ncols);
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = bars->tmem;
+    pdl_wait();                 // X may be produced by the preceding kernel; the previous call's readers of R are done
+    pdl_launch_dependents();
+    if (warp == 0) {
+        bool ok = true;
+        for (int i = 0; i < n; ++i) {
+            const int s = i % a.stages;
+            if (i >= a.stages && ok) ok = mbar_wait_warp(smem_u32(&bars->empty[s]), (uint32_t)(i / a.stages - 1) & 1u, a.status);
+            const uint32_t full = smem_u32(&bars->full[s]), dst = smem_u32(sm) + (uint32_t)(s * sbytes);
+            expect_tx_elect(full, (uint32_t)sbytes);
+            tma_load_2d_elect(dst, &a.tmX, full, (kb0 + i) * 64, t0);
+            tma_load_2d_elect(dst + 128 * 128, &a.tmB, full, (kb0 + i) * 64, 0);
+        }
+    } else if (warp == 1) {
+        const uint32_t idesc = f16_idesc(128, a.rn);
+        bool ok = true;
+        for (int i = 0; i < n; ++i) {
+            const int s = i % a.stages;
+            if (ok) ok = mbar_wait_warp(smem_u32(&bars->full[s]), (uint32_t)(i / a.stages) & 1u, a.status);
+            tc_fence_after();
+            const uint64_t ad = sw128_kmajor_desc(smem_u32(sm) + (uint32_t)(s * sbytes));
+            umma_f16_stage_elect(tmem, ad, ad + (uint64_t)(128 * 128 / 16), idesc, i > 0 ? 1u : 0u, smem_u32(&bars->empty[s]));
+        }
+        umma_commit_elect(smem_u32(&bars->acc));
+    }
+    // the part's sums over the ring (its loads and products are complete): [128 tokens][pitch]
+    const int pitch = proj_pitch(a.rn);
+    float* sums = reinterpret_cast<float*>(sm);
+    if (warp >= 2) {
+        const int quarter = warp & 3, row = quarter * 32 + lane;
+        mbar_wait(&bars->acc, 0, a.status);
+        tc_fence_after();
+        for (int c = 0; c < a.rn; c += 32) {
+            uint32_t v[32];
+            if (n > 0) {
+                tmem_ld32(tmem + ((uint32_t)(quarter * 32) << 16) + (uint32_t)c, v);
+            } else {
+#pragma unroll
+                for (int j = 0; j < 32; ++j) v[j] = 0u;
+            }
+#pragma unroll
+            for (int j = 0; j < 32; j += 4)
+                if (c + j < a.rn)
+                    *reinterpret_cast<uint4*>(sums + row * pitch + c + j) = make_uint4(v[j], v[j + 1], v[j + 2], v[j + 3]);
+        }
+    }
+    tc_fence_before();
+    __syncwarp();
+    cluster_sync_all();
+    const int q4 = a.r / 4;
+    for (int i = threadIdx.x; i < 16 * q4; i += kProjThreads) {
+        const int row = (int)part * 16 + i / q4, c = i % q4 * 4;
+        float4 p[kProjParts];
+#pragma unroll
+        for (int k = 0; k < kProjParts; ++k) {
+            const uint32_t at = cluster_addr(sums + row * pitch + c, (uint32_t)k);
+            asm volatile("ld.shared::cluster.v4.f32 {%0,%1,%2,%3}, [%4];"
+                         : "=f"(p[k].x), "=f"(p[k].y), "=f"(p[k].z), "=f"(p[k].w)
+                         : "r"(at)
+                         : "memory");
+        }
+        float4 v = p[0];
+#pragma unroll
+        for (int k = 1; k < kProjParts; ++k) v.x += p[k].x, v.y += p[k].y, v.z += p[k].z, v.w += p[k].w;
+        if (t0 + row < a.T) {
+            uint2 o;
+            o.x = h2_as_u32(__floats2half2_rn(v.x, v.y));
+            o.y = h2_as_u32(__floats2half2_rn(v.z, v.w));
+            *reinterpret_cast<uint2*>(a.R + (int64_t)(t0 + row) * a.r + c) = o;
+        }
+    }
+    __syncwarp();
+    cluster_sync_all();          // no block's shared memory is read any more
+    tc_fence_after();
+    if (warp == 1) tmem_dealloc(tmem, ncols);
+}
+
+// ---------------------------------------------------------------------------
+// Split tiles: one block per 128 rows x 32 tokens of a tile, a warp per 32
+// rows.  Lane (g, t) has the rows 4 g .. 4 g + 3 (they are rows g and g + 8 of
+// the MMA's two row tiles) of tokens 2 t, 2 t + 1 of each 8, so sums come 16
+// bytes and outputs go 8 bytes at a time.
+// ---------------------------------------------------------------------------
+constexpr int kJoinThreads = 128;
+
 struct I8JoinModule {
     const float* s;
     const __half* A;
@@ -454,7 +576,7 @@ struct I8JoinArgs {
     int m, T, r, bn, ntiles_n;
 };
 
-__global__ void __launch_bounds__(256) int8_join_kernel(const __grid_constant__ I8JoinArgs a) {
+__global__ void __launch_bounds__(kJoinThreads) int8_join_kernel(const __grid_constant__ I8JoinArgs a) {
     pdl_launch_dependents();
     const int chunks = a.bn / 32;
     const int ch = blockIdx.x % chunks, half = (blockIdx.x / chunks) & 1, rel = blockIdx.x / chunks / 2;
@@ -465,82 +587,116 @@ __global__ void __launch_bounds__(256) int8_join_kernel(const __grid_constant__ 
         if (mt >= a.mod[i].mtile_begin) mi = i;
     const I8JoinModule& md = a.mod[mi];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
-    const int wrow = warp * 16, row0 = (mt - md.mtile_begin) * 2 * kI8Rows + half * kI8Rows + wrow;
+    const int trow = warp * 32 + 4 * g;                   // this lane's first row within the CTA's 128
+    const int row = (mt - md.mtile_begin) * 2 * kI8Rows + half * kI8Rows + trow;
     const int t0 = nt * a.bn + ch * 32;
-    if (t0 >= a.T || row0 >= md.O) {                      // (O % 16 == 0: a warp's rows are all there or none)
-        pdl_wait();
-        return;
-    }
     // A and the scales are static; R, the sums and the token scales come from the preceding kernels
-    const float s0 = __ldg(md.s + row0 + g), s1 = __ldg(md.s + row0 + g + 8);
-    const bool corrects = a.r > 0 && md.A;
-    uint4 af[4] = {};
+    const bool there = row < md.O, corrects = a.r > 0 && md.A;      // (O % 16 == 0: four rows are there or none)
+    float4 so = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (there) so = make_float4(__ldg(md.s + row), __ldg(md.s + row + 1), __ldg(md.s + row + 2), __ldg(md.s + row + 3));
+    uint4 af[4][2];
     auto load_a = [&](int j0) {
-        const __half* A = md.A + (int64_t)(row0 + g) * a.r + j0 + 16 * t;
 #pragma unroll
-        for (int p = 0; p < 2; ++p) {
-            af[p] = af[2 + p] = make_uint4(0, 0, 0, 0);
-            if (j0 + 16 * t + 8 * p < a.r) {
-                af[p] = ldg_128(A + 8 * p);
-                af[2 + p] = ldg_128(A + 8 * p + (int64_t)8 * a.r);
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+            for (int p = 0; p < 2; ++p) {
+                const int j = j0 + 16 * t + 8 * p;
+                af[i][p] = make_uint4(0, 0, 0, 0);
+                if (there && j < a.r) af[i][p] = ldg_128(md.A + (int64_t)(row + i) * a.r + j);
             }
-        }
     };
     if (corrects) load_a(0);
     pdl_wait();
-    // the segments that hold the tile's k-blocks [rel nkb, (rel + 1) nkb): pairs p0 .. p1
-    const int64_t lo = (int64_t)rel * a.split.nkb, hi = lo + a.split.nkb;
-    int p = (int)(lo * a.split.pairs / a.split.blocks);
+    if (t0 >= a.T) return;
+    // the segments that hold the tile's k-blocks [rel nkb, (rel + 1) nkb): those of pairs p0 .. p1
+    const int nkb = a.split.nkb, lo = rel * nkb, hi = lo + nkb;
+    int p = lo * a.split.pairs / a.split.blocks;
     while (i8_share(a.split, p + 1) <= lo) ++p;
     while (i8_share(a.split, p) > lo) --p;
-    int v[4][4] = {};
-    for (; p < a.split.pairs && i8_share(a.split, p) < hi; ++p) {
-        const int64_t begin = i8_share(a.split, p);
-        if (begin == i8_share(a.split, p + 1)) continue;  // no share (fewer blocks than pairs)
-        const int seg = (int)(rel - begin / a.split.nkb); // the pair's segments are one per tile, in order
+    // R of the first 64 columns and the token scales, in flight beside the sums
+    uint4 rx[4][2];
+    auto load_r = [&](int j0) {
+#pragma unroll
+        for (int n = 0; n < 4; ++n)
+#pragma unroll
+            for (int q = 0; q < 2; ++q) {
+                const int tok = t0 + n * 8 + g, j = j0 + 16 * t + 8 * q;
+                rx[n][q] = make_uint4(0, 0, 0, 0);
+                if (tok < a.T && j < a.r) rx[n][q] = ldcg_128(a.R + (int64_t)tok * a.r + j);
+            }
+    };
+    if (corrects) load_r(0);
+    float st[4][2];
+#pragma unroll
+    for (int n = 0; n < 4; ++n)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+            const int tok = t0 + n * 8 + 2 * t + e;
+            st[n][e] = tok < a.T ? ldcg_f32(a.xs + tok) : 0.f;
+        }
+    int v[4][2][4] = {};
+    for (int begin = i8_share(a.split, p), end; p < a.split.pairs && begin < hi; ++p, begin = end) {
+        end = i8_share(a.split, p + 1);
+        if (begin == end) continue;                       // no share (fewer blocks than pairs)
+        const int seg = rel - begin / nkb;                // the pair's segments are one per tile, in order
         const int* src = a.slots + (((int64_t)p * a.split.segments + seg) * 2 + half) * ((int64_t)a.bn * kI8Rows) +
-                         (int64_t)ch * 32 * kI8Rows + wrow + g;
+                         (int64_t)ch * 32 * kI8Rows + trow;
+        int4 x[4][2];
 #pragma unroll
         for (int n = 0; n < 4; ++n)
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
                 const int tok = n * 8 + 2 * t + e;
-                if (t0 + tok < a.T) {
-                    v[n][e] += __ldcg(src + tok * kI8Rows);
-                    v[n][2 + e] += __ldcg(src + tok * kI8Rows + 8);
-                }
+                x[n][e] = make_int4(0, 0, 0, 0);
+                if (t0 + tok < a.T) x[n][e] = __ldcg(reinterpret_cast<const int4*>(src + tok * kI8Rows));
+            }
+#pragma unroll
+        for (int n = 0; n < 4; ++n)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                v[n][e][0] += x[n][e].x;
+                v[n][e][1] += x[n][e].y;
+                v[n][e][2] += x[n][e].z;
+                v[n][e][3] += x[n][e].w;
             }
     }
-    float c[4][4] = {};
+    float c[2][4][4] = {};
     if (corrects) {
         for (int j0 = 0; j0 < a.r; j0 += 64) {
-            if (j0 > 0) load_a(j0);
+            if (j0 > 0) {
+                load_a(j0);
+                load_r(j0);
+            }
 #pragma unroll
             for (int n = 0; n < 4; ++n) {
-                const int tok = t0 + n * 8 + g;
+                const uint4(&x)[2] = rx[n];
 #pragma unroll
-                for (int q = 0; q < 2; ++q) {
-                    const int j = j0 + 16 * t + 8 * q;
-                    uint4 x = make_uint4(0, 0, 0, 0);
-                    if (tok < a.T && j < a.r) x = ldcg_128(a.R + (int64_t)tok * a.r + j);
-                    const uint32_t a1[4] = {af[q].x, af[2 + q].x, af[q].y, af[2 + q].y}, b1[2] = {x.x, x.y};
-                    const uint32_t a2[4] = {af[q].z, af[2 + q].z, af[q].w, af[2 + q].w}, b2[2] = {x.z, x.w};
-                    mma_16816(c[n], a1, b1);
-                    mma_16816(c[n], a2, b2);
-                }
+                for (int q = 0; q < 2; ++q)
+#pragma unroll
+                    for (int w = 0; w < 2; ++w) {         // row tiles: rows 4 g, 4 g + 1 and 4 g + 2, 4 g + 3
+                        const uint4 &u = af[2 * w][q], &l = af[2 * w + 1][q];
+                        const uint32_t a1[4] = {u.x, l.x, u.y, l.y}, b1[2] = {x[q].x, x[q].y};
+                        const uint32_t a2[4] = {u.z, l.z, u.w, l.w}, b2[2] = {x[q].z, x[q].w};
+                        mma_16816(c[w][n], a1, b1);
+                        mma_16816(c[w][n], a2, b2);
+                    }
             }
         }
     }
+    if (!there) return;
 #pragma unroll
     for (int n = 0; n < 4; ++n)
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
             const int tok = t0 + n * 8 + 2 * t + e;
             if (tok < a.T) {
-                const float st = ldcg_f32(a.xs + tok);
-                __half* y = md.Y + (int64_t)tok * md.ldY + row0 + g;
-                y[0] = __float2half_rn(fmaf((float)v[n][e] * st, s0, c[n][e]));
-                y[8] = __float2half_rn(fmaf((float)v[n][2 + e] * st, s1, c[n][2 + e]));
+                const float s = st[n][e];
+                uint2 y;
+                y.x = h2_as_u32(__floats2half2_rn(fmaf((float)v[n][e][0] * s, so.x, c[0][n][e]),
+                                                  fmaf((float)v[n][e][1] * s, so.y, c[0][n][2 + e])));
+                y.y = h2_as_u32(__floats2half2_rn(fmaf((float)v[n][e][2] * s, so.z, c[1][n][e]),
+                                                  fmaf((float)v[n][e][3] * s, so.w, c[1][n][2 + e])));
+                *reinterpret_cast<uint2*>(md.Y + (int64_t)tok * md.ldY + row) = y;
             }
         }
 }
@@ -548,6 +704,45 @@ __global__ void __launch_bounds__(256) int8_join_kernel(const __grid_constant__ 
 // ---------------------------------------------------------------------------
 // Host side
 // ---------------------------------------------------------------------------
+cudaError_t launch_int8_project(const uint16_t* X, const uint16_t* B, int64_t T, int d, int r, uint16_t* R,
+                                cudaStream_t st) {
+    I8ProjArgs a;
+    std::memset(&a, 0, sizeof(a));
+    a.rn = (r + 15) / 16 * 16;
+    if (!make_map(&a.tmX, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, X, (uint64_t)d, (uint64_t)T, (uint64_t)d * 2, 64, 128,
+                  CU_TENSOR_MAP_SWIZZLE_128B) ||
+        !make_map(&a.tmB, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, B, (uint64_t)d, (uint64_t)r, (uint64_t)d * 2, 64, (uint32_t)a.rn,
+                  CU_TENSOR_MAP_SWIZZLE_128B))
+        return cudaErrorInvalidValue;
+    a.R = reinterpret_cast<__half*>(R);
+    a.d = d;
+    a.T = (int)T;
+    a.r = r;
+    a.status = device_status_ptr();
+    const int most = 200 * 1024 / proj_stage_bytes(a.rn);        // 4 at r = 256
+    a.stages = most > kProjStages ? kProjStages : most;
+    uint32_t ring = (uint32_t)proj_ring_bytes(a.rn, a.stages);
+    cudaError_t e = cudaFuncSetAttribute((const void*)int8_project_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                         kI8SmemMax);
+    if (e != cudaSuccess) return e;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)((T + 127) / 128 * kProjParts));
+    cfg.blockDim = dim3(kProjThreads);
+    cfg.dynamicSmemBytes = ring + 1024 + 256;
+    cfg.stream = st;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = kProjParts;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[1].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 2;
+    void* args[] = {(void*)&a, (void*)&ring};
+    return cudaLaunchKernelExC(&cfg, (const void*)int8_project_kernel, args);
+}
+
 // Token width: the fewest token tiles, then the narrowest that holds T in them.
 // Whole rounds of tiles for every pair, and the rest split, unless a last round
 // of whole tiles ends sooner: in clocks, a k-block 600, a split the stores of
@@ -572,8 +767,8 @@ I8GemmPlan plan_int8_gemm(int64_t T, int64_t d, int64_t mtiles, int num_sms) {
     }
     p.split.rounds = (int)rounds;
     p.split.nkb = (int)nkb;
-    p.split.blocks = rest * nkb;
-    p.split.segments = (int)((p.split.blocks + pairs - 1) / pairs / nkb + 2);
+    p.split.blocks = (int)(rest * nkb);
+    p.split.segments = (int)((rest * nkb + pairs - 1) / pairs / nkb + 2);
     p.rest = rest;
     p.slot_bytes = rest > 0 ? (size_t)pairs * p.split.segments * 2 * kI8Rows * p.bn * 4 : 0;
     return p;
@@ -656,7 +851,8 @@ cudaError_t launch_int8_gemm(const Int8ModuleView* mods, int m, int d, int64_t T
     j.bn = p.bn;
     j.ntiles_n = a.ntiles_n;
     void* args[] = {(void*)&j};
-    return launch_pdl((const void*)int8_join_kernel, (unsigned)(p.rest * 2 * (p.bn / 32)), 256, 0, st, args);
+    return launch_pdl((const void*)int8_join_kernel, (unsigned)(p.rest * 2 * (p.bn / 32)), kJoinThreads, 0, st,
+                      args);
 }
 
 }  // namespace glowq

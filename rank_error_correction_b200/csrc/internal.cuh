@@ -91,10 +91,11 @@ constexpr int64_t kInt8MaxD = 131072;          // 127^2 d < 2^31
 constexpr int kInt8SmallTokens = 16;           // tokens up to which the weight-streaming product runs
 constexpr int kInt8ZeroBytes = 65536;          // tickets at the workspace's start
 constexpr int kInt8MaxTickets = kInt8ZeroBytes / 4;
-// Decomposition of the small-T product: S CTAs share a tile's k, wk warps of a CTA.
+// Decomposition of the small-T product: S blocks share a tile's k.
 struct Int8GemvPlan {
     bool ok;             // false: the shape is left to the tensor-core GEMM
-    int S, wk, grid, smem;
+    bool self;           // the product quantises X by itself
+    int S, grid, smem;
     size_t slot_bytes;   // partial sums (S > 1)
 };
 int int8_small_tokens(int64_t T);
@@ -103,18 +104,24 @@ cudaError_t launch_pack_int8(const float* W, int64_t O, int64_t d, int8_t* codes
 cudaError_t launch_dequant_int8(const int8_t* codes, const float* scales, int64_t O, int64_t d, uint16_t* out,
                                 cudaStream_t st);
 cudaError_t launch_quantize_act_int8(const uint16_t* X, int64_t T, int64_t d, int8_t* codes, float* scales,
-                                     cudaStream_t st, bool beside = false);
+                                     cudaStream_t st);
 cudaError_t launch_int8_small(const Int8ModuleView* mods, int m, int d, int T, int r, const uint16_t* X,
                               const uint16_t* B, uint16_t* R, int8_t* xq, float* xs, unsigned int* tickets, int* slots,
                               const Int8GemvPlan& p, cudaStream_t st);
+// The token quantiser behind a kernel of the same call that has waited for X: its end implies that kernel's.
+cudaError_t launch_quantize_beside(const uint16_t* X, int64_t T, int64_t d, int8_t* codes, float* scales,
+                                   cudaStream_t st);
 // int8_gemm.cu: T > 16 on the tensor cores.  `rounds` whole tiles per pair
 // (tiles [0, whole)), then the other tiles' k-blocks as one run of `blocks` cut
 // evenly among the pairs; a pair's share has at most `segments` tiles' segments.
 struct I8Split {
     int pairs, rounds, nkb, segments;
-    int64_t whole, blocks;
+    int64_t whole;
+    int blocks;          // below pairs nkb, so that blocks x pairs fits an int
 };
-__host__ __device__ inline int64_t i8_share(const I8Split& s, int pair) { return s.blocks * pair / s.pairs; }
+__host__ __device__ inline int i8_share(const I8Split& s, int pair) {
+    return (int)((unsigned)s.blocks * (unsigned)pair / (unsigned)s.pairs);
+}
 struct I8GemmPlan {
     int bn;              // tokens per pair tile
     I8Split split;
@@ -122,12 +129,10 @@ struct I8GemmPlan {
     size_t slot_bytes;   // their partial sums
 };
 I8GemmPlan plan_int8_gemm(int64_t T, int64_t d, int64_t mtiles, int num_sms);
+cudaError_t launch_int8_project(const uint16_t* X, const uint16_t* B, int64_t T, int d, int r, uint16_t* R,
+                                cudaStream_t st);
 cudaError_t launch_int8_gemm(const Int8ModuleView* mods, int m, int d, int64_t T, int r, const int8_t* xq,
                              const float* xs, const uint16_t* R, int* slots, const I8GemmPlan& p, cudaStream_t st);
-// prefill.cu: R = X B^T on the tensor cores (scratch of prefill_partial_bytes(T, r))
-cudaError_t launch_rproj_prefill(const uint16_t* X, const uint16_t* B, int64_t T, int d, int r, uint16_t* R,
-                                 float* partial, int num_sms, cudaStream_t st, const float* tok_scale,
-                                 uint16_t* R_scaled);
 // solve.cu: the offline group solve (float64)
 struct SolveModule {
     const float* W;      // O x d fp32 weights

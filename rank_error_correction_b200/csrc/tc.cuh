@@ -161,6 +161,69 @@ __device__ __forceinline__ void umma_commit_pair(uint32_t caddr) {
     asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(caddr)
                  : "memory");
 }
+// The same from a loop that a whole warp runs: one lane issues, the operands stay warp-uniform.
+__device__ __forceinline__ void expect_tx_elect(uint32_t bar, uint32_t bytes) {
+    asm volatile(
+        "{\n\t.reg .pred pe;\n\telect.sync _|pe, 0xffffffff;\n\t"
+        "@pe mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;\n\t}" ::"r"(bar), "r"(bytes)
+        : "memory");
+}
+__device__ __forceinline__ void tma_load_2d_elect(uint32_t dst, const void* map, uint32_t bar, int x, int y) {
+    asm volatile(
+        "{\n\t.reg .pred pe;\n\telect.sync _|pe, 0xffffffff;\n\t"
+        "@pe cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];\n\t}"
+        ::"r"(dst), "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(bar)
+        : "memory");
+}
+// The four K = 16 products of a 128-byte stage on one CTA, and the commit that frees it.
+__device__ __forceinline__ void umma_f16_stage_elect(uint32_t dacc, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
+                                                     uint32_t accumulate, uint32_t empty) {
+    asm volatile(
+        "{\n\t.reg .pred pe, pa, pt;\n\t.reg .b64 a1, a2, a3, b1, b2, b3;\n\t"
+        "elect.sync _|pe, 0xffffffff;\n\t"
+        "setp.ne.b32 pa, %2, 0;\n\tsetp.eq.b32 pt, %2, %2;\n\t"
+        "add.s64 a1, %4, 2;\n\tadd.s64 a2, %4, 4;\n\tadd.s64 a3, %4, 6;\n\t"
+        "add.s64 b1, %5, 2;\n\tadd.s64 b2, %5, 4;\n\tadd.s64 b3, %5, 6;\n\t"
+        "@pe tcgen05.mma.cta_group::1.kind::f16 [%0], %4, %5, %1, pa;\n\t"
+        "@pe tcgen05.mma.cta_group::1.kind::f16 [%0], a1, b1, %1, pt;\n\t"
+        "@pe tcgen05.mma.cta_group::1.kind::f16 [%0], a2, b2, %1, pt;\n\t"
+        "@pe tcgen05.mma.cta_group::1.kind::f16 [%0], a3, b3, %1, pt;\n\t"
+        "@pe tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%3];\n\t}"
+        ::"r"(dacc), "r"(idesc), "r"(accumulate), "r"(empty), "l"(adesc), "l"(bdesc)
+        : "memory");
+}
+__device__ __forceinline__ void umma_commit_elect(uint32_t bar) {
+    asm volatile(
+        "{\n\t.reg .pred pe;\n\telect.sync _|pe, 0xffffffff;\n\t"
+        "@pe tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(bar)
+        : "memory");
+}
+// 2-D tiled TMA load into this CTA's shared memory that completes on a barrier
+// of either CTA of the pair (`cbar`: its cluster address).
+__device__ __forceinline__ void tma_load_2d_pair(uint32_t dst, const void* map, uint32_t cbar, int x, int y) {
+    asm volatile(
+        "{\n\t.reg .pred pe;\n\telect.sync _|pe, 0xffffffff;\n\t"
+        "@pe cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+        " [%0], [%1, {%2, %3}], [%4];\n\t}" ::"r"(dst), "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(cbar)
+        : "memory");
+}
+// Bounded wait by a whole warp, with control flow that stays uniform (see the MMA issuers).
+__device__ __forceinline__ bool mbar_wait_warp(uint32_t bar, uint32_t parity, unsigned int* status,
+                                               uint32_t limit = (1u << 20)) {
+    for (uint32_t it = 0; it < limit; ++it) {
+        uint32_t done;
+        asm volatile(
+            "{\n\t.reg .pred p;\n\t"
+            "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+            "selp.u32 %0, 1, 0, p;\n\t}"
+            : "=r"(done)
+            : "r"(bar), "r"(parity)
+            : "memory");
+        if (__all_sync(~0u, done != 0)) return true;
+    }
+    record_status(status, GLOWQ_ERR_TIMEOUT);
+    return false;
+}
 __device__ __forceinline__ void tmem_alloc_pair(uint32_t* dst_smem, uint32_t ncols) {
     asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(dst_smem)),
                  "r"(ncols)
