@@ -27,7 +27,7 @@ NVCC_FLAGS = ["-O3", "-lineinfo", "-std=c++17", "--expt-relaxed-constexpr", "-Xc
               "-Xcompiler", "-fvisibility=hidden", f"-I{INCLUDE}", f"-I{CSRC}"]
 SOURCES = ["api.cu", "pack.cu", "fp4.cu", "decode.cu", "prefill.cu", "solve.cu", "noalloc.cu", "int8.cu", "int8_gemm.cu", "kvcache.cu", "attention.cu",
            "select.cpp"]
-HEADERS = ["common.cuh", "internal.cuh", "kvcache.cuh", "tc.cuh"]
+HEADERS = ["common.cuh", "internal.cuh", "kvcache.cuh", "quant8.cuh", "tc.cuh"]
 
 
 def nvcc() -> str:

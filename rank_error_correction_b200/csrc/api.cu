@@ -248,9 +248,9 @@ static glowq_status w8a8_impl(const glowq_int8_module* mods, int32_t m, int64_t 
     } else {
         if (!encode_fn()) return GLOWQ_ERR_CUDA;
         if (r > 0) e = launch_int8_project(X, B, T, (int)d, r, R, st);
+        if (e == cudaSuccess) e = launch_quantize_beside(X, T, d, codes, scales, tickets + kInt8Ready, r == 0, st);
         if (e == cudaSuccess)
-            e = r > 0 ? launch_quantize_beside(X, T, d, codes, scales, st) : launch_quantize_act_int8(X, T, d, codes, scales, st);
-        if (e == cudaSuccess) e = launch_int8_gemm(hm, m, (int)d, T, r, codes, scales, R, slots, L.gemm, st);
+            e = launch_int8_gemm(hm, m, (int)d, T, r, codes, scales, R, tickets, slots, L.gemm, st);
     }
     return e == cudaSuccess ? GLOWQ_OK : GLOWQ_ERR_CUDA;
 }

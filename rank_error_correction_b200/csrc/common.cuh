@@ -183,6 +183,22 @@ __device__ __forceinline__ void fence_proxy_async_smem() {
     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
 }
 
+// Until *f >= target, or until the grids that this one depends on, which count
+// on it, are complete: that takes longer to be known, so the count is polled a
+// while (some 10 ms) first.
+__device__ __forceinline__ void wait_ready(const unsigned int* f, unsigned int target) {
+    for (uint32_t it = 0; it < (1u << 14); ++it) {
+        if (flag_acquire_load(f) >= target) return;
+        if (it >= 64) __nanosleep(64);
+    }
+    pdl_wait();
+}
+// Order what this thread has acquired from other kernels' generic-proxy writes
+// before its later async-proxy (bulk, TMA) reads of them.
+__device__ __forceinline__ void fence_proxy_async_all() {
+    asm volatile("fence.proxy.async;" ::: "memory");
+}
+
 // ---- half2 packing -------------------------------------------------------
 __device__ __forceinline__ uint32_t h2_as_u32(__half2 h) {
     return *reinterpret_cast<uint32_t*>(&h);

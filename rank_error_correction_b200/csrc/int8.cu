@@ -12,6 +12,7 @@
 
 #include "common.cuh"
 #include "internal.cuh"
+#include "quant8.cuh"
 
 namespace glowq {
 
@@ -33,22 +34,6 @@ __device__ __forceinline__ int int8_code(float x, float s) {
 __device__ __forceinline__ uint32_t int8_pack4(float a, float b, float c, float d, float s) {
     return (uint32_t)(int8_code(a, s) & 255) | ((uint32_t)(int8_code(b, s) & 255) << 8) |
            ((uint32_t)(int8_code(c, s) & 255) << 16) | ((uint32_t)(int8_code(d, s) & 255) << 24);
-}
-// The same code from p = x * fp32(1 / s), and without a division unless p is
-// within 1e-4 of a half-integer: |p| < 128 and p is off the quotient by 2^-22
-// relative at most (3.1e-5), so elsewhere both round to the same integer.  (An
-// IEEE division per element made the quantiser ALU-bound: 12 us instead of 5
-// at T = 2048, d = 4096.)  Adding 1.5 2^23 rounds to even and leaves the
-// integer in the low bits.  s >= 2^-24 / 127, as for fp16 rows.
-__device__ __forceinline__ uint32_t int8_code_fast(float x, float s, float inv) {
-    const float p = x * inv, m = p + 12582912.f;
-    if (fabsf(fabsf(p - (m - 12582912.f)) - 0.5f) < 1e-4f) return (uint32_t)int8_code(x, s);
-    return __float_as_uint(m);
-}
-__device__ __forceinline__ uint32_t int8_pack4_fast(float a, float b, float c, float d, float s, float inv) {
-    const uint32_t lo = __byte_perm(int8_code_fast(a, s, inv), int8_code_fast(b, s, inv), 0x0040);
-    const uint32_t hi = __byte_perm(int8_code_fast(c, s, inv), int8_code_fast(d, s, inv), 0x0040);
-    return __byte_perm(lo, hi, 0x5410);
 }
 // Maximum of |x| and whether every x is finite, over the block; the result in every thread.
 __device__ __forceinline__ void block_amax(float& amax, bool& finite) {
@@ -101,80 +86,88 @@ __global__ void __launch_bounds__(256) dequant_int8_kernel(const int8_t* __restr
     for (int64_t k = threadIdx.x; k < d; k += 256) out[o * d + k] = __float2half_rn((float)codes[o * d + k] * s);
 }
 
-// Quantises token `t` of X by the whole block; codes4(i, v) receives the codes
-// of elements 4 i .. 4 i + 3.  d % 8 == 0, rows 16-byte aligned.
+// Quantises token `t` of X by the whole block; store(i, v) receives the codes
+// of elements 8 i .. 8 i + 7.  d % 8 == 0, rows 16-byte aligned.
 template <class Store>
 __device__ __forceinline__ void quantize_token(const uint16_t* __restrict__ X, int64_t t, int64_t d,
-                                               float* __restrict__ scales, Store codes8) {
+                                               float* __restrict__ scales, Store store) {
     const uint4* x = reinterpret_cast<const uint4*>(X + t * d);
     const int n8 = (int)(d / 8);
     constexpr int kKeep = 4;                 // the first 8 kKeep 256 elements of a row stay in registers
     uint4 keep[kKeep];
-    float amax = 0.f;
-    bool finite = true;
-    auto see = [&](const uint4& u) {
-        const uint32_t w[4] = {u.x, u.y, u.z, u.w};
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            const float2 f = __half22float2(u32_as_h2(w[j]));
-            amax = fmaxf(amax, fmaxf(fabsf(f.x), fabsf(f.y)));
-            finite &= fabsf(f.x) <= FLT_MAX && fabsf(f.y) <= FLT_MAX;
-        }
-    };
+    __half2 am = __half2half2(__ushort_as_half(0));
 #pragma unroll
     for (int j = 0; j < kKeep; ++j) {
         const int i = threadIdx.x + j * kQuantThreads;
-        if (i < n8) {
-            keep[j] = ldcg_128(x + i);
-            see(keep[j]);
-        }
+        keep[j] = make_uint4(0, 0, 0, 0);
+        if (i < n8) keep[j] = ldcg_128(x + i);
     }
-    for (int i = threadIdx.x + kKeep * kQuantThreads; i < n8; i += kQuantThreads) see(ldcg_128(x + i));
+#pragma unroll
+    for (int j = 0; j < kKeep; ++j) amax8(keep[j], am);
+#pragma unroll 4
+    for (int i = threadIdx.x + kKeep * kQuantThreads; i < n8; i += kQuantThreads) amax8(ldcg_128(x + i), am);
+    float amax = amax_float(am);
+    bool finite = amax <= 65504.f;
     block_amax(amax, finite);
     const float s = int8_row_scale(amax, finite);
     if (threadIdx.x == 0) scales[t] = s;
     const float inv = __fdiv_rn(1.f, s);
-    auto code = [&](int i, const uint4& u) {
-        const float2 a = __half22float2(u32_as_h2(u.x)), b = __half22float2(u32_as_h2(u.y));
-        const float2 c = __half22float2(u32_as_h2(u.z)), e = __half22float2(u32_as_h2(u.w));
-        uint2 q = make_uint2(0u, 0u);
-        if (finite) {
-            q.x = int8_pack4_fast(a.x, a.y, b.x, b.y, s, inv);
-            q.y = int8_pack4_fast(c.x, c.y, e.x, e.y, s, inv);
-        }
-        codes8(i, q);
-    };
+    auto code = [&](int i, const uint4& u) { store(i, finite ? codes8(u, s, inv) : make_uint2(0u, 0u)); };
 #pragma unroll
     for (int j = 0; j < kKeep; ++j) {
         const int i = threadIdx.x + j * kQuantThreads;
         if (i < n8) code(i, keep[j]);
     }
+#pragma unroll 4
     for (int i = threadIdx.x + kKeep * kQuantThreads; i < n8; i += kQuantThreads) code(i, ldcg_128(x + i));
 }
 
-// One token per block, codes row-major [T][d].  BESIDE: launched behind the
-// projection of the same call, which has waited for X: it runs beside it and
-// waits for its end at its own, so that its end implies both.
-template <bool BESIDE>
+// One token per block, codes row-major [T][d].
 __global__ void __launch_bounds__(kQuantThreads) quantize_act_int8_kernel(const uint16_t* __restrict__ X, int64_t d,
                                                                           int8_t* __restrict__ codes,
                                                                           float* __restrict__ scales) {
-    if (!BESIDE) pdl_wait();
+    pdl_wait();
     pdl_launch_dependents();
     const int64_t t = blockIdx.x;
     uint2* out = reinterpret_cast<uint2*>(codes + t * d);
     quantize_token(X, t, d, scales, [&](int i, uint2 q) { out[i] = q; });
-    if (BESIDE) pdl_wait();
+}
+// This block's codes and scale are complete: count it, for a product that does
+// not wait for the whole grid (a grid's end takes 1.5 us to reach the next).
+__device__ __forceinline__ void count_ready(unsigned int* ready) {
+    __syncthreads();
+    if (threadIdx.x == 0) {
+        __threadfence();
+        flag_release_add(ready, 1u);
+    }
+}
+// The same inside a forward call, counting the tokens done.  Behind the
+// projection (!first), which has waited for X, it runs beside it; one block
+// waits for its end, so that this grid's end implies both.
+__global__ void __launch_bounds__(kQuantThreads) int8_quantize_kernel(const uint16_t* __restrict__ X, int64_t d,
+                                                                      int8_t* __restrict__ codes,
+                                                                      float* __restrict__ scales, unsigned int* ready,
+                                                                      bool first) {
+    if (first) pdl_wait();
+    pdl_launch_dependents();
+    const int64_t t = blockIdx.x;
+    uint2* out = reinterpret_cast<uint2*>(codes + t * d);
+    quantize_token(X, t, d, scales, [&](int i, uint2 q) { out[i] = q; });
+    count_ready(ready);
+    if (!first && t == 0) pdl_wait();
 }
 
 // ---------------------------------------------------------------------------
 // Small T (<= 16), first launch.  The first blocks compute R = X B^T, two rows
 // of B for all tokens per block, fp32 sums in a fixed order, rounded to fp16
 // (splitting d over blocks as well costs more in joining the parts than it
-// saves: 8.0 us against 4.9 at T = 1, d = 4096).  The others (only when the
-// product does not quantise by itself) quantise a token each into the layout
-// that the product stages with one bulk copy, [d/64][TOK][64]; tokens past T
-// are zero.
+// saves: 8.0 us against 4.9 at T = 1, d = 4096).  The others quantise a token
+// each into the layout that the product stages with one bulk copy,
+// [d/64][TOK][64] (tokens past T zero).  (Measured at T = 1, LLaMA-2-7B Q/K/V:
+// quantising in every block of the product instead 16.8 us against 14.8, as X
+// then queues behind the weights already in flight; counting the codes ready
+// so that the product need not wait for this grid's end 16.2 us, as the product
+// may then not fetch weights before the previous call has ended.)
 // ---------------------------------------------------------------------------
 constexpr int kPrepRows = 2, kPrepTokens = 16;
 
@@ -239,8 +232,8 @@ __device__ __forceinline__ void prep_rows(const Int8PrepArgs& a) {
 }
 
 __global__ void __launch_bounds__(kQuantThreads) int8_prep_kernel(const Int8PrepArgs a) {
+    pdl_launch_dependents();                     // the product may take its SMs and fetch weights
     pdl_wait();                                  // X is final; the previous call's readers of xq, xs, R are done
-    pdl_launch_dependents();                     // (only now: the product may read X without waiting for this kernel)
     if ((int)blockIdx.x < a.r / kPrepRows) {
         if (a.T <= 4) prep_rows<4>(a);
         else prep_rows<kPrepTokens>(a);
@@ -266,14 +259,11 @@ __global__ void __launch_bounds__(kQuantThreads) int8_prep_kernel(const Int8Prep
 // between copy and use.  mma.m16n8k32 takes k in any order as long as both
 // operands agree: lane (g, t) holds the 16 bytes k = 64 h + 16 t .. + 15 of
 // rows g and g + 8, and of token g of the staged activations.
-// SELF: the block quantises the tokens itself (few of them: each block reads
-// all of X), which needs no kernel to wait for; the projection of R runs beside
-// and is waited for before the first output.
+// The first blocks of W are in flight while the first launch runs.
 // ---------------------------------------------------------------------------
 constexpr int kGemvWarps = 8;
 constexpr int kGemvStages = 4;
 constexpr int kBlockBytes = 2048;                // 16 rows x 128 k
-constexpr int kSelfElements = 16384;             // T d up to which SELF is used
 
 struct Int8GemvModule {
     const int8_t* q;
@@ -285,8 +275,7 @@ struct Int8GemvModule {
 };
 struct Int8GemvArgs {
     Int8GemvModule mod[GLOWQ_MAX_MODULES];
-    const uint16_t* X;      // SELF: [T][d]
-    const int8_t* xq;       // else: [d/64][TOK][64] and
+    const int8_t* xq;       // [d/64][TOK][64]
     const float* xs;        // [TOK]
     const __half* R;        // [T][r]
     int* slots;             // [tile][NT][S][4][32] partial sums (S > 1)
@@ -326,71 +315,7 @@ __host__ __device__ inline Int8GemvSmem int8_gemv_smem(int nt, int kblocks, int 
     return s;
 }
 
-// Codes (of k blocks [kb0, kb1)) and scales of all tokens into shared memory:
-// a token by 8 / P warps, P = T rounded up to a power of two.
-template <int TOK>
-__device__ __forceinline__ void self_quantize(const Int8GemvArgs& a, unsigned char* codes, float* xs, float* red, int kb0,
-                                              int kb1) {
-    static_assert(TOK == 8, "a warp or more per token");
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int per = a.T > 4 ? 1 : a.T > 2 ? 2 : a.T > 1 ? 4 : 8;         // warps per token
-    const int t = warp / per, first = (warp % per) * 32 + lane, step = per * 32, n8 = a.d / 8;
-    const uint4* x = reinterpret_cast<const uint4*>(a.X + (int64_t)t * a.d);
-    constexpr int kKeep = 8;
-    uint4 keep[kKeep];
-    float amax = 0.f;
-    bool finite = true;
-    auto see = [&](const uint4& u) {
-        const uint32_t w[4] = {u.x, u.y, u.z, u.w};
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            const float2 f = __half22float2(u32_as_h2(w[j]));
-            amax = fmaxf(amax, fmaxf(fabsf(f.x), fabsf(f.y)));
-            finite &= fabsf(f.x) <= FLT_MAX && fabsf(f.y) <= FLT_MAX;
-        }
-    };
-    if (t < a.T) {
-#pragma unroll
-        for (int j = 0; j < kKeep; ++j)
-            if (first + j * step < n8) keep[j] = ldcg_128(x + first + j * step);
-#pragma unroll
-        for (int j = 0; j < kKeep; ++j)
-            if (first + j * step < n8) see(keep[j]);
-        for (int i = first + kKeep * step; i < n8; i += step) see(ldcg_128(x + i));
-    }
-    for (int o = 16; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(~0u, amax, o));
-    if (__any_sync(~0u, !finite)) amax = INFINITY;                       // carries "not finite" through the maximum
-    if (lane == 0) red[warp] = amax;
-    __syncthreads();
-    for (int w = 0; w < per; ++w) amax = fmaxf(amax, red[t * per + w]);
-    finite = amax <= FLT_MAX;
-    const float s = int8_row_scale(amax, finite), inv = __fdiv_rn(1.f, s);
-    if (warp % per == 0 && lane == 0) xs[t] = s;
-    auto code = [&](int i, const uint4& u) {
-        if (i < kb0 * 16 || i >= kb1 * 16) return;
-        const float2 a0 = __half22float2(u32_as_h2(u.x)), b = __half22float2(u32_as_h2(u.y));
-        const float2 c = __half22float2(u32_as_h2(u.z)), e = __half22float2(u32_as_h2(u.w));
-        uint2 q = make_uint2(0u, 0u);
-        if (finite) {
-            q.x = int8_pack4_fast(a0.x, a0.y, b.x, b.y, s, inv);
-            q.y = int8_pack4_fast(c.x, c.y, e.x, e.y, s, inv);
-        }
-        *reinterpret_cast<uint2*>(codes + ((i >> 3) - 2 * kb0) * (TOK * 64) + t * 64 + (i & 7) * 8) = q;
-    };
-    if (t < a.T) {
-#pragma unroll
-        for (int j = 0; j < kKeep; ++j)
-            if (first + j * step < n8) code(first + j * step, keep[j]);
-        for (int i = first + kKeep * step; i < n8; i += step) code(i, ldcg_128(x + i));
-    }
-    // tokens past T: their sums are not stored, but the codes must be numbers that are written
-    for (int i = threadIdx.x; i < (kb1 - kb0) * 2 * (TOK - a.T) * 4; i += kGemvWarps * 32) {
-        const int c = i & 3, rest = i >> 2, tok = a.T + rest % (TOK - a.T), kb = rest / (TOK - a.T);
-        *reinterpret_cast<uint4*>(codes + (kb * TOK + tok) * 64 + c * 16) = make_uint4(0, 0, 0, 0);
-    }
-}
-
-template <int NT, bool SELF>
+template <int NT>
 __global__ void __launch_bounds__(kGemvWarps * 32) int8_gemv_kernel(const __grid_constant__ Int8GemvArgs a) {
     extern __shared__ __align__(128) unsigned char sm[];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
@@ -404,7 +329,7 @@ __global__ void __launch_bounds__(kGemvWarps * 32) int8_gemv_kernel(const __grid
     uint64_t* bar = reinterpret_cast<uint64_t*>(sm + L.bar);
     const int nsteps = (kb1 - kb0 + kGemvWarps - 1) / kGemvWarps;      // ring blocks per tile (the last may be absent)
     const uint64_t policy = l2_policy_evict_first();
-    if (!SELF && threadIdx.x == 0) {
+    if (threadIdx.x == 0) {
         mbar_init(bar, 1);
         fence_mbar_init();
     }
@@ -455,33 +380,22 @@ __global__ void __launch_bounds__(kGemvWarps * 32) int8_gemv_kernel(const __grid
             }
         }
     };
-    auto stage_r = [&]() {
-        for (int i = threadIdx.x; i < NT * a.r; i += kGemvWarps * 32) {   // 8 halves each
-            uint4 v = make_uint4(0, 0, 0, 0);
-            if (i * 8 / a.r < a.T) v = ldcg_128(a.R + i * 8);
-            *reinterpret_cast<uint4*>(sm + L.rt + i * 16) = v;
-        }
-    };
     for (int i = 0; i < kGemvStages - 1; ++i) prefetch();
-    if constexpr (SELF) {
-        // launched behind the projection, which has waited for X (r > 0), or first in the call
-        if (a.r == 0) pdl_wait();
-        pdl_launch_dependents();
-        self_quantize<8>(a, sm, xs, reinterpret_cast<float*>(sm + L.red), kb0, kb1);
-    } else {
-        __syncthreads();                                 // the barrier is initialised
-        pdl_wait();                                      // codes, scales and R of this call are complete
-        pdl_launch_dependents();
-        if (threadIdx.x == 0) {
-            const uint32_t bytes = (uint32_t)(NT * 8 * 128) * (uint32_t)(kb1 - kb0);
-            fence_proxy_async_smem();
-            mbar_arrive_expect_tx(bar, bytes);
-            bulk_g2s(base, a.xq + (int64_t)kb0 * (NT * 8 * 128), bytes, bar);
-        }
-        for (int i = threadIdx.x; i < NT * 8; i += kGemvWarps * 32) xs[i] = ldcg_f32(a.xs + i);
-        stage_r();
-        mbar_wait(bar, 0, a.status);
+    __syncthreads();                                     // the barrier is initialised
+    pdl_wait();                                          // codes, scales and R of this call are complete
+    pdl_launch_dependents();
+    if (threadIdx.x == 0) {
+        const uint32_t bytes = (uint32_t)(NT * 8 * 128) * (uint32_t)(kb1 - kb0);
+        mbar_arrive_expect_tx(bar, bytes);
+        bulk_g2s(base, a.xq + (int64_t)kb0 * (NT * 8 * 128), bytes, bar);
     }
+    for (int i = threadIdx.x; i < NT * a.r; i += kGemvWarps * 32) {   // 8 halves each
+        uint4 v = make_uint4(0, 0, 0, 0);
+        if (i * 8 / a.r < a.T) v = ldcg_128(a.R + i * 8);
+        *reinterpret_cast<uint4*>(sm + L.rt + i * 16) = v;
+    }
+    if (threadIdx.x < NT * 8) xs[threadIdx.x] = ldcg_f32(a.xs + threadIdx.x);
+    mbar_wait(bar, 0, a.status);
     __syncthreads();
     int cs = 0, par = 0;
     for (int tile = tile0; tile < a.tiles; tile += step, par ^= 1) {
@@ -511,10 +425,6 @@ __global__ void __launch_bounds__(kGemvWarps * 32) int8_gemv_kernel(const __grid
                 }
             }
             if (++cs == kGemvStages) cs = 0;
-        }
-        if (SELF && tile == tile0 && a.r > 0) {
-            pdl_wait();                                  // R is complete
-            stage_r();
         }
         // the warps' sums meet in shared memory (double buffered: one barrier per tile)
         int4* red = reinterpret_cast<int4*>(sm + L.red + par * kGemvWarps * NT * 512);
@@ -615,13 +525,13 @@ cudaError_t launch_pdl(const void* fn, unsigned grid, unsigned block, size_t sme
 cudaError_t launch_quantize_act_int8(const uint16_t* X, int64_t T, int64_t d, int8_t* codes, float* scales,
                                      cudaStream_t st) {
     void* args[] = {(void*)&X, (void*)&d, (void*)&codes, (void*)&scales};
-    return launch_pdl((const void*)quantize_act_int8_kernel<false>, (unsigned)T, kQuantThreads, 0, st, args);
+    return launch_pdl((const void*)quantize_act_int8_kernel, (unsigned)T, kQuantThreads, 0, st, args);
 }
 
 cudaError_t launch_quantize_beside(const uint16_t* X, int64_t T, int64_t d, int8_t* codes, float* scales,
-                                   cudaStream_t st) {
-    void* args[] = {(void*)&X, (void*)&d, (void*)&codes, (void*)&scales};
-    return launch_pdl((const void*)quantize_act_int8_kernel<true>, (unsigned)T, kQuantThreads, 0, st, args);
+                                   unsigned int* ready, bool first, cudaStream_t st) {
+    void* args[] = {(void*)&X, (void*)&d, (void*)&codes, (void*)&scales, (void*)&ready, (void*)&first};
+    return launch_pdl((const void*)int8_quantize_kernel, (unsigned)T, kQuantThreads, 0, st, args);
 }
 
 // Token width (a multiple of 8) of the small-T kernels.
@@ -639,16 +549,15 @@ Int8GemvPlan plan_int8_gemv(int64_t T, int64_t d, int64_t tiles, int r, int num_
     }
     p.smem = int8_gemv_smem(nt, (nkb + p.S - 1) / p.S, r).total;
     p.ok = p.smem <= 227 * 1024 && (p.S == 1 || tiles * nt <= kInt8MaxTickets) && tiles < (1 << 24);
-    p.self = T <= 8 && T * d <= kSelfElements;
     const int64_t slots = (int64_t)num_sms * (p.smem <= 113 * 1024 ? 2 : 1) / p.S;
     p.grid = (int)(tiles < slots ? tiles : (slots < 1 ? 1 : slots)) * p.S;
     p.slot_bytes = p.S > 1 ? (size_t)tiles * nt * p.S * 512 : 0;
     return p;
 }
 
-template <int NT, bool SELF>
+template <int NT>
 static cudaError_t launch_int8_gemv_t(const Int8GemvArgs& a, const Int8GemvPlan& p, cudaStream_t st) {
-    const void* fn = (const void*)int8_gemv_kernel<NT, SELF>;
+    const void* fn = (const void*)int8_gemv_kernel<NT>;
     cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, 227 * 1024);
     if (e != cudaSuccess) return e;
     void* args[] = {(void*)&a};
@@ -661,11 +570,8 @@ cudaError_t launch_int8_small(const Int8ModuleView* mods, int m, int d, int T, i
     const int tok = int8_small_tokens(T);
     Int8PrepArgs pa = {X, B, xq, xs, reinterpret_cast<__half*>(R), d, T, tok, r};
     void* pargs[] = {(void*)&pa};
-    const unsigned blocks = (unsigned)(r / kPrepRows + (p.self ? 0 : tok));
-    if (blocks > 0) {
-        cudaError_t e = launch_pdl((const void*)int8_prep_kernel, blocks, kQuantThreads, 0, st, pargs);
-        if (e != cudaSuccess) return e;
-    }
+    cudaError_t e = launch_pdl((const void*)int8_prep_kernel, (unsigned)(r / kPrepRows + tok), kQuantThreads, 0, st, pargs);
+    if (e != cudaSuccess) return e;
     Int8GemvArgs a = {};
     int tile = 0;
     for (int i = 0; i < m; ++i) {
@@ -673,7 +579,6 @@ cudaError_t launch_int8_small(const Int8ModuleView* mods, int m, int d, int T, i
                     mods[i].ldY, tile};
         tile += (int)(mods[i].O / 16);
     }
-    a.X = X;
     a.xq = xq;
     a.xs = xs;
     a.R = reinterpret_cast<const __half*>(R);
@@ -686,8 +591,7 @@ cudaError_t launch_int8_small(const Int8ModuleView* mods, int m, int d, int T, i
     a.tiles = tile;
     a.S = p.S;
     a.status = device_status_ptr();
-    if (p.self) return launch_int8_gemv_t<1, true>(a, p, st);
-    return T <= 8 ? launch_int8_gemv_t<1, false>(a, p, st) : launch_int8_gemv_t<2, false>(a, p, st);
+    return T <= 8 ? launch_int8_gemv_t<1>(a, p, st) : launch_int8_gemv_t<2>(a, p, st);
 }
 
 }  // namespace glowq

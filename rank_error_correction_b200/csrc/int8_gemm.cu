@@ -67,6 +67,7 @@ struct I8GemmArgs {
     int ntiles_n;
     I8Split split;
     int* slots;                            // [pair][segment][2 CTAs][BN tokens][128 rows]
+    unsigned int* counters;                // tokens quantised, blocks done (internal.cuh)
     unsigned int* status;
 };
 
@@ -231,7 +232,7 @@ __global__ void __launch_bounds__(kI8Threads, 1) int8_gemm_kernel(const __grid_c
 
     if (warp == 0) {
         // ---------------- producer (both CTAs, the whole warp) ----------------
-        bool ok = true;
+        bool ok = true, r_ready = false;
         int g = 0, s = 0, early = 0;                       // stages so far, ring stage, stages whose W is fetched ahead
         uint32_t ph = 1;                                   // parity of empty[s] that frees the stage (the first use: free)
         const uint32_t base = smem_u32(sm), empty0 = smem_u32(&bars->empty[0]), full0 = smem_u32(&bars->full[0]);
@@ -257,14 +258,14 @@ __global__ void __launch_bounds__(kI8Threads, 1) int8_gemm_kernel(const __grid_c
             a, BN, pair,
             [&](const I8Unit& c, int n) {
                 if (n > 0) return;
-                // the codes of W are static: the first of them are fetched before the
-                // kernels that quantise X and compute R are known to be complete
+                // the codes of W are static: the first of them are fetched while X is quantised
                 early = min(kStages, c.nkb);
                 for (int i = 0; i < early; ++i) {
                     announce(i);
                     load(0, &a.tmW[c.mi], i, (c.kb0 + i) * kI8Block, c.m0 + row_off);
                 }
-                pdl_wait();
+                wait_ready(a.counters, (unsigned)a.T);
+                fence_proxy_async_all();
             },
             [&](const I8Unit& c, int n, int i) {
                 if (g >= early) {
@@ -277,6 +278,8 @@ __global__ void __launch_bounds__(kI8Threads, 1) int8_gemm_kernel(const __grid_c
             },
             [&](const I8Unit&, int) {},
             [&](const I8Unit& c, int n, int j) {
+                if (!r_ready) pdl_wait();                  // R is complete
+                r_ready = true;
                 room();
                 announce(s);
                 load(0, &a.tmA[c.mi], s, j * 64, c.m0 + row_off);
@@ -296,7 +299,7 @@ __global__ void __launch_bounds__(kI8Threads, 1) int8_gemm_kernel(const __grid_c
             bool ok = true;
             int s = 0, units = 0;
             uint32_t ph = 0, convs = 0;                    // convs: bit b: parity of conv[b]
-            pdl_wait();
+            wait_ready(a.counters, (unsigned)a.T);         // (the bounded waits below begin when the codes can come)
             auto stage = [&](auto integer, uint32_t acc, uint32_t accumulate) {
                 if (ok) ok = mbar_wait_warp(full0 + 8u * (uint32_t)s, ph, a.status);
                 tc_fence_after();
@@ -340,7 +343,8 @@ __global__ void __launch_bounds__(kI8Threads, 1) int8_gemm_kernel(const __grid_c
         bool ok = true;
         int chunk = 0;
         uint32_t slabs = 0;                               // bit b: parity of slab_full[b]
-        pdl_wait();                                       // the token scales are complete
+        wait_ready(a.counters, (unsigned)a.T);            // the token scales are complete
+        pdl_wait();                                       // ... and the previous readers of Y and the slots are done
         i8_walk(
             a, BN, pair, [&](const I8Unit&, int) {}, [&](const I8Unit&, int, int) {},
             [&](const I8Unit& c, int n) {
@@ -424,6 +428,12 @@ __global__ void __launch_bounds__(kI8Threads, 1) int8_gemm_kernel(const __grid_c
     __syncwarp();
     cluster_sync_all();                                   // no arrivals or MMA reads into either CTA remain
     if (warp == 1) tmem_dealloc_pair(tmem, TL::kCols);
+    if (threadIdx.x == 0) {                               // the last block to end returns the counters to zero
+        if (atomicAdd(a.counters + 1, 1u) == gridDim.x - 1) {
+            atomicExch(a.counters, 0u);
+            atomicExch(a.counters + 1, 0u);
+        }
+    }
 }
 
 // ---------------------------------------------------------------------------
@@ -576,7 +586,7 @@ struct I8JoinArgs {
     int m, T, r, bn, ntiles_n;
 };
 
-__global__ void __launch_bounds__(kJoinThreads) int8_join_kernel(const __grid_constant__ I8JoinArgs a) {
+__global__ void __launch_bounds__(kJoinThreads, 3) int8_join_kernel(const __grid_constant__ I8JoinArgs a) {
     pdl_launch_dependents();
     const int chunks = a.bn / 32;
     const int ch = blockIdx.x % chunks, half = (blockIdx.x / chunks) & 1, rel = blockIdx.x / chunks / 2;
@@ -610,7 +620,7 @@ __global__ void __launch_bounds__(kJoinThreads) int8_join_kernel(const __grid_co
     if (t0 >= a.T) return;
     // the segments that hold the tile's k-blocks [rel nkb, (rel + 1) nkb): those of pairs p0 .. p1
     const int nkb = a.split.nkb, lo = rel * nkb, hi = lo + nkb;
-    int p = lo * a.split.pairs / a.split.blocks;
+    int p = lo * a.split.sharers / a.split.blocks;
     while (i8_share(a.split, p + 1) <= lo) ++p;
     while (i8_share(a.split, p) > lo) --p;
     // R of the first 64 columns and the token scales, in flight beside the sums
@@ -635,9 +645,7 @@ __global__ void __launch_bounds__(kJoinThreads) int8_join_kernel(const __grid_co
             st[n][e] = tok < a.T ? ldcg_f32(a.xs + tok) : 0.f;
         }
     int v[4][2][4] = {};
-    for (int begin = i8_share(a.split, p), end; p < a.split.pairs && begin < hi; ++p, begin = end) {
-        end = i8_share(a.split, p + 1);
-        if (begin == end) continue;                       // no share (fewer blocks than pairs)
+    for (int begin = i8_share(a.split, p); p < a.split.sharers && begin < hi; begin = i8_share(a.split, ++p)) {
         const int seg = rel - begin / nkb;                // the pair's segments are one per tile, in order
         const int* src = a.slots + (((int64_t)p * a.split.segments + seg) * 2 + half) * ((int64_t)a.bn * kI8Rows) +
                          (int64_t)ch * 32 * kI8Rows + trow;
@@ -719,7 +727,7 @@ cudaError_t launch_int8_project(const uint16_t* X, const uint16_t* B, int64_t T,
     a.T = (int)T;
     a.r = r;
     a.status = device_status_ptr();
-    const int most = 200 * 1024 / proj_stage_bytes(a.rn);        // 4 at r = 256
+    const int most = 104 * 1024 / proj_stage_bytes(a.rn);        // two blocks an SM: 4 stages at r = 64, 2 at r = 256
     a.stages = most > kProjStages ? kProjStages : most;
     uint32_t ring = (uint32_t)proj_ring_bytes(a.rn, a.stages);
     cudaError_t e = cudaFuncSetAttribute((const void*)int8_project_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
@@ -749,28 +757,32 @@ cudaError_t launch_int8_project(const uint16_t* X, const uint16_t* B, int64_t T,
 // its sums and the join (about 2 us, and the sums' way at 5 TB/s).
 I8GemmPlan plan_int8_gemm(int64_t T, int64_t d, int64_t mtiles, int num_sms) {
     I8GemmPlan p;
-    const int64_t pairs = gemm_max_pairs(num_sms), nkb = d / kI8Block;
-    const int64_t nt = (T + 255) / 256;
+    const int64_t nkb = d / kI8Block, nt = (T + 255) / 256, tiles = mtiles * nt;
     p.bn = (int)(((T + nt - 1) / nt + 63) / 64 * 64);
-    const int64_t tiles = mtiles * nt;
+    int64_t pairs = gemm_max_pairs(num_sms);
     int64_t rounds = tiles / pairs, rest = tiles - rounds * pairs;
-    const double blocks = (double)rest * nkb;
-    const double split = blocks / pairs * 600 + 4000 + (double)rest * 256 * p.bn * 8 / 2600.0;
-    p.split.pairs = (int)(tiles < pairs && rest > 0 && nkb * 600.0 < split ? tiles : pairs);
-    if (rest > 0 && nkb * 600.0 < split) {
+    p.split.whole = rounds * pairs;
+    // no share below 8 blocks: the join reads every share of a tile
+    int64_t sharers = rest * nkb / 8;
+    sharers = sharers < 1 ? 1 : sharers > pairs ? pairs : sharers;
+    const double whole = nkb * 600.0;
+    const double split = (double)rest * nkb / sharers * 600 + 4000 + (double)rest * 256 * p.bn * 8 / 2600.0;
+    if (rest > 0 && whole < split) {
         // the last round is one of whole tiles: pairs without a tile in it have none
         p.split.whole = tiles;
+        if (rounds == 0) pairs = tiles;
+        ++rounds;
         rest = 0;
-        rounds = (tiles + p.split.pairs - 1) / p.split.pairs;
-    } else {
-        p.split.whole = rounds * pairs;
     }
+    if (rest > 0 && rounds == 0) pairs = sharers;
+    p.split.pairs = (int)pairs;
+    p.split.sharers = (int)sharers;
     p.split.rounds = (int)rounds;
     p.split.nkb = (int)nkb;
     p.split.blocks = (int)(rest * nkb);
-    p.split.segments = (int)((rest * nkb + pairs - 1) / pairs / nkb + 2);
+    p.split.segments = (int)((rest * nkb + sharers - 1) / sharers / nkb + 2);
     p.rest = rest;
-    p.slot_bytes = rest > 0 ? (size_t)pairs * p.split.segments * 2 * kI8Rows * p.bn * 4 : 0;
+    p.slot_bytes = rest > 0 ? (size_t)sharers * p.split.segments * 2 * kI8Rows * p.bn * 4 : 0;
     return p;
 }
 
@@ -798,7 +810,8 @@ static cudaError_t launch_int8_gemm_t(const I8GemmArgs& a, int pairs, cudaStream
 }
 
 cudaError_t launch_int8_gemm(const Int8ModuleView* mods, int m, int d, int64_t T, int r, const int8_t* xq,
-                             const float* xs, const uint16_t* R, int* slots, const I8GemmPlan& p, cudaStream_t st) {
+                             const float* xs, const uint16_t* R, unsigned int* tickets, int* slots, const I8GemmPlan& p,
+                             cudaStream_t st) {
     I8GemmArgs a;
     std::memset(&a, 0, sizeof(a));
     const uint32_t half = (uint32_t)(p.bn / 2);
@@ -830,6 +843,7 @@ cudaError_t launch_int8_gemm(const Int8ModuleView* mods, int m, int d, int64_t T
     a.ntiles_n = (int)((T + p.bn - 1) / p.bn);
     a.split = p.split;
     a.slots = slots;
+    a.counters = tickets + kInt8Ready;
     a.status = device_status_ptr();
     const int pairs = p.split.pairs;
     cudaError_t e = p.bn == 64    ? launch_int8_gemm_t<64>(a, pairs, st)

@@ -90,11 +90,14 @@ struct Int8ModuleView {
 constexpr int64_t kInt8MaxD = 131072;          // 127^2 d < 2^31
 constexpr int kInt8SmallTokens = 16;           // tokens up to which the weight-streaming product runs
 constexpr int kInt8ZeroBytes = 65536;          // tickets at the workspace's start
-constexpr int kInt8MaxTickets = kInt8ZeroBytes / 4;
+constexpr int kInt8MaxTickets = kInt8ZeroBytes / 4 - 64;
+// Behind the tickets, two counters between the quantiser and the product that
+// runs beside its end: tokens quantised so far, blocks of the product done with
+// waiting (the last one returns both to zero).
+constexpr int kInt8Ready = kInt8MaxTickets, kInt8Done = kInt8MaxTickets + 1;
 // Decomposition of the small-T product: S blocks share a tile's k.
 struct Int8GemvPlan {
     bool ok;             // false: the shape is left to the tensor-core GEMM
-    bool self;           // the product quantises X by itself
     int S, grid, smem;
     size_t slot_bytes;   // partial sums (S > 1)
 };
@@ -109,18 +112,21 @@ cudaError_t launch_int8_small(const Int8ModuleView* mods, int m, int d, int T, i
                               const uint16_t* B, uint16_t* R, int8_t* xq, float* xs, unsigned int* tickets, int* slots,
                               const Int8GemvPlan& p, cudaStream_t st);
 // The token quantiser behind a kernel of the same call that has waited for X: its end implies that kernel's.
+// It counts the tokens that are done on `ready`.
 cudaError_t launch_quantize_beside(const uint16_t* X, int64_t T, int64_t d, int8_t* codes, float* scales,
-                                   cudaStream_t st);
+                                   unsigned int* ready, bool first, cudaStream_t st);
 // int8_gemm.cu: T > 16 on the tensor cores.  `rounds` whole tiles per pair
 // (tiles [0, whole)), then the other tiles' k-blocks as one run of `blocks` cut
-// evenly among the pairs; a pair's share has at most `segments` tiles' segments.
+// evenly among the first `sharers` pairs (every one has a share, in at most
+// `segments` tiles).
 struct I8Split {
-    int pairs, rounds, nkb, segments;
+    int pairs, rounds, nkb, sharers, segments;
     int64_t whole;
     int blocks;          // below pairs nkb, so that blocks x pairs fits an int
 };
+// Where a pair's share begins (at `sharers` and behind: the end of the run).
 __host__ __device__ inline int i8_share(const I8Split& s, int pair) {
-    return (int)((unsigned)s.blocks * (unsigned)pair / (unsigned)s.pairs);
+    return pair >= s.sharers ? s.blocks : (int)((unsigned)s.blocks * (unsigned)pair / (unsigned)s.sharers);
 }
 struct I8GemmPlan {
     int bn;              // tokens per pair tile
@@ -132,7 +138,8 @@ I8GemmPlan plan_int8_gemm(int64_t T, int64_t d, int64_t mtiles, int num_sms);
 cudaError_t launch_int8_project(const uint16_t* X, const uint16_t* B, int64_t T, int d, int r, uint16_t* R,
                                 cudaStream_t st);
 cudaError_t launch_int8_gemm(const Int8ModuleView* mods, int m, int d, int64_t T, int r, const int8_t* xq,
-                             const float* xs, const uint16_t* R, int* slots, const I8GemmPlan& p, cudaStream_t st);
+                             const float* xs, const uint16_t* R, unsigned int* tickets, int* slots, const I8GemmPlan& p,
+                             cudaStream_t st);
 // solve.cu: the offline group solve (float64)
 struct SolveModule {
     const float* W;      // O x d fp32 weights

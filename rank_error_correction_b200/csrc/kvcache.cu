@@ -10,6 +10,7 @@
 #include "common.cuh"
 #include "internal.cuh"
 #include "kvcache.cuh"
+#include "quant8.cuh"
 
 namespace glowq {
 
@@ -56,30 +57,6 @@ __device__ __forceinline__ HalfRow rotate(const HalfRow& v, const float* cs, int
     }
     return {make_uint4(x[0], x[1], x[2], x[3]), make_uint4(y[0], y[1], y[2], y[3])};
 }
-__device__ __forceinline__ void see_halves(const uint4& u, float& amax, bool& finite) {
-    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-        const float2 f = __half22float2(u32_as_h2(w[j]));
-        amax = fmaxf(amax, fmaxf(fabsf(f.x), fabsf(f.y)));
-        finite &= fabsf(f.x) <= 65504.f && fabsf(f.y) <= 65504.f;
-    }
-}
-__device__ __forceinline__ int kv_code(float x, float s) {
-    return (int)fminf(fmaxf(rintf(__fdiv_rn(x, s)), -127.f), 127.f);
-}
-// Codes of 8 consecutive elements.
-__device__ __forceinline__ uint2 codes_of(const uint4& u, float s, bool finite) {
-    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
-    uint32_t q[4];
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-        const float2 f = __half22float2(u32_as_h2(w[j]));
-        q[j] = finite ? ((uint32_t)(kv_code(f.x, s) & 255) | ((uint32_t)(kv_code(f.y, s) & 255) << 8)) : 0u;
-    }
-    return make_uint2(q[0] | (q[1] << 16), q[2] | (q[3] << 16));
-}
-
 // One block: one page that the step touches, of one sequence and kv head (and
 // the query heads that share it).  The block of the first touched page also
 // takes the last one when that stays incomplete: it reads the old tail for the
@@ -88,7 +65,7 @@ template <int D>
 __global__ void __launch_bounds__(kAppendThreads) kv_append_kernel(const __grid_constant__ KvAppendArgs a) {
     constexpr int kHalf = D / 2, kItems = D / 16;        // items of 8 + 8 elements per row
     constexpr int kPer = kKvPage * kItems / kAppendThreads;
-    __shared__ float red[4][kAppendThreads / 32];
+    __shared__ float red[2][kAppendThreads / 32];
     __shared__ __align__(16) unsigned char vt[D][kKvPage + 16];   // codes of V by dimension
     pdl_wait();
     pdl_launch_dependents();
@@ -134,8 +111,7 @@ __global__ void __launch_bounds__(kAppendThreads) kv_append_kernel(const __grid_
             }
         } else {
             HalfRow k[kPer], v[kPer];
-            float ka = 0.f, va = 0.f;
-            bool kf = true, vf = true;
+            __half2 kam = __half2half2(__ushort_as_half(0)), vam = kam;
 #pragma unroll
             for (int q = 0; q < kPer; ++q) {
                 const int it = tid + q * kAppendThreads, i = it % kItems, pos = p * kKvPage + it / kItems;
@@ -149,35 +125,34 @@ __global__ void __launch_bounds__(kAppendThreads) kv_append_kernel(const __grid_
                     v[q] = load_row(a.V + row * a.ldV + (int64_t)h * D, i, kHalf);
                     if (a.rope) k[q] = rotate(k[q], a.rope + (int64_t)pos * D, i, kHalf);
                 }
-                see_halves(k[q].lo, ka, kf);
-                see_halves(k[q].hi, ka, kf);
-                see_halves(v[q].lo, va, vf);
-                see_halves(v[q].hi, va, vf);
+                amax8(k[q].lo, kam);
+                amax8(k[q].hi, kam);
+                amax8(v[q].lo, vam);
+                amax8(v[q].hi, vam);
             }
             for (int o = 16; o > 0; o >>= 1) {
-                ka = fmaxf(ka, __shfl_xor_sync(~0u, ka, o));
-                va = fmaxf(va, __shfl_xor_sync(~0u, va, o));
+                kam = __hmax2_nan(kam, __shfl_xor_sync(~0u, kam, o));
+                vam = __hmax2_nan(vam, __shfl_xor_sync(~0u, vam, o));
             }
-            const bool kb = __any_sync(~0u, !kf), vb = __any_sync(~0u, !vf);
             if ((tid & 31) == 0) {
-                red[0][tid >> 5] = ka;
-                red[1][tid >> 5] = va;
-                red[2][tid >> 5] = kb;
-                red[3][tid >> 5] = vb;
+                red[0][tid >> 5] = amax_float(kam);
+                red[1][tid >> 5] = amax_float(vam);
             }
             __syncthreads();
-            float knf = 0.f, vnf = 0.f;
+            float ka = 0.f, va = 0.f;
+            bool kf = true, vf = true;
 #pragma unroll
             for (int w = 0; w < kAppendThreads / 32; ++w) {
                 ka = fmaxf(ka, red[0][w]);
                 va = fmaxf(va, red[1][w]);
-                knf += red[2][w];
-                vnf += red[3][w];
+                kf &= red[0][w] <= 65504.f;
+                vf &= red[1][w] <= 65504.f;
             }
             // 2^-24 is fp16's smallest value: the scale of an all-zero page, below every other
             const float nan = __int_as_float(0x7fffffff);
-            const float ks = knf == 0.f ? __fdiv_rn(fmaxf(ka, 5.9604644775390625e-8f), 127.f) : nan;
-            const float vs = vnf == 0.f ? __fdiv_rn(fmaxf(va, 5.9604644775390625e-8f), 127.f) : nan;
+            const float ks = kf ? __fdiv_rn(fmaxf(ka, 5.9604644775390625e-8f), 127.f) : nan;
+            const float vs = vf ? __fdiv_rn(fmaxf(va, 5.9604644775390625e-8f), 127.f) : nan;
+            const float kinv = __fdiv_rn(1.f, ks), vinv = __fdiv_rn(1.f, vs);
             const int page = ldcg_s32(a.b.table + (int64_t)b * a.b.max_pages + p);
             if (page < 0 || page >= a.c.pages) {
                 if (tid == 0) record_status(a.status, GLOWQ_ERR_INDEX);
@@ -196,8 +171,8 @@ __global__ void __launch_bounds__(kAppendThreads) kv_append_kernel(const __grid_
                     for (int e = 0; e < 2; ++e) {        // dimensions 8 i .. + 7 and the same behind the middle
                         const int dim = e * kHalf + 8 * i;
                         *reinterpret_cast<uint2*>(kc + ((dim >> 6) * kKvPage + tok) * 64 + (dim & 63)) =
-                            codes_of(e ? k[q].hi : k[q].lo, ks, knf == 0.f);
-                        const uint2 c = codes_of(e ? v[q].hi : v[q].lo, vs, vnf == 0.f);
+                            kf ? codes8(e ? k[q].hi : k[q].lo, ks, kinv) : make_uint2(0u, 0u);
+                        const uint2 c = vf ? codes8(e ? v[q].hi : v[q].lo, vs, vinv) : make_uint2(0u, 0u);
 #pragma unroll
                         for (int r = 0; r < 8; ++r)
                             vt[dim + r][tok] = (unsigned char)((r < 4 ? c.x >> (8 * r) : c.y >> (8 * (r - 4))) & 255u);
