@@ -468,6 +468,7 @@ static size_t attn_smem(int D) {
 
 KvAttnPlan plan_kv_attention(const KvBatchView& b, int G, int kv_heads, int head_dim, int num_sms) {
     KvAttnPlan p;
+    p.tc = (int64_t)b.max_new * G >= 64;
     p.rt = (int)(((int64_t)b.max_new * G + 15) / 16);
     const int64_t units = (int64_t)b.n_seq * kv_heads * p.rt;
     p.S = 1;
@@ -478,6 +479,7 @@ KvAttnPlan plan_kv_attention(const KvBatchView& b, int G, int kv_heads, int head
         if (S > 64) S = 64;
         if (S > 1) p.S = (int)S;
     }
+    if (p.tc) p.S = 1;
     p.partial_bytes = p.S > 1 ? (size_t)units * p.S * 16 * (head_dim + 2) * sizeof(float) : 0;
     return p;
 }
@@ -494,6 +496,7 @@ static cudaError_t launch_attn(const KvAttnArgs& a, unsigned grid, cudaStream_t 
 cudaError_t launch_kv_attention(const KvCacheView& c, const KvBatchView& b, const uint16_t* Q, int64_t ldQ, int q_heads,
                                 float scale, uint16_t* Y, int64_t ldY, unsigned int* tickets, float* partial,
                                 const KvAttnPlan& p, cudaStream_t st) {
+    if (p.tc) return launch_kv_attention_tc(c, b, Q, ldQ, q_heads, scale, Y, ldY, st);
     KvAttnArgs a = {c, b, Q, Y, ldQ, ldY, scale * 1.44269504088896340736f, q_heads / c.kv_heads, p.rt, p.S, partial, tickets,
                     device_status_ptr()};
     const unsigned grid = (unsigned)((int64_t)b.n_seq * c.kv_heads * p.rt * p.S);

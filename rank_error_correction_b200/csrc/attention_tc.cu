@@ -1,0 +1,538 @@
+// attention_tc.cu -- attention of many query rows (prefill, chunks) over the
+// paged 8-bit cache on the 5th-generation tensor cores; the formulas of
+// attention.cu.
+//
+// A block takes 256 rows (row = new token i and query head gq of the kv head's
+// group, i G + gq) of one sequence and kv head, as two tiles of 128 rows that
+// share every key and value, over tiles of 128 tokens (two pages):
+//   S_t = Q_t K^T       128 x 128 x D, Q and K in shared memory (fp16)
+//   P_t = 2^(S_t a - m) in fp16 over S_t's columns of TMEM
+//   O_t += P_t V        P from TMEM, V in shared memory
+// The four accumulators S_0, S_1, O_0, O_1 fill TMEM at D = 128.  While one
+// tile's softmax runs, the tensor cores work on the other's products.
+// The cache's layouts are the operands': a row of 64 codes (64 dimensions of a
+// key, 64 tokens of a value's dimension) becomes a 128-byte row of fp16 in the
+// K-major 128-byte-swizzled layout, so converting is all the staging there is.
+// A row's reference m is moved only when its maximum has grown by 2^6 or more
+// (then O is rescaled in TMEM): weights stay below 2^14.
+// Warps: 0-3 and 4-7 softmax of tiles 0 and 1 (a thread per row), 8-11 convert
+// pages, 12 issues the MMAs.
+#include "internal.cuh"
+#include "kvcache.cuh"
+#include "tc.cuh"
+
+namespace glowq {
+
+constexpr int kTcRows = 256, kTcTokens = 128, kTcThreads = 512, kTcMeta = 4;
+constexpr float kTcWeightExp = 8.f, kTcSlack = 6.f;
+
+struct KvTcArgs {
+    KvCacheView c;
+    KvBatchView b;
+    const uint16_t* Q;
+    uint16_t* Y;
+    int64_t ldQ, ldY;
+    float scale_log2;
+    int G, rt;               // query heads per kv head, row tiles of the widest sequence
+    unsigned int* status;
+};
+
+// What a softmax needs of a tile's two pages.
+struct KvTcMeta {
+    float a[2];              // s_K scale log2(e)
+    float lv[2];             // log2 s_V
+    float inv[2];            // 1 / s_V
+    int valid[2];            // tokens present
+    unsigned int poison[4];  // tokens (of 128) whose value is not finite
+};
+struct __align__(8) KvTcShared {
+    uint64_t q_full, kf[2], ke[2], vf[2], ve[2], s_full[2], p_full[2], o_done[2];
+    KvTcMeta meta[kTcMeta];
+    unsigned int tail_max, tail_poison[2];
+    uint32_t tmem;
+};
+
+template <int D>
+struct KvTc {
+    static constexpr int kPanels = D / 64;
+    static constexpr int kQBytes = 128 * D * 2;          // one row tile: panels of [128 rows][128 B]
+    static constexpr int kKBytes = kTcTokens * D * 2;    // panels of [128 tokens][128 B]
+    static constexpr int kVBytes = 2 * D * 128;          // pages of [D][128 B]
+    static constexpr int kSmem = 2 * kQBytes + 2 * kKBytes + 2 * kVBytes + (int)sizeof(KvTcShared) + 1024;
+};
+
+__device__ __forceinline__ void tc_cvt_codes(uint32_t w, uint32_t& lo, uint32_t& hi) {
+    const uint32_t u = w ^ 0x80808080u;
+    const __half2 bias = u32_as_h2(0x64806480u);         // 1152
+    lo = h2_as_u32(__hsub2(u32_as_h2(__byte_perm(u, 0x64646464u, 0x4140)), bias));
+    hi = h2_as_u32(__hsub2(u32_as_h2(__byte_perm(u, 0x64646464u, 0x4342)), bias));
+}
+__device__ __forceinline__ float tc_ex2(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+// 32 columns of this thread's lane, not waited for.
+__device__ __forceinline__ void tmem_ld32_async(uint32_t taddr, uint32_t (&v)[32]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
+        "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
+        "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+        : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7]),
+          "=r"(v[8]), "=r"(v[9]), "=r"(v[10]), "=r"(v[11]), "=r"(v[12]), "=r"(v[13]), "=r"(v[14]), "=r"(v[15]),
+          "=r"(v[16]), "=r"(v[17]), "=r"(v[18]), "=r"(v[19]), "=r"(v[20]), "=r"(v[21]), "=r"(v[22]), "=r"(v[23]),
+          "=r"(v[24]), "=r"(v[25]), "=r"(v[26]), "=r"(v[27]), "=r"(v[28]), "=r"(v[29]), "=r"(v[30]), "=r"(v[31])
+        : "r"(taddr));
+}
+// The loads' registers may be read behind this (they are operands, so that no use moves ahead of it).
+__device__ __forceinline__ void tmem_ld_wait(uint32_t (&v)[32]) {
+    asm volatile("tcgen05.wait::ld.sync.aligned;"
+                 : "+r"(v[0]), "+r"(v[1]), "+r"(v[2]), "+r"(v[3]), "+r"(v[4]), "+r"(v[5]), "+r"(v[6]), "+r"(v[7]),
+                   "+r"(v[8]), "+r"(v[9]), "+r"(v[10]), "+r"(v[11]), "+r"(v[12]), "+r"(v[13]), "+r"(v[14]), "+r"(v[15]),
+                   "+r"(v[16]), "+r"(v[17]), "+r"(v[18]), "+r"(v[19]), "+r"(v[20]), "+r"(v[21]), "+r"(v[22]), "+r"(v[23]),
+                   "+r"(v[24]), "+r"(v[25]), "+r"(v[26]), "+r"(v[27]), "+r"(v[28]), "+r"(v[29])
+                 :
+                 : "memory");
+    asm volatile("" : "+r"(v[30]), "+r"(v[31]));
+}
+__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&v)[16]) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};"
+        ::"r"(taddr), "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]),
+          "r"(v[8]), "r"(v[9]), "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15])
+        : "memory");
+}
+__device__ __forceinline__ void tmem_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+// One K = 16 step, A in shared memory or in TMEM; issued by one lane of the warp.
+__device__ __forceinline__ void umma_ss_elect(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
+    asm volatile(
+        "{\n\t.reg .pred pe, pa;\n\telect.sync _|pe, 0xffffffff;\n\tsetp.ne.b32 pa, %4, 0;\n\t"
+        "@pe tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, pa;\n\t}" ::"r"(d), "l"(a), "l"(b), "r"(idesc), "r"(acc)
+        : "memory");
+}
+__device__ __forceinline__ void umma_ts_elect(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
+    asm volatile(
+        "{\n\t.reg .pred pe, pa;\n\telect.sync _|pe, 0xffffffff;\n\tsetp.ne.b32 pa, %4, 0;\n\t"
+        "@pe tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, pa;\n\t}" ::"r"(d), "r"(a), "l"(b), "r"(idesc), "r"(acc)
+        : "memory");
+}
+// Byte offset of 16-byte chunk c of row r in the swizzled layout.
+__device__ __forceinline__ uint32_t sw128(int r, int c) {
+    return (uint32_t)((r >> 3) * 1024 + (r & 7) * 128 + ((c ^ (r & 7)) << 4));
+}
+
+template <int D>
+__global__ void __launch_bounds__(kTcThreads, 1) kv_attention_tc_kernel(const __grid_constant__ KvTcArgs a) {
+    using L = KvTc<D>;
+    extern __shared__ __align__(1024) unsigned char raw[];
+    unsigned char* sq = reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~uintptr_t(1023));
+    unsigned char* sk = sq + 2 * L::kQBytes;
+    unsigned char* sv = sk + 2 * L::kKBytes;
+    KvTcShared* sh = reinterpret_cast<KvTcShared*>(sv + 2 * L::kVBytes);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int nbh = a.b.n_seq * a.c.kv_heads;
+    const int tile = a.rt - 1 - (int)(blockIdx.x / nbh);             // the longest rows first
+    const int bh = blockIdx.x % nbh, h = bh % a.c.kv_heads, b = bh / a.c.kv_heads;
+    if (threadIdx.x == 0) {
+        mbar_init(&sh->q_full, 8);
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&sh->kf[i], 4);
+            mbar_init(&sh->ke[i], 1);
+            mbar_init(&sh->vf[i], 4);
+            mbar_init(&sh->ve[i], 1);
+            mbar_init(&sh->s_full[i], 1);
+            mbar_init(&sh->p_full[i], 4);
+            mbar_init(&sh->o_done[i], 1);
+        }
+        fence_mbar_init();
+    }
+    pdl_wait();
+    const KvSeq s = kv_sequence(a.b, b);
+    const int rows = s.nq * a.G, row0 = tile * kTcRows;
+    if (!s.ok && threadIdx.x == 0) record_status(a.status, GLOWQ_ERR_INDEX);
+    if (row0 >= rows) return;
+    // a length that the table or the tails cannot hold: nothing is visible, and the rows are zero
+    const bool tailed = s.len % kKvPage != 0;
+    const bool bad = s.len > (int64_t)a.b.max_pages * kKvPage || (tailed && (s.slot < 0 || s.slot >= a.c.slots));
+    if (bad && threadIdx.x == 0) record_status(a.status, GLOWQ_ERR_INDEX);
+    int nt[2];                                                       // token tiles that each row tile sees
+#pragma unroll
+    for (int t = 0; t < 2; ++t) {
+        const int first = row0 + t * 128, last = min(first + 127, rows - 1);
+        const int seen = bad || first >= rows ? 0 : max(0, s.start + last / a.G + 1);
+        nt[t] = (seen + kTcTokens - 1) / kTcTokens;
+    }
+    const int nmax = max(nt[0], nt[1]);
+    if (warp == 12) tmem_alloc(&sh->tmem, 512);
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = sh->tmem;                                  // S_0, S_1 (128 columns each), O_0, O_1
+    // only now: a kernel that began earlier might take TMEM that a block of this
+    // grid still waits for, and wait for this grid's end itself
+    pdl_launch_dependents();
+    bool ok = true;
+
+    if (warp < 8) {
+        // ---------------- softmax: one thread per row ----------------
+        const int t = warp >> 2, r = (warp & 3) * 32 + lane, row = row0 + t * 128 + r;
+        const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
+        const uint32_t ts = tmem + lanes + (uint32_t)(t * 128), to = tmem + lanes + (uint32_t)(256 + t * 128);
+        const bool there = row < rows;
+        const int64_t qrow = s.q0 + (there ? row / a.G : 0);
+        const int64_t head = (int64_t)(h * a.G + (there ? row % a.G : 0)) * D;
+#pragma unroll
+        for (int c = 0; c < D / 8; ++c) {
+            uint4 v = make_uint4(0, 0, 0, 0);
+            if (there) v = ldcg_128(a.Q + qrow * a.ldQ + head + 8 * c);
+            *reinterpret_cast<uint4*>(sq + t * L::kQBytes + (c >> 3) * 16384 + sw128(r, c & 7)) = v;
+        }
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sh->q_full);
+        const int limit = there ? s.start + row / a.G : -1;
+        const int least = s.start + (row0 + t * 128) / a.G;          // the tile's first row sees least
+        float ref = -INFINITY, l = 0.f;
+        for (int j = 0; j < nt[t]; ++j) {
+            if (ok) ok = mbar_wait(&sh->s_full[t], j & 1, a.status);
+            tc_fence_after();
+            const KvTcMeta& mt = sh->meta[j % kTcMeta];
+            const float sa[2] = {mt.a[0], mt.a[1]}, slv[2] = {mt.lv[0], mt.lv[1]};
+            const bool poisoned = (mt.poison[0] | mt.poison[1] | mt.poison[2] | mt.poison[3]) != 0u;
+            const bool masked = poisoned || row0 + t * 128 + 128 > rows || least < j * kTcTokens + kTcTokens - 1 ||
+                                mt.valid[0] < kKvPage || mt.valid[1] < kKvPage;
+            // tokens of each page that this row sees
+            const int see0 = min(mt.valid[0], limit - j * kTcTokens + 1), see1 = min(mt.valid[1], limit - j * kTcTokens - kKvPage + 1);
+            float cand = -INFINITY;
+            {
+                uint32_t v[2][32];
+                tmem_ld32_async(ts, v[0]);
+#pragma unroll
+                for (int c = 0; c < 4; ++c) {
+                    tmem_ld_wait(v[c & 1]);
+                    if (c < 3) tmem_ld32_async(ts + (c + 1) * 32, v[(c + 1) & 1]);
+                    float mx = -INFINITY;
+                    if (!masked) {
+#pragma unroll
+                        for (int i = 0; i < 32; ++i) mx = fmaxf(mx, __uint_as_float(v[c & 1][i]));
+                        cand = fmaxf(cand, fmaf(mx, sa[c >> 1], slv[c >> 1]));
+                    } else {
+                        const int see = (c < 2 ? see0 : see1) - (c & 1) * 32;
+#pragma unroll
+                        for (int i = 0; i < 32; ++i)
+                            if (i < see) cand = fmaxf(cand, fmaf(__uint_as_float(v[c & 1][i]), sa[c >> 1], slv[c >> 1]));
+                    }
+                }
+            }
+            if (__any_sync(~0u, cand > ref + kTcSlack || (ref == -INFINITY && cand > -INFINITY))) {
+                const float next = fmaxf(ref, cand);
+                if (j > 0) {
+                    const float f = ref == next ? 1.f : tc_ex2(ref - next);
+                    if (ok) ok = mbar_wait(&sh->o_done[t], (j - 1) & 1, a.status);
+                    tc_fence_after();
+#pragma unroll
+                    for (int c = 0; c < D / 32; ++c) {
+                        uint32_t v[32];
+                        tmem_ld32_async(to + c * 32, v);
+                        tmem_ld_wait(v);
+#pragma unroll
+                        for (int i = 0; i < 32; ++i) v[i] = __float_as_uint(__uint_as_float(v[i]) * f);
+                        tmem_st32(to + c * 32, v);
+                    }
+                    l *= f;
+                }
+                ref = next;
+            }
+            const float base = (ref == -INFINITY ? 0.f : ref) - kTcWeightExp;
+            const float sc[2] = {slv[0] - base, slv[1] - base};
+            float sum[2] = {0.f, 0.f};
+            {
+                uint32_t v[2][32];
+                tmem_ld32_async(ts, v[0]);
+#pragma unroll
+                for (int c = 0; c < 4; ++c) {
+                    tmem_ld_wait(v[c & 1]);
+                    if (c < 3) tmem_ld32_async(ts + (c + 1) * 32, v[(c + 1) & 1]);
+                    uint32_t p[16];
+                    float s0 = 0.f, s1 = 0.f;
+                    if (!masked) {
+#pragma unroll
+                        for (int i = 0; i < 16; ++i) {
+                            const float w0 = tc_ex2(fmaf(__uint_as_float(v[c & 1][2 * i]), sa[c >> 1], sc[c >> 1]));
+                            const float w1 = tc_ex2(fmaf(__uint_as_float(v[c & 1][2 * i + 1]), sa[c >> 1], sc[c >> 1]));
+                            s0 += w0;
+                            s1 += w1;
+                            p[i] = h2_as_u32(__floats2half2_rn(w0, w1));
+                        }
+                    } else {
+                        const int see = (c < 2 ? see0 : see1) - (c & 1) * 32;
+                        const unsigned int bits = mt.poison[c];
+#pragma unroll
+                        for (int i = 0; i < 16; ++i) {
+                            float w[2];
+#pragma unroll
+                            for (int e = 0; e < 2; ++e) {
+                                w[e] = tc_ex2(fmaf(__uint_as_float(v[c & 1][2 * i + e]), sa[c >> 1], sc[c >> 1]));
+                                if ((bits >> (2 * i + e)) & 1u) w[e] = __int_as_float(0x7fffffff);
+                                if (2 * i + e >= see) w[e] = 0.f;
+                            }
+                            s0 += w[0];
+                            s1 += w[1];
+                            p[i] = h2_as_u32(__floats2half2_rn(w[0], w[1]));
+                        }
+                    }
+                    sum[c >> 1] += s0 + s1;
+                    tmem_st16(ts + c * 16, p);           // columns 16 c ..: read (as scores) by this chunk or an earlier one
+                }
+            }
+            // a row that sees nothing of a page takes nothing from its scale (which may be NaN)
+            if (sum[0] != 0.f) l += sum[0] * mt.inv[0];
+            if (sum[1] != 0.f) l += sum[1] * mt.inv[1];
+            tmem_st_wait();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&sh->p_full[t]);
+        }
+        if (nt[t] > 0) {
+            if (ok) ok = mbar_wait(&sh->o_done[t], (nt[t] - 1) & 1, a.status);
+            tc_fence_after();
+        }
+        const float inv = l == 0.f ? 0.f : 1.f / l;                  // a row that sees nothing is zero
+#pragma unroll
+        for (int c = 0; c < D / 32; ++c) {
+            uint32_t v[32];
+            if (nt[t] > 0) {
+                tmem_ld32_async(to + c * 32, v);
+                tmem_ld_wait(v);
+            }
+            if (there) {
+#pragma unroll
+                for (int i = 0; i < 32; i += 8) {
+                    uint4 y = make_uint4(0, 0, 0, 0);
+                    if (nt[t] > 0 && l != 0.f) {
+                        y.x = h2_as_u32(__floats2half2_rn(__uint_as_float(v[i]) * inv, __uint_as_float(v[i + 1]) * inv));
+                        y.y = h2_as_u32(__floats2half2_rn(__uint_as_float(v[i + 2]) * inv, __uint_as_float(v[i + 3]) * inv));
+                        y.z = h2_as_u32(__floats2half2_rn(__uint_as_float(v[i + 4]) * inv, __uint_as_float(v[i + 5]) * inv));
+                        y.w = h2_as_u32(__floats2half2_rn(__uint_as_float(v[i + 6]) * inv, __uint_as_float(v[i + 7]) * inv));
+                    }
+                    *reinterpret_cast<uint4*>(a.Y + qrow * a.ldY + head + c * 32 + i) = y;
+                }
+            }
+        }
+    } else if (warp < 12) {
+        // ---------------- pages to operands (128 threads) ----------------
+        const int tid = threadIdx.x - 256;
+        const int full = s.len / kKvPage, ntok = s.len - full * kKvPage;
+        const int64_t tail = ((int64_t)s.slot * a.c.kv_heads + h) * kKvPage * D;
+        const int* table = a.b.table + (int64_t)b * a.b.max_pages;
+        constexpr int kPieces = kKvPage * D / 16 / 128;              // 16-byte pieces of a page's K (or V) per thread
+        // kind of page p: its id, -1 absent (or out of range), -2 the tail
+        auto page_of = [&](int p) -> int {
+            if (p < full) {
+                const int id = ldcg_s32(table + p);
+                if (id >= 0 && id < a.c.pages) return id;
+                if (tid == 0) record_status(a.status, GLOWQ_ERR_INDEX);
+                return -1;
+            }
+            return p == full && ntok > 0 ? -2 : -1;
+        };
+        auto codes_to = [&](const uint4& u, unsigned char* panel, int row, int c) {
+            const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+            uint32_t o[8];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) tc_cvt_codes(w[i], o[2 * i], o[2 * i + 1]);
+            *reinterpret_cast<uint4*>(panel + sw128(row, 2 * c)) = make_uint4(o[0], o[1], o[2], o[3]);
+            *reinterpret_cast<uint4*>(panel + sw128(row, 2 * c + 1)) = make_uint4(o[4], o[5], o[6], o[7]);
+        };
+        // the tail's piece i: 8 dimensions of a token; tokens past the end are zero
+        auto tail_piece = [&](const uint16_t* src, int i) {
+            const int tok = i / (D / 8), c = i % (D / 8);
+            return tok < ntok ? ldcg_128(src + tail + (int64_t)tok * D + 8 * c) : make_uint4(0, 0, 0, 0);
+        };
+        for (int j = 0; j < nmax; ++j) {
+            const int st = j & 1;
+            int id[2];
+            uint4 kc[2][kPieces], vc[2][kPieces];
+#pragma unroll
+            for (int q = 0; q < 2; ++q) {
+                id[q] = page_of(2 * j + q);
+                if (id[q] >= 0) {
+                    const int64_t at = ((int64_t)id[q] * a.c.kv_heads + h) * kKvPage * D;
+#pragma unroll
+                    for (int i = 0; i < kPieces; ++i) {
+                        kc[q][i] = ldcg_128(a.c.k_codes + at + (tid + i * 128) * 16);
+                        vc[q][i] = ldcg_128(a.c.v_codes + at + (tid + i * 128) * 16);
+                    }
+                }
+            }
+            KvTcMeta& mt = sh->meta[j % kTcMeta];
+            if (tid < 2) {
+                const int p = id[tid];
+                float ks = 0.f, vs = 1.f;
+                if (p >= 0) {
+                    ks = ldcg_f32(a.c.k_scales + (int64_t)p * a.c.kv_heads + h);
+                    vs = ldcg_f32(a.c.v_scales + (int64_t)p * a.c.kv_heads + h);
+                }
+                mt.a[tid] = p == -2 ? a.scale_log2 : ks * a.scale_log2;
+                mt.lv[tid] = log2f(vs);
+                mt.inv[tid] = 1.f / vs;
+                mt.valid[tid] = p >= 0 ? kKvPage : p == -2 ? ntok : 0;
+                mt.poison[2 * tid] = mt.poison[2 * tid + 1] = 0u;
+            }
+            __half2 up = __half2half2(__ushort_as_half(0x3c00));     // the tail's power of two (attention.cu)
+            if (id[0] == -2 || id[1] == -2) {
+                const int q = id[0] == -2 ? 0 : 1;
+                if (tid == 0) sh->tail_max = sh->tail_poison[0] = sh->tail_poison[1] = 0u;
+                named_barrier_sync(1, 128);
+                __half2 am = __half2half2(__ushort_as_half(0));
+                for (int i = tid; i < kKvPage * D / 8; i += 128) {
+                    const uint4 u = tail_piece(a.c.v_tail, i);
+                    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        uint32_t x = w[e];
+                        const bool lo = (x & 0x7c00u) == 0x7c00u, hi = (x & 0x7c000000u) == 0x7c000000u;
+                        if (lo) x &= 0xffff0000u;
+                        if (hi) x &= 0x0000ffffu;
+                        if (lo || hi) atomicOr(&sh->tail_poison[i / (D / 8) >> 5], 1u << (i / (D / 8) & 31));
+                        am = __hmax2(am, __habs2(u32_as_h2(x)));
+                    }
+                }
+                atomicMax(&sh->tail_max, max(h2_as_u32(am) & 0x7c00u, (h2_as_u32(am) >> 16) & 0x7c00u) >> 10);
+                named_barrier_sync(1, 128);
+                const int k2 = min(15, 21 - (int)sh->tail_max);
+                up = __half2half2(__ushort_as_half((unsigned short)((k2 + 15) << 10)));
+                if (tid == 0) {
+                    mt.lv[q] = (float)-k2;
+                    mt.inv[q] = exp2f((float)k2);
+                    mt.poison[2 * q] = sh->tail_poison[0];
+                    mt.poison[2 * q + 1] = sh->tail_poison[1];
+                }
+            }
+            // ---- K ----
+            if (j >= 2 && ok) ok = mbar_wait(&sh->ke[st], ((j >> 1) - 1) & 1, a.status);
+            unsigned char* kd = sk + st * L::kKBytes;
+#pragma unroll
+            for (int q = 0; q < 2; ++q) {
+                if (id[q] >= 0) {
+#pragma unroll
+                    for (int i = 0; i < kPieces; ++i) {              // piece: panel, token, quarter of the 64 dimensions
+                        const int x = tid + i * 128;
+                        codes_to(kc[q][i], kd + (x >> 8) * 16384, q * kKvPage + ((x >> 2) & 63), x & 3);
+                    }
+                } else {
+                    for (int i = tid; i < kKvPage * D / 8; i += 128) {
+                        const int tok = i / (D / 8), c = i % (D / 8);
+                        const uint4 u = id[q] == -2 ? tail_piece(a.c.k_tail, i) : make_uint4(0, 0, 0, 0);
+                        *reinterpret_cast<uint4*>(kd + (c >> 3) * 16384 + sw128(q * kKvPage + tok, c & 7)) = u;
+                    }
+                }
+            }
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&sh->kf[st]);
+            // ---- V ----
+            if (j >= 2 && ok) ok = mbar_wait(&sh->ve[st], ((j >> 1) - 1) & 1, a.status);
+            unsigned char* vd = sv + st * L::kVBytes;
+#pragma unroll
+            for (int q = 0; q < 2; ++q) {
+                unsigned char* page = vd + q * D * 128;
+                if (id[q] >= 0) {
+#pragma unroll
+                    for (int i = 0; i < kPieces; ++i) {              // piece: dimension, quarter of the 64 tokens
+                        const int x = tid + i * 128;
+                        codes_to(vc[q][i], page, x >> 2, x & 3);
+                    }
+                } else if (id[q] == -2) {
+                    for (int i = tid; i < kKvPage * D / 8; i += 128) {
+                        const int tok = i / (D / 8), dim = i % (D / 8) * 8;
+                        const uint4 u = tail_piece(a.c.v_tail, i);
+                        uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            if ((w[e] & 0x7c00u) == 0x7c00u) w[e] &= 0xffff0000u;
+                            if ((w[e] & 0x7c000000u) == 0x7c000000u) w[e] &= 0x0000ffffu;
+                            const __half2 x = __hmul2(u32_as_h2(w[e]), up);
+                            *reinterpret_cast<__half*>(page + sw128(dim + 2 * e, tok >> 3) + (tok & 7) * 2) = __low2half(x);
+                            *reinterpret_cast<__half*>(page + sw128(dim + 2 * e + 1, tok >> 3) + (tok & 7) * 2) = __high2half(x);
+                        }
+                    }
+                } else {
+                    for (int i = tid; i < D * 8; i += 128) *reinterpret_cast<uint4*>(page + i * 16) = make_uint4(0, 0, 0, 0);
+                }
+            }
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&sh->vf[st]);
+        }
+    } else if (warp == 12 && nmax > 0) {
+        // ---------------- MMA issuer (the whole warp; one lane issues) ----------------
+        const uint32_t ids = f16_idesc(128, kTcTokens), ido = f16_idesc(128, D);
+        const uint64_t qd = sw128_kmajor_desc(smem_u32(sq)), kd = sw128_kmajor_desc(smem_u32(sk)), vd = sw128_kmajor_desc(smem_u32(sv));
+        auto qk = [&](int t, int st) {
+#pragma unroll
+            for (int k = 0; k < D / 16; ++k) {                       // panels of 64 dimensions 16 KB apart
+                const uint64_t off = (uint64_t)((k >> 2) * 1024 + (k & 3) * 2);
+                umma_ss_elect(tmem + (uint32_t)(t * 128), qd + (uint64_t)(t * (L::kQBytes >> 4)) + off,
+                              kd + (uint64_t)(st * (L::kKBytes >> 4)) + off, ids, k > 0);
+            }
+            umma_commit_elect(smem_u32(&sh->s_full[t]));
+        };
+        ok = mbar_wait_warp(smem_u32(&sh->q_full), 0, a.status);
+        if (ok) ok = mbar_wait_warp(smem_u32(&sh->kf[0]), 0, a.status);
+        tc_fence_after();
+        for (int t = 0; t < 2; ++t)
+            if (nt[t] > 0) qk(t, 0);
+        umma_commit_elect(smem_u32(&sh->ke[0]));
+        for (int j = 0; j < nmax; ++j) {
+            const int st = j & 1, sn = st ^ 1;
+            if (ok) ok = mbar_wait_warp(smem_u32(&sh->vf[st]), (j >> 1) & 1, a.status);
+            if (j + 1 < nmax && ok) ok = mbar_wait_warp(smem_u32(&sh->kf[sn]), ((j + 1) >> 1) & 1, a.status);
+            for (int t = 0; t < 2; ++t) {
+                if (j >= nt[t]) continue;
+                if (ok) ok = mbar_wait_warp(smem_u32(&sh->p_full[t]), j & 1, a.status);
+                tc_fence_after();
+#pragma unroll
+                for (int k = 0; k < kTcTokens / 16; ++k)             // pages of 64 tokens D rows apart
+                    umma_ts_elect(tmem + (uint32_t)(256 + t * 128), tmem + (uint32_t)(t * 128 + k * 8),
+                                  vd + (uint64_t)(st * (L::kVBytes >> 4) + (k >> 2) * (D * 8) + (k & 3) * 2), ido, j > 0 || k > 0);
+                umma_commit_elect(smem_u32(&sh->o_done[t]));
+                if (j + 1 < nt[t]) qk(t, sn);
+            }
+            umma_commit_elect(smem_u32(&sh->ve[st]));
+            if (j + 1 < nmax) umma_commit_elect(smem_u32(&sh->ke[sn]));
+        }
+        // the last commits land before the block may exit
+        for (int j = (nmax > 2 ? nmax - 2 : 0); j < nmax; ++j) {
+            if (ok) ok = mbar_wait_warp(smem_u32(&sh->ke[j & 1]), (j >> 1) & 1, a.status);
+            if (ok) ok = mbar_wait_warp(smem_u32(&sh->ve[j & 1]), (j >> 1) & 1, a.status);
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    if (warp == 12) tmem_dealloc(tmem, 512);
+}
+
+template <int D>
+static cudaError_t launch_tc(const KvTcArgs& a, unsigned grid, cudaStream_t st) {
+    cudaError_t e = cudaFuncSetAttribute((const void*)kv_attention_tc_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                         KvTc<D>::kSmem);
+    if (e != cudaSuccess) return e;
+    void* args[] = {(void*)&a};
+    return launch_pdl((const void*)kv_attention_tc_kernel<D>, grid, kTcThreads, KvTc<D>::kSmem, st, args);
+}
+
+int64_t kv_tc_blocks(const KvBatchView& b, int G, int kv_heads) {
+    return ((int64_t)b.max_new * G + kTcRows - 1) / kTcRows * b.n_seq * kv_heads;
+}
+cudaError_t launch_kv_attention_tc(const KvCacheView& c, const KvBatchView& b, const uint16_t* Q, int64_t ldQ, int q_heads,
+                                   float scale, uint16_t* Y, int64_t ldY, cudaStream_t st) {
+    const int G = q_heads / c.kv_heads;
+    const KvTcArgs a = {c, b, Q, Y, ldQ, ldY, scale * 1.44269504088896340736f, G,
+                        (int)(((int64_t)b.max_new * G + kTcRows - 1) / kTcRows), device_status_ptr()};
+    const unsigned grid = (unsigned)kv_tc_blocks(b, G, c.kv_heads);
+    return c.head_dim == 64 ? launch_tc<64>(a, grid, st) : launch_tc<128>(a, grid, st);
+}
+
+}  // namespace glowq

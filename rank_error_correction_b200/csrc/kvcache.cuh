@@ -57,6 +57,7 @@ cudaError_t launch_kv_read(const KvCacheView& c, const KvBatchView& b, const int
 
 // attention.cu
 struct KvAttnPlan {
+    bool tc;             // many rows: attention_tc.cu
     int rt;              // 16-row tiles of the widest sequence
     int S;               // CTAs that share a tile's pages
     size_t partial_bytes;
@@ -65,5 +66,10 @@ KvAttnPlan plan_kv_attention(const KvBatchView& b, int G, int kv_heads, int head
 cudaError_t launch_kv_attention(const KvCacheView& c, const KvBatchView& b, const uint16_t* Q, int64_t ldQ, int q_heads,
                                 float scale, uint16_t* Y, int64_t ldY, unsigned int* tickets, float* partial,
                                 const KvAttnPlan& p, cudaStream_t st);
+
+// attention_tc.cu: many rows on the tensor cores (no workspace)
+int64_t kv_tc_blocks(const KvBatchView& b, int G, int kv_heads);
+cudaError_t launch_kv_attention_tc(const KvCacheView& c, const KvBatchView& b, const uint16_t* Q, int64_t ldQ, int q_heads,
+                                   float scale, uint16_t* Y, int64_t ldY, cudaStream_t st);
 
 }  // namespace glowq
