@@ -43,10 +43,10 @@ struct KvTcMeta {
     float lv[2];             // log2 s_V
     float inv[2];            // 1 / s_V
     int valid[2];            // tokens present
-    unsigned int poison[4];  // tokens (of 128) whose value is not finite
 };
 struct __align__(8) KvTcShared {
     uint64_t q_full, kf[2], ke[2], vf[2], ve[2], s_full[2], p_full[2], o_done[2];
+    uint64_t codes[2];                   // the staged codes of K, of V
     KvTcMeta meta[kTcMeta];
     unsigned int tail_max, tail_poison[2];
     uint32_t tmem;
@@ -58,7 +58,9 @@ struct KvTc {
     static constexpr int kQBytes = 128 * D * 2;          // one row tile: panels of [128 rows][128 B]
     static constexpr int kKBytes = kTcTokens * D * 2;    // panels of [128 tokens][128 B]
     static constexpr int kVBytes = 2 * D * 128;          // pages of [D][128 B]
-    static constexpr int kSmem = 2 * kQBytes + 2 * kKBytes + 2 * kVBytes + (int)sizeof(KvTcShared) + 1024;
+    static constexpr int kCodes = 2 * kKvPage * D;       // one tile's K (or V) codes
+    static constexpr int kSmem = 2 * kQBytes + 2 * kKBytes + 2 * kVBytes + 2 * kCodes + (int)sizeof(KvTcShared) + 1024;
+    static_assert(kSmem <= 232448, "shared memory per block");
 };
 
 __device__ __forceinline__ void tc_cvt_codes(uint32_t w, uint32_t& lo, uint32_t& hi) {
@@ -103,6 +105,28 @@ __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&v)[16
         : "memory");
 }
 __device__ __forceinline__ void tmem_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+// Pairs of fp32 in one register pair, and the largest of three.
+__device__ __forceinline__ uint64_t pack_f2(float x, float y) {
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(x), "f"(y));
+    return r;
+}
+__device__ __forceinline__ void unpack_f2(uint64_t v, float& x, float& y) { asm("mov.b64 {%0, %1}, %2;" : "=f"(x), "=f"(y) : "l"(v)); }
+__device__ __forceinline__ uint64_t fma_f2(uint64_t a, uint64_t b, uint64_t c) {
+    uint64_t r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+__device__ __forceinline__ uint64_t add_f2(uint64_t a, uint64_t b) {
+    uint64_t r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ float max3(float a, float b, float c) {
+    float r;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+    return r;
+}
 // One K = 16 step, A in shared memory or in TMEM; issued by one lane of the warp.
 __device__ __forceinline__ void umma_ss_elect(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
     asm volatile(
@@ -128,7 +152,8 @@ __global__ void __launch_bounds__(kTcThreads, 1) kv_attention_tc_kernel(const __
     unsigned char* sq = reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~uintptr_t(1023));
     unsigned char* sk = sq + 2 * L::kQBytes;
     unsigned char* sv = sk + 2 * L::kKBytes;
-    KvTcShared* sh = reinterpret_cast<KvTcShared*>(sv + 2 * L::kVBytes);
+    unsigned char* sc = sv + 2 * L::kVBytes;
+    KvTcShared* sh = reinterpret_cast<KvTcShared*>(sc + 2 * L::kCodes);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int nbh = a.b.n_seq * a.c.kv_heads;
     const int tile = a.rt - 1 - (int)(blockIdx.x / nbh);             // the longest rows first
@@ -143,6 +168,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) kv_attention_tc_kernel(const __
             mbar_init(&sh->s_full[i], 1);
             mbar_init(&sh->p_full[i], 4);
             mbar_init(&sh->o_done[i], 1);
+            mbar_init(&sh->codes[i], 1);
         }
         fence_mbar_init();
     }
@@ -181,11 +207,16 @@ __global__ void __launch_bounds__(kTcThreads, 1) kv_attention_tc_kernel(const __
         const bool there = row < rows;
         const int64_t qrow = s.q0 + (there ? row / a.G : 0);
         const int64_t head = (int64_t)(h * a.G + (there ? row % a.G : 0)) * D;
+        {
+            uint4 v[D / 8];                              // every load in flight before the first store
 #pragma unroll
-        for (int c = 0; c < D / 8; ++c) {
-            uint4 v = make_uint4(0, 0, 0, 0);
-            if (there) v = ldcg_128(a.Q + qrow * a.ldQ + head + 8 * c);
-            *reinterpret_cast<uint4*>(sq + t * L::kQBytes + (c >> 3) * 16384 + sw128(r, c & 7)) = v;
+            for (int c = 0; c < D / 8; ++c) {
+                v[c] = make_uint4(0, 0, 0, 0);
+                if (there) v[c] = ldcg_128(a.Q + qrow * a.ldQ + head + 8 * c);
+            }
+#pragma unroll
+            for (int c = 0; c < D / 8; ++c)
+                *reinterpret_cast<uint4*>(sq + t * L::kQBytes + (c >> 3) * 16384 + sw128(r, c & 7)) = v[c];
         }
         fence_proxy_async_smem();
         __syncwarp();
@@ -197,32 +228,35 @@ __global__ void __launch_bounds__(kTcThreads, 1) kv_attention_tc_kernel(const __
             if (ok) ok = mbar_wait(&sh->s_full[t], j & 1, a.status);
             tc_fence_after();
             const KvTcMeta& mt = sh->meta[j % kTcMeta];
-            const float sa[2] = {mt.a[0], mt.a[1]}, slv[2] = {mt.lv[0], mt.lv[1]};
-            const bool poisoned = (mt.poison[0] | mt.poison[1] | mt.poison[2] | mt.poison[3]) != 0u;
-            const bool masked = poisoned || row0 + t * 128 + 128 > rows || least < j * kTcTokens + kTcTokens - 1 ||
-                                mt.valid[0] < kKvPage || mt.valid[1] < kKvPage;
             // tokens of each page that this row sees
-            const int see0 = min(mt.valid[0], limit - j * kTcTokens + 1), see1 = min(mt.valid[1], limit - j * kTcTokens - kKvPage + 1);
-            float cand = -INFINITY;
-            {
-                uint32_t v[2][32];
-                tmem_ld32_async(ts, v[0]);
+            const int see[2] = {min(mt.valid[0], limit - j * kTcTokens + 1), min(mt.valid[1], limit - j * kTcTokens - kKvPage + 1)};
+            const bool masked = row0 + t * 128 + 128 > rows || least < j * kTcTokens + kTcTokens - 1 ||
+                                mt.valid[0] < kKvPage || mt.valid[1] < kKvPage;
+            // a page of which the row sees nothing: any finite scale (its own may be NaN)
+            const float sa[2] = {see[0] > 0 ? mt.a[0] : 1.f, see[1] > 0 ? mt.a[1] : 1.f};
+            const float slv[2] = {see[0] > 0 ? mt.lv[0] : 0.f, see[1] > 0 ? mt.lv[1] : 0.f};
+            // 64 scores of page q (compact code: the loops over pages stay rolled)
+            auto scores = [&](int q, uint32_t (&v)[2][32]) {
+                tmem_ld32_async(ts + q * 64, v[0]);
+                tmem_ld32_async(ts + q * 64 + 32, v[1]);
+                tmem_ld_wait(v[0]);
+                tmem_ld_wait(v[1]);
+                if (masked) {                            // (the scales are above zero: -inf stays)
+                    const int n = q == 0 ? see[0] : see[1];
 #pragma unroll
-                for (int c = 0; c < 4; ++c) {
-                    tmem_ld_wait(v[c & 1]);
-                    if (c < 3) tmem_ld32_async(ts + (c + 1) * 32, v[(c + 1) & 1]);
-                    float mx = -INFINITY;
-                    if (!masked) {
-#pragma unroll
-                        for (int i = 0; i < 32; ++i) mx = fmaxf(mx, __uint_as_float(v[c & 1][i]));
-                        cand = fmaxf(cand, fmaf(mx, sa[c >> 1], slv[c >> 1]));
-                    } else {
-                        const int see = (c < 2 ? see0 : see1) - (c & 1) * 32;
-#pragma unroll
-                        for (int i = 0; i < 32; ++i)
-                            if (i < see) cand = fmaxf(cand, fmaf(__uint_as_float(v[c & 1][i]), sa[c >> 1], slv[c >> 1]));
-                    }
+                    for (int i = 0; i < 64; ++i) v[i >> 5][i & 31] = i < n ? v[i >> 5][i & 31] : 0xff800000u;
                 }
+            };
+            float cand = -INFINITY;
+#pragma unroll 1
+            for (int q = 0; q < 2; ++q) {
+                uint32_t v[2][32];
+                scores(q, v);
+                float m[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+                for (int i = 0; i < 32; ++i)
+                    m[i & 3] = max3(m[i & 3], __uint_as_float(v[i >> 4][2 * (i & 15)]), __uint_as_float(v[i >> 4][2 * (i & 15) + 1]));
+                cand = fmaxf(cand, fmaf(fmaxf(fmaxf(m[0], m[1]), fmaxf(m[2], m[3])), q == 0 ? sa[0] : sa[1], q == 0 ? slv[0] : slv[1]));
             }
             if (__any_sync(~0u, cand > ref + kTcSlack || (ref == -INFINITY && cand > -INFINITY))) {
                 const float next = fmaxf(ref, cand);
@@ -230,7 +264,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) kv_attention_tc_kernel(const __
                     const float f = ref == next ? 1.f : tc_ex2(ref - next);
                     if (ok) ok = mbar_wait(&sh->o_done[t], (j - 1) & 1, a.status);
                     tc_fence_after();
-#pragma unroll
+#pragma unroll 1
                     for (int c = 0; c < D / 32; ++c) {
                         uint32_t v[32];
                         tmem_ld32_async(to + c * 32, v);
@@ -244,50 +278,33 @@ __global__ void __launch_bounds__(kTcThreads, 1) kv_attention_tc_kernel(const __
                 ref = next;
             }
             const float base = (ref == -INFINITY ? 0.f : ref) - kTcWeightExp;
-            const float sc[2] = {slv[0] - base, slv[1] - base};
-            float sum[2] = {0.f, 0.f};
-            {
+#pragma unroll 1
+            for (int q = 0; q < 2; ++q) {
                 uint32_t v[2][32];
-                tmem_ld32_async(ts, v[0]);
+                scores(q, v);
+                const float sq_ = q == 0 ? sa[0] : sa[1], off = (q == 0 ? slv[0] : slv[1]) - base;
+                const uint64_t a2 = pack_f2(sq_, sq_), o2 = pack_f2(off, off);
+                uint64_t s2 = 0ull, s3 = 0ull;
 #pragma unroll
-                for (int c = 0; c < 4; ++c) {
-                    tmem_ld_wait(v[c & 1]);
-                    if (c < 3) tmem_ld32_async(ts + (c + 1) * 32, v[(c + 1) & 1]);
+                for (int c = 0; c < 2; ++c) {
                     uint32_t p[16];
-                    float s0 = 0.f, s1 = 0.f;
-                    if (!masked) {
 #pragma unroll
-                        for (int i = 0; i < 16; ++i) {
-                            const float w0 = tc_ex2(fmaf(__uint_as_float(v[c & 1][2 * i]), sa[c >> 1], sc[c >> 1]));
-                            const float w1 = tc_ex2(fmaf(__uint_as_float(v[c & 1][2 * i + 1]), sa[c >> 1], sc[c >> 1]));
-                            s0 += w0;
-                            s1 += w1;
-                            p[i] = h2_as_u32(__floats2half2_rn(w0, w1));
-                        }
-                    } else {
-                        const int see = (c < 2 ? see0 : see1) - (c & 1) * 32;
-                        const unsigned int bits = mt.poison[c];
-#pragma unroll
-                        for (int i = 0; i < 16; ++i) {
-                            float w[2];
-#pragma unroll
-                            for (int e = 0; e < 2; ++e) {
-                                w[e] = tc_ex2(fmaf(__uint_as_float(v[c & 1][2 * i + e]), sa[c >> 1], sc[c >> 1]));
-                                if ((bits >> (2 * i + e)) & 1u) w[e] = __int_as_float(0x7fffffff);
-                                if (2 * i + e >= see) w[e] = 0.f;
-                            }
-                            s0 += w[0];
-                            s1 += w[1];
-                            p[i] = h2_as_u32(__floats2half2_rn(w[0], w[1]));
-                        }
+                    for (int i = 0; i < 16; ++i) {
+                        float e0, e1;
+                        unpack_f2(fma_f2(pack_f2(__uint_as_float(v[c][2 * i]), __uint_as_float(v[c][2 * i + 1])), a2, o2), e0, e1);
+                        const float w0 = tc_ex2(e0), w1 = tc_ex2(e1);
+                        if (i & 1) s3 = add_f2(s3, pack_f2(w0, w1));
+                        else s2 = add_f2(s2, pack_f2(w0, w1));
+                        p[i] = h2_as_u32(__floats2half2_rn(w0, w1));
                     }
-                    sum[c >> 1] += s0 + s1;
-                    tmem_st16(ts + c * 16, p);           // columns 16 c ..: read (as scores) by this chunk or an earlier one
+                    tmem_st16(ts + q * 32 + c * 16, p);  // columns whose scores this page or the one before has read
                 }
+                float s0, s1;
+                unpack_f2(add_f2(s2, s3), s0, s1);
+                const float sum = s0 + s1;
+                // a row that sees nothing of a page takes nothing from its scale (which may be NaN)
+                if (sum != 0.f) l += sum * mt.inv[q];
             }
-            // a row that sees nothing of a page takes nothing from its scale (which may be NaN)
-            if (sum[0] != 0.f) l += sum[0] * mt.inv[0];
-            if (sum[1] != 0.f) l += sum[1] * mt.inv[1];
             tmem_st_wait();
             tc_fence_before();
             __syncwarp();
@@ -336,48 +353,71 @@ __global__ void __launch_bounds__(kTcThreads, 1) kv_attention_tc_kernel(const __
             }
             return p == full && ntok > 0 ? -2 : -1;
         };
-        auto codes_to = [&](const uint4& u, unsigned char* panel, int row, int c) {
+        // 16 codes -> 32 bytes of a swizzled row; a thread's pieces of a page are 32
+        // rows apart, 4 KB in the layout, with the same chunks
+        const uint32_t out0 = sw128(tid >> 2, 2 * (tid & 3)), out1 = sw128(tid >> 2, 2 * (tid & 3) + 1);
+        auto codes_to = [&](const uint4& u, unsigned char* at) {
             const uint32_t w[4] = {u.x, u.y, u.z, u.w};
             uint32_t o[8];
 #pragma unroll
             for (int i = 0; i < 4; ++i) tc_cvt_codes(w[i], o[2 * i], o[2 * i + 1]);
-            *reinterpret_cast<uint4*>(panel + sw128(row, 2 * c)) = make_uint4(o[0], o[1], o[2], o[3]);
-            *reinterpret_cast<uint4*>(panel + sw128(row, 2 * c + 1)) = make_uint4(o[4], o[5], o[6], o[7]);
+            *reinterpret_cast<uint4*>(at + out0) = make_uint4(o[0], o[1], o[2], o[3]);
+            *reinterpret_cast<uint4*>(at + out1) = make_uint4(o[4], o[5], o[6], o[7]);
         };
-        // the tail's piece i: 8 dimensions of a token; tokens past the end are zero
-        auto tail_piece = [&](const uint16_t* src, int i) {
-            const int tok = i / (D / 8), c = i % (D / 8);
-            return tok < ntok ? ldcg_128(src + tail + (int64_t)tok * D + 8 * c) : make_uint4(0, 0, 0, 0);
+        // the codes of a tile's K (which = 0) or V, staged ahead by bulk copies of one thread
+        auto stage_codes = [&](int which, const int (&id)[2]) {
+            if (tid != 0) return;
+            mbar_arrive_expect_tx(&sh->codes[which], (uint32_t)(((id[0] >= 0) + (id[1] >= 0)) * kKvPage * D));
+#pragma unroll
+            for (int q = 0; q < 2; ++q)
+                if (id[q] >= 0)
+                    bulk_g2s(smem_u32(sc + which * L::kCodes + q * kKvPage * D),
+                             (which ? a.c.v_codes : a.c.k_codes) + ((int64_t)id[q] * a.c.kv_heads + h) * kKvPage * D,
+                             kKvPage * D, &sh->codes[which]);
         };
+        // this thread's pieces of the tail (8 dimensions of a token each), all loads in
+        // flight; tokens past the end are zero
+        constexpr int kTail = kKvPage * D / 8 / 128;
+        auto tail_pieces = [&](const uint16_t* src, uint4 (&u)[kTail]) {
+#pragma unroll
+            for (int i = 0; i < kTail; ++i) {
+                const int x = tid + i * 128, tok = x / (D / 8), c = x % (D / 8);
+                u[i] = make_uint4(0, 0, 0, 0);
+                if (tok < ntok) u[i] = ldcg_128(src + tail + (int64_t)tok * D + 8 * c);
+            }
+        };
+        int id[2] = {page_of(0), page_of(1)};
+        float ks = 0.f, vs = 1.f;                        // thread q < 2: the scales of page q
+        auto scales_of = [&](const int (&id)[2], float& k, float& v) {
+            k = 0.f;
+            v = 1.f;
+            if (tid < 2 && id[tid] >= 0) {
+                k = ldcg_f32(a.c.k_scales + (int64_t)id[tid] * a.c.kv_heads + h);
+                v = ldcg_f32(a.c.v_scales + (int64_t)id[tid] * a.c.kv_heads + h);
+            }
+        };
+        if (nmax > 0) {
+            stage_codes(0, id);
+            stage_codes(1, id);
+            scales_of(id, ks, vs);
+        }
         for (int j = 0; j < nmax; ++j) {
             const int st = j & 1;
-            int id[2];
-            uint4 kc[2][kPieces], vc[2][kPieces];
-#pragma unroll
-            for (int q = 0; q < 2; ++q) {
-                id[q] = page_of(2 * j + q);
-                if (id[q] >= 0) {
-                    const int64_t at = ((int64_t)id[q] * a.c.kv_heads + h) * kKvPage * D;
-#pragma unroll
-                    for (int i = 0; i < kPieces; ++i) {
-                        kc[q][i] = ldcg_128(a.c.k_codes + at + (tid + i * 128) * 16);
-                        vc[q][i] = ldcg_128(a.c.v_codes + at + (tid + i * 128) * 16);
-                    }
-                }
+            // the next tile's pages and scales, loaded ahead
+            int nid[2] = {-1, -1};
+            float nks = 0.f, nvs = 1.f;
+            if (j + 1 < nmax) {
+                nid[0] = page_of(2 * j + 2);
+                nid[1] = page_of(2 * j + 3);
+                scales_of(nid, nks, nvs);
             }
             KvTcMeta& mt = sh->meta[j % kTcMeta];
             if (tid < 2) {
                 const int p = id[tid];
-                float ks = 0.f, vs = 1.f;
-                if (p >= 0) {
-                    ks = ldcg_f32(a.c.k_scales + (int64_t)p * a.c.kv_heads + h);
-                    vs = ldcg_f32(a.c.v_scales + (int64_t)p * a.c.kv_heads + h);
-                }
                 mt.a[tid] = p == -2 ? a.scale_log2 : ks * a.scale_log2;
                 mt.lv[tid] = log2f(vs);
                 mt.inv[tid] = 1.f / vs;
                 mt.valid[tid] = p >= 0 ? kKvPage : p == -2 ? ntok : 0;
-                mt.poison[2 * tid] = mt.poison[2 * tid + 1] = 0u;
             }
             __half2 up = __half2half2(__ushort_as_half(0x3c00));     // the tail's power of two (attention.cu)
             if (id[0] == -2 || id[1] == -2) {
@@ -385,9 +425,12 @@ __global__ void __launch_bounds__(kTcThreads, 1) kv_attention_tc_kernel(const __
                 if (tid == 0) sh->tail_max = sh->tail_poison[0] = sh->tail_poison[1] = 0u;
                 named_barrier_sync(1, 128);
                 __half2 am = __half2half2(__ushort_as_half(0));
-                for (int i = tid; i < kKvPage * D / 8; i += 128) {
-                    const uint4 u = tail_piece(a.c.v_tail, i);
-                    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+                uint4 tv[kTail];
+                tail_pieces(a.c.v_tail, tv);
+#pragma unroll
+                for (int n = 0; n < kTail; ++n) {
+                    const int i = tid + n * 128;
+                    const uint32_t w[4] = {tv[n].x, tv[n].y, tv[n].z, tv[n].w};
 #pragma unroll
                     for (int e = 0; e < 4; ++e) {
                         uint32_t x = w[e];
@@ -405,26 +448,44 @@ __global__ void __launch_bounds__(kTcThreads, 1) kv_attention_tc_kernel(const __
                 if (tid == 0) {
                     mt.lv[q] = (float)-k2;
                     mt.inv[q] = exp2f((float)k2);
-                    mt.poison[2 * q] = sh->tail_poison[0];
-                    mt.poison[2 * q + 1] = sh->tail_poison[1];
                 }
             }
+            uint4 u[2][kPieces];
+            // takes a tile's codes into registers, and lets the next tile's come
+            auto take_codes = [&](int which) {
+                if (ok) ok = mbar_wait(&sh->codes[which], j & 1, a.status);
+#pragma unroll
+                for (int q = 0; q < 2; ++q)
+#pragma unroll
+                    for (int i = 0; i < kPieces; ++i)
+                        if (id[q] >= 0)
+                            u[q][i] = *reinterpret_cast<const uint4*>(sc + which * L::kCodes + q * kKvPage * D + (tid + i * 128) * 16);
+                if (j + 1 < nmax) {
+                    named_barrier_sync(1, 128);
+                    stage_codes(which, nid);
+                }
+            };
             // ---- K ----
+            take_codes(0);
             if (j >= 2 && ok) ok = mbar_wait(&sh->ke[st], ((j >> 1) - 1) & 1, a.status);
             unsigned char* kd = sk + st * L::kKBytes;
 #pragma unroll
             for (int q = 0; q < 2; ++q) {
                 if (id[q] >= 0) {
 #pragma unroll
-                    for (int i = 0; i < kPieces; ++i) {              // piece: panel, token, quarter of the 64 dimensions
-                        const int x = tid + i * 128;
-                        codes_to(kc[q][i], kd + (x >> 8) * 16384, q * kKvPage + ((x >> 2) & 63), x & 3);
-                    }
+                    for (int i = 0; i < kPieces; ++i)    // piece: panel, token, quarter of the 64 dimensions
+                        codes_to(u[q][i], kd + q * 8192 + (i & 1) * 4096 + (i >> 1) * 16384);
                 } else {
-                    for (int i = tid; i < kKvPage * D / 8; i += 128) {
-                        const int tok = i / (D / 8), c = i % (D / 8);
-                        const uint4 u = id[q] == -2 ? tail_piece(a.c.k_tail, i) : make_uint4(0, 0, 0, 0);
-                        *reinterpret_cast<uint4*>(kd + (c >> 3) * 16384 + sw128(q * kKvPage + tok, c & 7)) = u;
+                    uint4 tk[kTail];
+#pragma unroll
+                    for (int n = 0; n < kTail; ++n) tk[n] = make_uint4(0, 0, 0, 0);
+                    if (id[q] == -2) tail_pieces(a.c.k_tail, tk);
+#pragma unroll
+                    for (int n = 0; n < kTail; ++n) {
+                        const int i = tid + n * 128, tok = i / (D / 8), c = i % (D / 8);
+                        // a token whose value is not finite (taken out of V): scores NaN for the rows that see it
+                        if (id[q] == -2 && ((sh->tail_poison[tok >> 5] >> (tok & 31)) & 1u)) tk[n] = make_uint4(~0u, ~0u, ~0u, ~0u);
+                        *reinterpret_cast<uint4*>(kd + (c >> 3) * 16384 + sw128(q * kKvPage + tok, c & 7)) = tk[n];
                     }
                 }
             }
@@ -432,6 +493,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) kv_attention_tc_kernel(const __
             __syncwarp();
             if (lane == 0) mbar_arrive(&sh->kf[st]);
             // ---- V ----
+            take_codes(1);
             if (j >= 2 && ok) ok = mbar_wait(&sh->ve[st], ((j >> 1) - 1) & 1, a.status);
             unsigned char* vd = sv + st * L::kVBytes;
 #pragma unroll
@@ -439,15 +501,15 @@ __global__ void __launch_bounds__(kTcThreads, 1) kv_attention_tc_kernel(const __
                 unsigned char* page = vd + q * D * 128;
                 if (id[q] >= 0) {
 #pragma unroll
-                    for (int i = 0; i < kPieces; ++i) {              // piece: dimension, quarter of the 64 tokens
-                        const int x = tid + i * 128;
-                        codes_to(vc[q][i], page, x >> 2, x & 3);
-                    }
+                    for (int i = 0; i < kPieces; ++i)    // piece: dimension, quarter of the 64 tokens
+                        codes_to(u[q][i], page + i * 4096);
                 } else if (id[q] == -2) {
-                    for (int i = tid; i < kKvPage * D / 8; i += 128) {
-                        const int tok = i / (D / 8), dim = i % (D / 8) * 8;
-                        const uint4 u = tail_piece(a.c.v_tail, i);
-                        uint32_t w[4] = {u.x, u.y, u.z, u.w};
+                    uint4 tv[kTail];
+                    tail_pieces(a.c.v_tail, tv);
+#pragma unroll
+                    for (int n = 0; n < kTail; ++n) {
+                        const int i = tid + n * 128, tok = i / (D / 8), dim = i % (D / 8) * 8;
+                        uint32_t w[4] = {tv[n].x, tv[n].y, tv[n].z, tv[n].w};
 #pragma unroll
                         for (int e = 0; e < 4; ++e) {
                             if ((w[e] & 0x7c00u) == 0x7c00u) w[e] &= 0xffff0000u;
@@ -464,6 +526,10 @@ __global__ void __launch_bounds__(kTcThreads, 1) kv_attention_tc_kernel(const __
             fence_proxy_async_smem();
             __syncwarp();
             if (lane == 0) mbar_arrive(&sh->vf[st]);
+            id[0] = nid[0];
+            id[1] = nid[1];
+            ks = nks;
+            vs = nvs;
         }
     } else if (warp == 12 && nmax > 0) {
         // ---------------- MMA issuer (the whole warp; one lane issues) ----------------
@@ -529,7 +595,9 @@ int64_t kv_tc_blocks(const KvBatchView& b, int G, int kv_heads) {
 cudaError_t launch_kv_attention_tc(const KvCacheView& c, const KvBatchView& b, const uint16_t* Q, int64_t ldQ, int q_heads,
                                    float scale, uint16_t* Y, int64_t ldY, cudaStream_t st) {
     const int G = q_heads / c.kv_heads;
-    const KvTcArgs a = {c, b, Q, Y, ldQ, ldY, scale * 1.44269504088896340736f, G,
+    // above zero, so that a masked score of -inf stays one (below 1e-25 every score is zero beside fp32's steps)
+    const float scale_log2 = scale > 1e-25f ? scale * 1.44269504088896340736f : 1e-25f;
+    const KvTcArgs a = {c, b, Q, Y, ldQ, ldY, scale_log2, G,
                         (int)(((int64_t)b.max_new * G + kTcRows - 1) / kTcRows), device_status_ptr()};
     const unsigned grid = (unsigned)kv_tc_blocks(b, G, c.kv_heads);
     return c.head_dim == 64 ? launch_tc<64>(a, grid, st) : launch_tc<128>(a, grid, st);
