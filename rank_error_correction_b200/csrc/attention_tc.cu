@@ -205,23 +205,29 @@ __global__ void __launch_bounds__(kTcThreads, 1) kv_attention_tc_kernel(const __
         const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
         const uint32_t ts = tmem + lanes + (uint32_t)(t * 128), to = tmem + lanes + (uint32_t)(256 + t * 128);
         const bool there = row < rows;
-        const int64_t qrow = s.q0 + (there ? row / a.G : 0);
-        const int64_t head = (int64_t)(h * a.G + (there ? row % a.G : 0)) * D;
+        const int tok = there ? row / a.G : 0, gq = there ? row - tok * a.G : 0;
+        // rows of a warp's 32, two (D = 128) or four at a time: 16 bytes of a row per lane
+        constexpr int kLanes = D / 8, kAtOnce = 32 / kLanes;
+        const int sub = lane / kLanes, ch = lane % kLanes;
+        unsigned char* mine = sq + t * L::kQBytes + (ch >> 3) * 16384;
+        const int64_t head = (int64_t)h * a.G * D + 8 * ch;
         {
-            uint4 v[D / 8];                              // every load in flight before the first store
+            uint4 v[32 / kAtOnce];                       // every load in flight before the first store
 #pragma unroll
-            for (int c = 0; c < D / 8; ++c) {
-                v[c] = make_uint4(0, 0, 0, 0);
-                if (there) v[c] = ldcg_128(a.Q + qrow * a.ldQ + head + 8 * c);
+            for (int i = 0; i < 32 / kAtOnce; ++i) {
+                const int from = i * kAtOnce + sub, ft = __shfl_sync(~0u, tok, from), fg = __shfl_sync(~0u, gq, from);
+                v[i] = make_uint4(0, 0, 0, 0);
+                if (row0 + t * 128 + (warp & 3) * 32 + from < rows)
+                    v[i] = ldcg_128(a.Q + (int64_t)(s.q0 + ft) * a.ldQ + head + (int64_t)fg * D);
             }
 #pragma unroll
-            for (int c = 0; c < D / 8; ++c)
-                *reinterpret_cast<uint4*>(sq + t * L::kQBytes + (c >> 3) * 16384 + sw128(r, c & 7)) = v[c];
+            for (int i = 0; i < 32 / kAtOnce; ++i)
+                *reinterpret_cast<uint4*>(mine + sw128((warp & 3) * 32 + i * kAtOnce + sub, ch & 7)) = v[i];
         }
         fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) mbar_arrive(&sh->q_full);
-        const int limit = there ? s.start + row / a.G : -1;
+        const int limit = there ? s.start + tok : -1;
         const int least = s.start + (row0 + t * 128) / a.G;          // the tile's first row sees least
         float ref = -INFINITY, l = 0.f;
         for (int j = 0; j < nt[t]; ++j) {
@@ -315,26 +321,35 @@ __global__ void __launch_bounds__(kTcThreads, 1) kv_attention_tc_kernel(const __
             tc_fence_after();
         }
         const float inv = l == 0.f ? 0.f : 1.f / l;                  // a row that sees nothing is zero
-#pragma unroll
+        // (the tile's products are complete, so its queries' buffer takes the outputs; a warp's rows are its own)
+        unsigned char* out = sq + t * L::kQBytes;
+#pragma unroll 1
         for (int c = 0; c < D / 32; ++c) {
             uint32_t v[32];
             if (nt[t] > 0) {
                 tmem_ld32_async(to + c * 32, v);
                 tmem_ld_wait(v);
             }
-            if (there) {
 #pragma unroll
-                for (int i = 0; i < 32; i += 8) {
-                    uint4 y = make_uint4(0, 0, 0, 0);
-                    if (nt[t] > 0 && l != 0.f) {
-                        y.x = h2_as_u32(__floats2half2_rn(__uint_as_float(v[i]) * inv, __uint_as_float(v[i + 1]) * inv));
-                        y.y = h2_as_u32(__floats2half2_rn(__uint_as_float(v[i + 2]) * inv, __uint_as_float(v[i + 3]) * inv));
-                        y.z = h2_as_u32(__floats2half2_rn(__uint_as_float(v[i + 4]) * inv, __uint_as_float(v[i + 5]) * inv));
-                        y.w = h2_as_u32(__floats2half2_rn(__uint_as_float(v[i + 6]) * inv, __uint_as_float(v[i + 7]) * inv));
-                    }
-                    *reinterpret_cast<uint4*>(a.Y + qrow * a.ldY + head + c * 32 + i) = y;
+            for (int i = 0; i < 32; i += 8) {
+                uint4 y = make_uint4(0, 0, 0, 0);
+                if (nt[t] > 0 && l != 0.f) {
+                    y.x = h2_as_u32(__floats2half2_rn(__uint_as_float(v[i]) * inv, __uint_as_float(v[i + 1]) * inv));
+                    y.y = h2_as_u32(__floats2half2_rn(__uint_as_float(v[i + 2]) * inv, __uint_as_float(v[i + 3]) * inv));
+                    y.z = h2_as_u32(__floats2half2_rn(__uint_as_float(v[i + 4]) * inv, __uint_as_float(v[i + 5]) * inv));
+                    y.w = h2_as_u32(__floats2half2_rn(__uint_as_float(v[i + 6]) * inv, __uint_as_float(v[i + 7]) * inv));
                 }
+                const int x = c * 4 + (i >> 3);
+                *reinterpret_cast<uint4*>(out + (x >> 3) * 16384 + sw128(r, x & 7)) = y;
             }
+        }
+        __syncwarp();
+#pragma unroll
+        for (int i = 0; i < 32 / kAtOnce; ++i) {
+            const int from = i * kAtOnce + sub, ft = __shfl_sync(~0u, tok, from), fg = __shfl_sync(~0u, gq, from);
+            if (row0 + t * 128 + (warp & 3) * 32 + from < rows)
+                *reinterpret_cast<uint4*>(a.Y + (int64_t)(s.q0 + ft) * a.ldY + head + (int64_t)fg * D) =
+                    *reinterpret_cast<const uint4*>(mine + sw128((warp & 3) * 32 + from, ch & 7));
         }
     } else if (warp < 12) {
         // ---------------- pages to operands (128 threads) ----------------
@@ -343,12 +358,13 @@ __global__ void __launch_bounds__(kTcThreads, 1) kv_attention_tc_kernel(const __
         const int64_t tail = ((int64_t)s.slot * a.c.kv_heads + h) * kKvPage * D;
         const int* table = a.b.table + (int64_t)b * a.b.max_pages;
         constexpr int kPieces = kKvPage * D / 16 / 128;              // 16-byte pieces of a page's K (or V) per thread
-        // kind of page p: its id, -1 absent (or out of range), -2 the tail
-        auto page_of = [&](int p) -> int {
+        // the table's entry for page p (loaded a tile ahead of its use), and what it
+        // says: the page's id, -1 absent (or out of range), -2 the tail
+        auto entry = [&](int p) { return p < full && p < 2 * nmax ? ldcg_s32(table + p) : -1; };
+        auto page_of = [&](int p, int id) -> int {
             if (p < full) {
-                const int id = ldcg_s32(table + p);
                 if (id >= 0 && id < a.c.pages) return id;
-                if (tid == 0) record_status(a.status, GLOWQ_ERR_INDEX);
+                if (tid == 0 && p < 2 * nmax) record_status(a.status, GLOWQ_ERR_INDEX);
                 return -1;
             }
             return p == full && ntok > 0 ? -2 : -1;
@@ -386,7 +402,9 @@ __global__ void __launch_bounds__(kTcThreads, 1) kv_attention_tc_kernel(const __
                 if (tok < ntok) u[i] = ldcg_128(src + tail + (int64_t)tok * D + 8 * c);
             }
         };
-        int id[2] = {page_of(0), page_of(1)};
+        const int first[2] = {entry(0), entry(1)};
+        int ahead[2] = {entry(2), entry(3)};             // the next tile's entries
+        int id[2] = {page_of(0, first[0]), page_of(1, first[1])};
         float ks = 0.f, vs = 1.f;                        // thread q < 2: the scales of page q
         auto scales_of = [&](const int (&id)[2], float& k, float& v) {
             k = 0.f;
@@ -407,9 +425,11 @@ __global__ void __launch_bounds__(kTcThreads, 1) kv_attention_tc_kernel(const __
             int nid[2] = {-1, -1};
             float nks = 0.f, nvs = 1.f;
             if (j + 1 < nmax) {
-                nid[0] = page_of(2 * j + 2);
-                nid[1] = page_of(2 * j + 3);
+                nid[0] = page_of(2 * j + 2, ahead[0]);
+                nid[1] = page_of(2 * j + 3, ahead[1]);
                 scales_of(nid, nks, nvs);
+                ahead[0] = entry(2 * j + 4);
+                ahead[1] = entry(2 * j + 5);
             }
             KvTcMeta& mt = sh->meta[j % kTcMeta];
             if (tid < 2) {
@@ -451,7 +471,6 @@ __global__ void __launch_bounds__(kTcThreads, 1) kv_attention_tc_kernel(const __
                 }
             }
             uint4 u[2][kPieces];
-            // takes a tile's codes into registers, and lets the next tile's come
             auto take_codes = [&](int which) {
                 if (ok) ok = mbar_wait(&sh->codes[which], j & 1, a.status);
 #pragma unroll
@@ -460,7 +479,13 @@ __global__ void __launch_bounds__(kTcThreads, 1) kv_attention_tc_kernel(const __
                     for (int i = 0; i < kPieces; ++i)
                         if (id[q] >= 0)
                             u[q][i] = *reinterpret_cast<const uint4*>(sc + which * L::kCodes + q * kKvPage * D + (tid + i * 128) * 16);
+            };
+            // The codes' buffer may be filled again only behind the conversion, which
+            // has waited for the reads: a barrier behind the reads alone lets a bulk
+            // copy overtake them (seen at D = 64: a tile read its successor's values).
+            auto next_codes = [&](int which) {
                 if (j + 1 < nmax) {
+                    fence_proxy_async_smem();
                     named_barrier_sync(1, 128);
                     stage_codes(which, nid);
                 }
@@ -492,6 +517,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) kv_attention_tc_kernel(const __
             fence_proxy_async_smem();
             __syncwarp();
             if (lane == 0) mbar_arrive(&sh->kf[st]);
+            next_codes(0);
             // ---- V ----
             take_codes(1);
             if (j >= 2 && ok) ok = mbar_wait(&sh->ve[st], ((j >> 1) - 1) & 1, a.status);
@@ -526,6 +552,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) kv_attention_tc_kernel(const __
             fence_proxy_async_smem();
             __syncwarp();
             if (lane == 0) mbar_arrive(&sh->vf[st]);
+            next_codes(1);
             id[0] = nid[0];
             id[1] = nid[1];
             ks = nks;
