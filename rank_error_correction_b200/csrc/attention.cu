@@ -159,9 +159,8 @@ __global__ void __launch_bounds__(kAttnWarps * 32) kv_attention_kernel(const __g
 
     for (int i = threadIdx.x; i < 16 * D / 8; i += kAttnWarps * 32) {
         const int r = i / (D / 8), row = row0 + r;
-        uint4 v = make_uint4(0, 0, 0, 0);
-        if (row < rows) v = ldcg_128(a.Q + (int64_t)(s.q0 + row / a.G) * a.ldQ + (int64_t)(h * a.G + row % a.G) * D + (i % (D / 8)) * 8);
-        reinterpret_cast<uint4*>(sq)[i] = v;
+        reinterpret_cast<uint4*>(sq)[i] =
+            ldcg_128_if(a.Q + (int64_t)(s.q0 + row / a.G) * a.ldQ + (int64_t)(h * a.G + row % a.G) * D + (i % (D / 8)) * 8, row < rows);
     }
     __syncthreads();
     // Q as A fragments: panel p, step q: dimensions 64 p + 16 t + 4 q .. + 3 of rows g and g + 8

@@ -211,19 +211,18 @@ __global__ void __launch_bounds__(kTcThreads, 1) kv_attention_tc_kernel(const __
         const int sub = lane / kLanes, ch = lane % kLanes;
         unsigned char* mine = sq + t * L::kQBytes + (ch >> 3) * 16384;
         const int64_t head = (int64_t)h * a.G * D + 8 * ch;
-        {
-            uint4 v[32 / kAtOnce];                       // every load in flight before the first store
-#pragma unroll
-            for (int i = 0; i < 32 / kAtOnce; ++i) {
-                const int from = i * kAtOnce + sub, ft = __shfl_sync(~0u, tok, from), fg = __shfl_sync(~0u, gq, from);
-                v[i] = make_uint4(0, 0, 0, 0);
-                if (row0 + t * 128 + (warp & 3) * 32 + from < rows)
-                    v[i] = ldcg_128(a.Q + (int64_t)(s.q0 + ft) * a.ldQ + head + (int64_t)fg * D);
-            }
-#pragma unroll
-            for (int i = 0; i < 32 / kAtOnce; ++i)
-                *reinterpret_cast<uint4*>(mine + sw128((warp & 3) * 32 + i * kAtOnce + sub, ch & 7)) = v[i];
+        // (rolled loops here and at the end: code that a block runs once is fetched cold)
+        const uint32_t qdst = smem_u32(mine);
+#pragma unroll 1
+        for (int i = 0; i < 32; i += kAtOnce) {
+            const int from = i + sub, ft = __shfl_sync(~0u, tok, from), fg = __shfl_sync(~0u, gq, from);
+            const uint32_t n = row0 + t * 128 + (warp & 3) * 32 + from < rows ? 16u : 0u;   // (0: zero)
+            asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;"
+                         ::"r"(qdst + sw128((warp & 3) * 32 + from, ch & 7)),
+                         "l"(a.Q + (int64_t)(s.q0 + ft) * a.ldQ + head + (int64_t)fg * D), "r"(n)
+                         : "memory");
         }
+        asm volatile("cp.async.wait_all;" ::: "memory");
         fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) mbar_arrive(&sh->q_full);
@@ -344,12 +343,18 @@ __global__ void __launch_bounds__(kTcThreads, 1) kv_attention_tc_kernel(const __
             }
         }
         __syncwarp();
+#pragma unroll 1
+        for (int i = 0; i < 32; i += 4 * kAtOnce) {
+            uint4 y[4];
 #pragma unroll
-        for (int i = 0; i < 32 / kAtOnce; ++i) {
-            const int from = i * kAtOnce + sub, ft = __shfl_sync(~0u, tok, from), fg = __shfl_sync(~0u, gq, from);
-            if (row0 + t * 128 + (warp & 3) * 32 + from < rows)
-                *reinterpret_cast<uint4*>(a.Y + (int64_t)(s.q0 + ft) * a.ldY + head + (int64_t)fg * D) =
-                    *reinterpret_cast<const uint4*>(mine + sw128((warp & 3) * 32 + from, ch & 7));
+            for (int k = 0; k < 4; ++k)
+                y[k] = *reinterpret_cast<const uint4*>(mine + sw128((warp & 3) * 32 + i + k * kAtOnce + sub, ch & 7));
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                const int from = i + k * kAtOnce + sub, ft = __shfl_sync(~0u, tok, from), fg = __shfl_sync(~0u, gq, from);
+                if (row0 + t * 128 + (warp & 3) * 32 + from < rows)
+                    *reinterpret_cast<uint4*>(a.Y + (int64_t)(s.q0 + ft) * a.ldY + head + (int64_t)fg * D) = y[k];
+            }
         }
     } else if (warp < 12) {
         // ---------------- pages to operands (128 threads) ----------------
@@ -398,8 +403,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) kv_attention_tc_kernel(const __
 #pragma unroll
             for (int i = 0; i < kTail; ++i) {
                 const int x = tid + i * 128, tok = x / (D / 8), c = x % (D / 8);
-                u[i] = make_uint4(0, 0, 0, 0);
-                if (tok < ntok) u[i] = ldcg_128(src + tail + (int64_t)tok * D + 8 * c);
+                u[i] = ldcg_128_if(src + tail + (int64_t)tok * D + 8 * c, tok < ntok);
             }
         };
         const int first[2] = {entry(0), entry(1)};

@@ -61,6 +61,20 @@ __device__ __forceinline__ uint4 ldcg_128(const void* p) {
                  : "memory");
     return v;
 }
+// The same where `there`, else zero, without a branch: a load inside an `if`
+// whose result also has a value outside it is waited for at the end of the `if`,
+// so that a loop of such loads runs one memory latency per load.
+__device__ __forceinline__ uint4 ldcg_128_if(const void* p, bool there) {
+    uint4 v;
+    asm volatile(
+        "{\n\t.reg .pred q;\n\tsetp.ne.s32 q, %5, 0;\n\t"
+        "mov.u32 %0, 0;\n\tmov.u32 %1, 0;\n\tmov.u32 %2, 0;\n\tmov.u32 %3, 0;\n\t"
+        "@q ld.global.cg.v4.u32 {%0,%1,%2,%3}, [%4];\n\t}"
+        : "=&r"(v.x), "=&r"(v.y), "=&r"(v.z), "=&r"(v.w)
+        : "l"(p), "r"((int)there)
+        : "memory");
+    return v;
+}
 __device__ __forceinline__ float ldcg_f32(const float* p) {
     float v;
     asm volatile("ld.global.cg.f32 %0, [%1];" : "=f"(v) : "l"(p) : "memory");

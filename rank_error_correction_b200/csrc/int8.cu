@@ -93,14 +93,13 @@ __device__ __forceinline__ void quantize_token(const uint16_t* __restrict__ X, i
                                                float* __restrict__ scales, Store store) {
     const uint4* x = reinterpret_cast<const uint4*>(X + t * d);
     const int n8 = (int)(d / 8);
-    constexpr int kKeep = 4;                 // the first 8 kKeep 256 elements of a row stay in registers
+    constexpr int kKeep = 8;                 // the first 8 kKeep 256 elements of a row stay in registers
     uint4 keep[kKeep];
     __half2 am = __half2half2(__ushort_as_half(0));
 #pragma unroll
     for (int j = 0; j < kKeep; ++j) {
         const int i = threadIdx.x + j * kQuantThreads;
-        keep[j] = make_uint4(0, 0, 0, 0);
-        if (i < n8) keep[j] = ldcg_128(x + i);
+        keep[j] = ldcg_128_if(x + i, i < n8);
     }
 #pragma unroll
     for (int j = 0; j < kKeep; ++j) amax8(keep[j], am);
@@ -390,9 +389,7 @@ __global__ void __launch_bounds__(kGemvWarps * 32) int8_gemv_kernel(const __grid
         bulk_g2s(base, a.xq + (int64_t)kb0 * (NT * 8 * 128), bytes, bar);
     }
     for (int i = threadIdx.x; i < NT * a.r; i += kGemvWarps * 32) {   // 8 halves each
-        uint4 v = make_uint4(0, 0, 0, 0);
-        if (i * 8 / a.r < a.T) v = ldcg_128(a.R + i * 8);
-        *reinterpret_cast<uint4*>(sm + L.rt + i * 16) = v;
+        *reinterpret_cast<uint4*>(sm + L.rt + i * 16) = ldcg_128_if(a.R + i * 8, i * 8 / a.r < a.T);
     }
     if (threadIdx.x < NT * 8) xs[threadIdx.x] = ldcg_f32(a.xs + threadIdx.x);
     mbar_wait(bar, 0, a.status);

@@ -631,8 +631,7 @@ __global__ void __launch_bounds__(kJoinThreads, 3) int8_join_kernel(const __grid
 #pragma unroll
             for (int q = 0; q < 2; ++q) {
                 const int tok = t0 + n * 8 + g, j = j0 + 16 * t + 8 * q;
-                rx[n][q] = make_uint4(0, 0, 0, 0);
-                if (tok < a.T && j < a.r) rx[n][q] = ldcg_128(a.R + (int64_t)tok * a.r + j);
+                rx[n][q] = ldcg_128_if(a.R + (int64_t)tok * a.r + j, tok < a.T && j < a.r);
             }
     };
     if (corrects) load_r(0);
@@ -642,7 +641,7 @@ __global__ void __launch_bounds__(kJoinThreads, 3) int8_join_kernel(const __grid
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
             const int tok = t0 + n * 8 + 2 * t + e;
-            st[n][e] = tok < a.T ? ldcg_f32(a.xs + tok) : 0.f;
+            st[n][e] = ldcg_f32(a.xs + min(tok, a.T - 1));
         }
     int v[4][2][4] = {};
     for (int begin = i8_share(a.split, p); p < a.split.sharers && begin < hi; begin = i8_share(a.split, ++p)) {
@@ -655,8 +654,8 @@ __global__ void __launch_bounds__(kJoinThreads, 3) int8_join_kernel(const __grid
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
                 const int tok = n * 8 + 2 * t + e;
-                x[n][e] = make_int4(0, 0, 0, 0);
-                if (t0 + tok < a.T) x[n][e] = __ldcg(reinterpret_cast<const int4*>(src + tok * kI8Rows));
+                const uint4 u = ldcg_128_if(src + tok * kI8Rows, t0 + tok < a.T);
+                x[n][e] = make_int4((int)u.x, (int)u.y, (int)u.z, (int)u.w);
             }
 #pragma unroll
         for (int n = 0; n < 4; ++n)
