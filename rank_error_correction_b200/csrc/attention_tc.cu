@@ -74,28 +74,26 @@ __device__ __forceinline__ float tc_ex2(float x) {
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
 }
-// 32 columns of this thread's lane, not waited for.
-__device__ __forceinline__ void tmem_ld32_async(uint32_t taddr, uint32_t (&v)[32]) {
+// 64 columns of this thread's lane, complete on return (load and wait in one
+// statement: a wait of its own would need the registers as operands, and moves them).
+__device__ __forceinline__ void tmem_ld64(uint32_t taddr, uint32_t (&v)[64]) {
     asm volatile(
-        "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
-        "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
-        "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
-        : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7]),
-          "=r"(v[8]), "=r"(v[9]), "=r"(v[10]), "=r"(v[11]), "=r"(v[12]), "=r"(v[13]), "=r"(v[14]), "=r"(v[15]),
-          "=r"(v[16]), "=r"(v[17]), "=r"(v[18]), "=r"(v[19]), "=r"(v[20]), "=r"(v[21]), "=r"(v[22]), "=r"(v[23]),
-          "=r"(v[24]), "=r"(v[25]), "=r"(v[26]), "=r"(v[27]), "=r"(v[28]), "=r"(v[29]), "=r"(v[30]), "=r"(v[31])
-        : "r"(taddr));
-}
-// The loads' registers may be read behind this (they are operands, so that no use moves ahead of it).
-__device__ __forceinline__ void tmem_ld_wait(uint32_t (&v)[32]) {
-    asm volatile("tcgen05.wait::ld.sync.aligned;"
-                 : "+r"(v[0]), "+r"(v[1]), "+r"(v[2]), "+r"(v[3]), "+r"(v[4]), "+r"(v[5]), "+r"(v[6]), "+r"(v[7]),
-                   "+r"(v[8]), "+r"(v[9]), "+r"(v[10]), "+r"(v[11]), "+r"(v[12]), "+r"(v[13]), "+r"(v[14]), "+r"(v[15]),
-                   "+r"(v[16]), "+r"(v[17]), "+r"(v[18]), "+r"(v[19]), "+r"(v[20]), "+r"(v[21]), "+r"(v[22]), "+r"(v[23]),
-                   "+r"(v[24]), "+r"(v[25]), "+r"(v[26]), "+r"(v[27]), "+r"(v[28]), "+r"(v[29])
-                 :
-                 : "memory");
-    asm volatile("" : "+r"(v[30]), "+r"(v[31]));
+        "tcgen05.ld.sync.aligned.32x32b.x64.b32 {"
+        "%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
+        "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,"
+        "%32,%33,%34,%35,%36,%37,%38,%39,%40,%41,%42,%43,%44,%45,%46,%47,"
+        "%48,%49,%50,%51,%52,%53,%54,%55,%56,%57,%58,%59,%60,%61,%62,%63"
+        "}, [%64];\n\ttcgen05.wait::ld.sync.aligned;"
+        : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7]), 
+          "=r"(v[8]), "=r"(v[9]), "=r"(v[10]), "=r"(v[11]), "=r"(v[12]), "=r"(v[13]), "=r"(v[14]), "=r"(v[15]), 
+          "=r"(v[16]), "=r"(v[17]), "=r"(v[18]), "=r"(v[19]), "=r"(v[20]), "=r"(v[21]), "=r"(v[22]), "=r"(v[23]), 
+          "=r"(v[24]), "=r"(v[25]), "=r"(v[26]), "=r"(v[27]), "=r"(v[28]), "=r"(v[29]), "=r"(v[30]), "=r"(v[31]), 
+          "=r"(v[32]), "=r"(v[33]), "=r"(v[34]), "=r"(v[35]), "=r"(v[36]), "=r"(v[37]), "=r"(v[38]), "=r"(v[39]), 
+          "=r"(v[40]), "=r"(v[41]), "=r"(v[42]), "=r"(v[43]), "=r"(v[44]), "=r"(v[45]), "=r"(v[46]), "=r"(v[47]), 
+          "=r"(v[48]), "=r"(v[49]), "=r"(v[50]), "=r"(v[51]), "=r"(v[52]), "=r"(v[53]), "=r"(v[54]), "=r"(v[55]), 
+          "=r"(v[56]), "=r"(v[57]), "=r"(v[58]), "=r"(v[59]), "=r"(v[60]), "=r"(v[61]), "=r"(v[62]), "=r"(v[63])
+        : "r"(taddr)
+        : "memory");
 }
 __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&v)[16]) {
     asm volatile(
@@ -241,26 +239,23 @@ __global__ void __launch_bounds__(kTcThreads, 1) kv_attention_tc_kernel(const __
             const float sa[2] = {see[0] > 0 ? mt.a[0] : 1.f, see[1] > 0 ? mt.a[1] : 1.f};
             const float slv[2] = {see[0] > 0 ? mt.lv[0] : 0.f, see[1] > 0 ? mt.lv[1] : 0.f};
             // 64 scores of page q (compact code: the loops over pages stay rolled)
-            auto scores = [&](int q, uint32_t (&v)[2][32]) {
-                tmem_ld32_async(ts + q * 64, v[0]);
-                tmem_ld32_async(ts + q * 64 + 32, v[1]);
-                tmem_ld_wait(v[0]);
-                tmem_ld_wait(v[1]);
+            auto scores = [&](int q, uint32_t (&v)[64]) {
+                tmem_ld64(ts + q * 64, v);
                 if (masked) {                            // (the scales are above zero: -inf stays)
                     const int n = q == 0 ? see[0] : see[1];
 #pragma unroll
-                    for (int i = 0; i < 64; ++i) v[i >> 5][i & 31] = i < n ? v[i >> 5][i & 31] : 0xff800000u;
+                    for (int i = 0; i < 64; ++i) v[i] = i < n ? v[i] : 0xff800000u;
                 }
             };
             float cand = -INFINITY;
 #pragma unroll 1
             for (int q = 0; q < 2; ++q) {
-                uint32_t v[2][32];
+                uint32_t v[64];
                 scores(q, v);
                 float m[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
                 for (int i = 0; i < 32; ++i)
-                    m[i & 3] = max3(m[i & 3], __uint_as_float(v[i >> 4][2 * (i & 15)]), __uint_as_float(v[i >> 4][2 * (i & 15) + 1]));
+                    m[i & 3] = max3(m[i & 3], __uint_as_float(v[2 * i]), __uint_as_float(v[2 * i + 1]));
                 cand = fmaxf(cand, fmaf(fmaxf(fmaxf(m[0], m[1]), fmaxf(m[2], m[3])), q == 0 ? sa[0] : sa[1], q == 0 ? slv[0] : slv[1]));
             }
             if (__any_sync(~0u, cand > ref + kTcSlack || (ref == -INFINITY && cand > -INFINITY))) {
@@ -272,8 +267,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) kv_attention_tc_kernel(const __
 #pragma unroll 1
                     for (int c = 0; c < D / 32; ++c) {
                         uint32_t v[32];
-                        tmem_ld32_async(to + c * 32, v);
-                        tmem_ld_wait(v);
+                        tmem_ld32(to + c * 32, v);
 #pragma unroll
                         for (int i = 0; i < 32; ++i) v[i] = __float_as_uint(__uint_as_float(v[i]) * f);
                         tmem_st32(to + c * 32, v);
@@ -285,7 +279,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) kv_attention_tc_kernel(const __
             const float base = (ref == -INFINITY ? 0.f : ref) - kTcWeightExp;
 #pragma unroll 1
             for (int q = 0; q < 2; ++q) {
-                uint32_t v[2][32];
+                uint32_t v[64];
                 scores(q, v);
                 const float sq_ = q == 0 ? sa[0] : sa[1], off = (q == 0 ? slv[0] : slv[1]) - base;
                 const uint64_t a2 = pack_f2(sq_, sq_), o2 = pack_f2(off, off);
@@ -295,9 +289,11 @@ __global__ void __launch_bounds__(kTcThreads, 1) kv_attention_tc_kernel(const __
                     uint32_t p[16];
 #pragma unroll
                     for (int i = 0; i < 16; ++i) {
-                        float e0, e1;
-                        unpack_f2(fma_f2(pack_f2(__uint_as_float(v[c][2 * i]), __uint_as_float(v[c][2 * i + 1])), a2, o2), e0, e1);
-                        const float w0 = tc_ex2(e0), w1 = tc_ex2(e1);
+                        const uint64_t e2 = fma_f2(pack_f2(__uint_as_float(v[c * 32 + 2 * i]), __uint_as_float(v[c * 32 + 2 * i + 1])), a2, o2);
+                        float w0, w1;
+                        unpack_f2(e2, w0, w1);
+                        w0 = tc_ex2(w0);
+                        w1 = tc_ex2(w1);
                         if (i & 1) s3 = add_f2(s3, pack_f2(w0, w1));
                         else s2 = add_f2(s2, pack_f2(w0, w1));
                         p[i] = h2_as_u32(__floats2half2_rn(w0, w1));
@@ -308,7 +304,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) kv_attention_tc_kernel(const __
                 unpack_f2(add_f2(s2, s3), s0, s1);
                 const float sum = s0 + s1;
                 // a row that sees nothing of a page takes nothing from its scale (which may be NaN)
-                if (sum != 0.f) l += sum * mt.inv[q];
+                if ((q == 0 ? see[0] : see[1]) > 0) l += sum * mt.inv[q];
             }
             tmem_st_wait();
             tc_fence_before();
@@ -326,8 +322,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) kv_attention_tc_kernel(const __
         for (int c = 0; c < D / 32; ++c) {
             uint32_t v[32];
             if (nt[t] > 0) {
-                tmem_ld32_async(to + c * 32, v);
-                tmem_ld_wait(v);
+                tmem_ld32(to + c * 32, v);
             }
 #pragma unroll
             for (int i = 0; i < 32; i += 8) {
@@ -474,15 +469,21 @@ __global__ void __launch_bounds__(kTcThreads, 1) kv_attention_tc_kernel(const __
                     mt.inv[q] = exp2f((float)k2);
                 }
             }
-            uint4 u[2][kPieces];
-            auto take_codes = [&](int which) {
+            // The complete pages of a tile's K (which = 0) or V, from the staged codes.
+            // One rolled body for both: a thread's pieces i of a page are rows 32 apart
+            // (4 KB), and of K's second panel 16 KB, of V's second 64 dimensions 8 KB on.
+            auto convert = [&](int which, unsigned char* to, int half, int page) {
                 if (ok) ok = mbar_wait(&sh->codes[which], j & 1, a.status);
+                const unsigned char* from = sc + which * L::kCodes + tid * 16;
+#pragma unroll 1
+                for (int q = 0; q < 2; ++q, from += kKvPage * D, to += page) {
+                    if ((q ? id[1] : id[0]) < 0) continue;
+                    uint4 u[kPieces];
 #pragma unroll
-                for (int q = 0; q < 2; ++q)
+                    for (int i = 0; i < kPieces; ++i) u[i] = *reinterpret_cast<const uint4*>(from + i * 2048);
 #pragma unroll
-                    for (int i = 0; i < kPieces; ++i)
-                        if (id[q] >= 0)
-                            u[q][i] = *reinterpret_cast<const uint4*>(sc + which * L::kCodes + q * kKvPage * D + (tid + i * 128) * 16);
+                    for (int i = 0; i < kPieces; ++i) codes_to(u[i], to + (i & 1) * 4096 + (i >> 1) * half);
+                }
             };
             // The codes' buffer may be filled again only behind the conversion, which
             // has waited for the reads: a barrier behind the reads alone lets a bulk
@@ -495,25 +496,23 @@ __global__ void __launch_bounds__(kTcThreads, 1) kv_attention_tc_kernel(const __
                 }
             };
             // ---- K ----
-            take_codes(0);
             if (j >= 2 && ok) ok = mbar_wait(&sh->ke[st], ((j >> 1) - 1) & 1, a.status);
             unsigned char* kd = sk + st * L::kKBytes;
-#pragma unroll
-            for (int q = 0; q < 2; ++q) {
-                if (id[q] >= 0) {
-#pragma unroll
-                    for (int i = 0; i < kPieces; ++i)    // piece: panel, token, quarter of the 64 dimensions
-                        codes_to(u[q][i], kd + q * 8192 + (i & 1) * 4096 + (i >> 1) * 16384);
-                } else {
+            convert(0, kd, 16384, 8192);
+            if (id[0] < 0 || id[1] < 0) {
+#pragma unroll 1
+                for (int q = 0; q < 2; ++q) {
+                    const int p = q ? id[1] : id[0];
+                    if (p >= 0) continue;
                     uint4 tk[kTail];
 #pragma unroll
                     for (int n = 0; n < kTail; ++n) tk[n] = make_uint4(0, 0, 0, 0);
-                    if (id[q] == -2) tail_pieces(a.c.k_tail, tk);
+                    if (p == -2) tail_pieces(a.c.k_tail, tk);
 #pragma unroll
                     for (int n = 0; n < kTail; ++n) {
                         const int i = tid + n * 128, tok = i / (D / 8), c = i % (D / 8);
                         // a token whose value is not finite (taken out of V): scores NaN for the rows that see it
-                        if (id[q] == -2 && ((sh->tail_poison[tok >> 5] >> (tok & 31)) & 1u)) tk[n] = make_uint4(~0u, ~0u, ~0u, ~0u);
+                        if (p == -2 && ((sh->tail_poison[tok >> 5] >> (tok & 31)) & 1u)) tk[n] = make_uint4(~0u, ~0u, ~0u, ~0u);
                         *reinterpret_cast<uint4*>(kd + (c >> 3) * 16384 + sw128(q * kKvPage + tok, c & 7)) = tk[n];
                     }
                 }
@@ -523,34 +522,33 @@ __global__ void __launch_bounds__(kTcThreads, 1) kv_attention_tc_kernel(const __
             if (lane == 0) mbar_arrive(&sh->kf[st]);
             next_codes(0);
             // ---- V ----
-            take_codes(1);
             if (j >= 2 && ok) ok = mbar_wait(&sh->ve[st], ((j >> 1) - 1) & 1, a.status);
             unsigned char* vd = sv + st * L::kVBytes;
+            convert(1, vd, 8192, D * 128);
+            if (id[0] < 0 || id[1] < 0) {
+#pragma unroll 1
+                for (int q = 0; q < 2; ++q) {
+                    const int p = q ? id[1] : id[0];
+                    unsigned char* page = vd + q * D * 128;
+                    if (p == -2) {
+                        uint4 tv[kTail];
+                        tail_pieces(a.c.v_tail, tv);
 #pragma unroll
-            for (int q = 0; q < 2; ++q) {
-                unsigned char* page = vd + q * D * 128;
-                if (id[q] >= 0) {
+                        for (int n = 0; n < kTail; ++n) {
+                            const int i = tid + n * 128, tok = i / (D / 8), dim = i % (D / 8) * 8;
+                            uint32_t w[4] = {tv[n].x, tv[n].y, tv[n].z, tv[n].w};
 #pragma unroll
-                    for (int i = 0; i < kPieces; ++i)    // piece: dimension, quarter of the 64 tokens
-                        codes_to(u[q][i], page + i * 4096);
-                } else if (id[q] == -2) {
-                    uint4 tv[kTail];
-                    tail_pieces(a.c.v_tail, tv);
-#pragma unroll
-                    for (int n = 0; n < kTail; ++n) {
-                        const int i = tid + n * 128, tok = i / (D / 8), dim = i % (D / 8) * 8;
-                        uint32_t w[4] = {tv[n].x, tv[n].y, tv[n].z, tv[n].w};
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) {
-                            if ((w[e] & 0x7c00u) == 0x7c00u) w[e] &= 0xffff0000u;
-                            if ((w[e] & 0x7c000000u) == 0x7c000000u) w[e] &= 0x0000ffffu;
-                            const __half2 x = __hmul2(u32_as_h2(w[e]), up);
-                            *reinterpret_cast<__half*>(page + sw128(dim + 2 * e, tok >> 3) + (tok & 7) * 2) = __low2half(x);
-                            *reinterpret_cast<__half*>(page + sw128(dim + 2 * e + 1, tok >> 3) + (tok & 7) * 2) = __high2half(x);
+                            for (int e = 0; e < 4; ++e) {
+                                if ((w[e] & 0x7c00u) == 0x7c00u) w[e] &= 0xffff0000u;
+                                if ((w[e] & 0x7c000000u) == 0x7c000000u) w[e] &= 0x0000ffffu;
+                                const __half2 x = __hmul2(u32_as_h2(w[e]), up);
+                                *reinterpret_cast<__half*>(page + sw128(dim + 2 * e, tok >> 3) + (tok & 7) * 2) = __low2half(x);
+                                *reinterpret_cast<__half*>(page + sw128(dim + 2 * e + 1, tok >> 3) + (tok & 7) * 2) = __high2half(x);
+                            }
                         }
+                    } else if (p == -1) {
+                        for (int i = tid; i < D * 8; i += 128) *reinterpret_cast<uint4*>(page + i * 16) = make_uint4(0, 0, 0, 0);
                     }
-                } else {
-                    for (int i = tid; i < D * 8; i += 128) *reinterpret_cast<uint4*>(page + i * 16) = make_uint4(0, 0, 0, 0);
                 }
             }
             fence_proxy_async_smem();
