@@ -33,40 +33,91 @@ struct KvAppendArgs {
 struct HalfRow {
     uint4 lo, hi;
 };
-__device__ __forceinline__ HalfRow load_row(const uint16_t* p, int i, int half) {
-    return {ldcg_128(p + 8 * i), ldcg_128(p + half + 8 * i)};
+__device__ __forceinline__ HalfRow load_row_if(const uint16_t* p, int i, int half, bool there) {
+    return {ldcg_128_if(p + 8 * i, there), ldcg_128_if(p + half + 8 * i, there)};
 }
 __device__ __forceinline__ void store_row(uint16_t* p, int i, int half, const HalfRow& v) {
     *reinterpret_cast<uint4*>(p + 8 * i) = v.lo;
     *reinterpret_cast<uint4*>(p + half + 8 * i) = v.hi;
 }
+// Cosines and sines of the eight pairs (8 i + e, D/2 + 8 i + e) at one position.
+struct Turn {
+    float4 c[2], s[2];
+};
+__device__ __forceinline__ Turn load_turn(const float* cs, int i, int half) {
+    const float4 *c = reinterpret_cast<const float4*>(cs + 8 * i), *s = reinterpret_cast<const float4*>(cs + half + 8 * i);
+    return {{__ldg(c), __ldg(c + 1)}, {__ldg(s), __ldg(s + 1)}};
+}
 // Pairs (x_i, x_{i + D/2}) turned by the position's angle: two fp32 products and
 // one sum each, unfused, rounded to fp16 once.
-__device__ __forceinline__ HalfRow rotate(const HalfRow& v, const float* cs, int i, int half) {
+__device__ __forceinline__ void rotate(HalfRow& v, const Turn& t) {
     const uint32_t a[4] = {v.lo.x, v.lo.y, v.lo.z, v.lo.w}, b[4] = {v.hi.x, v.hi.y, v.hi.z, v.hi.w};
+    const float c[8] = {t.c[0].x, t.c[0].y, t.c[0].z, t.c[0].w, t.c[1].x, t.c[1].y, t.c[1].z, t.c[1].w};
+    const float s[8] = {t.s[0].x, t.s[0].y, t.s[0].z, t.s[0].w, t.s[1].x, t.s[1].y, t.s[1].z, t.s[1].w};
     uint32_t x[4], y[4];
 #pragma unroll
     for (int q = 0; q < 4; ++q) {
-        const float2 c = __ldg(reinterpret_cast<const float2*>(cs + 8 * i) + q);
-        const float2 s = __ldg(reinterpret_cast<const float2*>(cs + half + 8 * i) + q);
         const float2 f = __half22float2(u32_as_h2(a[q])), h = __half22float2(u32_as_h2(b[q]));
-        x[q] = h2_as_u32(__floats2half2_rn(__fsub_rn(__fmul_rn(f.x, c.x), __fmul_rn(h.x, s.x)),
-                                           __fsub_rn(__fmul_rn(f.y, c.y), __fmul_rn(h.y, s.y))));
-        y[q] = h2_as_u32(__floats2half2_rn(__fadd_rn(__fmul_rn(h.x, c.x), __fmul_rn(f.x, s.x)),
-                                           __fadd_rn(__fmul_rn(h.y, c.y), __fmul_rn(f.y, s.y))));
+        x[q] = h2_as_u32(__floats2half2_rn(__fsub_rn(__fmul_rn(f.x, c[2 * q]), __fmul_rn(h.x, s[2 * q])),
+                                           __fsub_rn(__fmul_rn(f.y, c[2 * q + 1]), __fmul_rn(h.y, s[2 * q + 1]))));
+        y[q] = h2_as_u32(__floats2half2_rn(__fadd_rn(__fmul_rn(h.x, c[2 * q]), __fmul_rn(f.x, s[2 * q])),
+                                           __fadd_rn(__fmul_rn(h.y, c[2 * q + 1]), __fmul_rn(f.y, s[2 * q + 1]))));
     }
-    return {make_uint4(x[0], x[1], x[2], x[3]), make_uint4(y[0], y[1], y[2], y[3])};
+    v = {make_uint4(x[0], x[1], x[2], x[3]), make_uint4(y[0], y[1], y[2], y[3])};
 }
+// A page's value codes on their way through shared memory: [D][64 tokens] in
+// words of four tokens, word w of row d at w ^ (d / 8 % 16) (eight dimensions
+// and a few tokens are moved at a time: no more than two lanes meet in a bank).
+template <int D>
+struct CodeTile {
+    uint32_t w[D][kKvPage / 4];
+    __device__ __forceinline__ uint32_t& at(int d, int i) { return w[d][i ^ ((d >> 3) & 15)]; }
+    // the 16 tokens from 16 c of row d
+    __device__ __forceinline__ uint4 chunk(int d, int c) {
+        const int f = (d >> 3) & 15;
+        uint4 v = *reinterpret_cast<const uint4*>(&w[d][4 * (c ^ (f >> 2))]);
+        if (f & 1) v = make_uint4(v.y, v.x, v.w, v.z);
+        if (f & 2) v = make_uint4(v.z, v.w, v.x, v.y);
+        return v;
+    }
+    __device__ __forceinline__ void set_chunk(int d, int c, uint4 v) {
+        const int f = (d >> 3) & 15;
+        if (f & 1) v = make_uint4(v.y, v.x, v.w, v.z);
+        if (f & 2) v = make_uint4(v.z, v.w, v.x, v.y);
+        *reinterpret_cast<uint4*>(&w[d][4 * (c ^ (f >> 2))]) = v;
+    }
+};
+// 4 x 4 bytes: byte j of r[i] and byte i of r[j] change places.
+__device__ __forceinline__ void transpose4(uint32_t (&r)[4]) {
+    const uint32_t a = __byte_perm(r[0], r[1], 0x5140), b = __byte_perm(r[2], r[3], 0x5140);
+    const uint32_t c = __byte_perm(r[0], r[1], 0x7362), d = __byte_perm(r[2], r[3], 0x7362);
+    r[0] = __byte_perm(a, b, 0x5410);
+    r[1] = __byte_perm(a, b, 0x7632);
+    r[2] = __byte_perm(c, d, 0x5410);
+    r[3] = __byte_perm(c, d, 0x7632);
+}
+// The same across four lanes S apart, each with one row: lane t gets byte t of all four.
+template <int S>
+__device__ __forceinline__ uint32_t transpose4_lanes(uint32_t w, int t) {
+    const uint32_t a = __shfl_xor_sync(~0u, w, S);
+    w = __byte_perm(w, a, t & 1 ? 0x3715 : 0x6240);      // bytes (t & 1) and (t & 1) + 2 of both lanes, the even lane's first
+    const uint32_t b = __shfl_xor_sync(~0u, w, 2 * S);
+    return __byte_perm(w, b, t & 2 ? 0x3276 : 0x5410);
+}
+
 // One block: one page that the step touches, of one sequence and kv head (and
 // the query heads that share it).  The block of the first touched page also
 // takes the last one when that stays incomplete: it reads the old tail for the
 // first and writes the new tail for the last, in this order.
+// Bound by memory: every load of a block is on its way before the first is
+// used (keys, values, the first query head and the angles, which a key and its
+// queries share).  @APPENDFIG
 template <int D>
-__global__ void __launch_bounds__(kAppendThreads) kv_append_kernel(const __grid_constant__ KvAppendArgs a) {
+__global__ void __launch_bounds__(kAppendThreads, 2) kv_append_kernel(const __grid_constant__ KvAppendArgs a) {
     constexpr int kHalf = D / 2, kItems = D / 16;        // items of 8 + 8 elements per row
     constexpr int kPer = kKvPage * kItems / kAppendThreads;
     __shared__ float red[2][kAppendThreads / 32];
-    __shared__ __align__(16) unsigned char vt[D][kKvPage + 16];   // codes of V by dimension
+    __shared__ __align__(16) CodeTile<D> vt;
     pdl_wait();
     pdl_launch_dependents();
     const int j = blockIdx.x % a.npg, bh = blockIdx.x / a.npg;
@@ -83,53 +134,71 @@ __global__ void __launch_bounds__(kAppendThreads) kv_append_kernel(const __grid_
     const bool open = s.len % kKvPage != 0;              // the last page stays incomplete
     if (p0 + j > p1 || (j > 0 && p0 + j == p1 && open)) return;
     const int64_t tail = ((int64_t)s.slot * a.c.kv_heads + h) * kKvPage * D;
-    const int tid = threadIdx.x;
+    const int tid = threadIdx.x, i = tid % kItems;
 
     for (int p = p0 + j;; p = p1) {
-        const int t0 = max(s.start, p * kKvPage), t1 = min(s.len, (p + 1) * kKvPage);   // new tokens of the page
-        // queries
-        if (a.G > 0) {
-            const int n = (t1 - t0) * a.G * kItems;
-            for (int it = tid; it < n; it += kAppendThreads) {
-                const int i = it % kItems, rg = it / kItems, gq = rg % a.G, pos = t0 + rg / a.G;
-                const int64_t row = s.q0 + (pos - s.start);
-                HalfRow v = load_row(a.Q + row * a.ldQ + (int64_t)(h * a.G + gq) * D, i, kHalf);
-                if (a.rope) v = rotate(v, a.rope + (int64_t)pos * D, i, kHalf);
-                store_row(a.Q_out + row * a.ldQo + (int64_t)(h * a.G + gq) * D, i, kHalf, v);
-            }
-        }
-        const bool complete = (p + 1) * kKvPage <= s.len;
-        if (!complete) {
-            const int n = (t1 - t0) * kItems;
-            for (int it = tid; it < n; it += kAppendThreads) {
-                const int i = it % kItems, pos = t0 + it / kItems;
+        if ((p + 1) * (int64_t)kKvPage > s.len) {        // stays incomplete: K, V and queries of its new tokens
+            const int t0 = max(s.start, p * kKvPage), n = (s.len - t0) * kItems;
+            int lw = 3;                                  // threads over (token, item): 2^lw; the others take other heads
+            while (lw < 8 && (1 << lw) < n) ++lw;
+            for (int it = tid & ((1 << lw) - 1); it < n; it += 1 << lw) {
+                const int pos = t0 + it / kItems;
                 const int64_t row = s.q0 + (pos - s.start), to = tail + (int64_t)(pos % kKvPage) * D;
-                HalfRow k = load_row(a.K + row * a.ldK + (int64_t)h * D, i, kHalf);
-                if (a.rope) k = rotate(k, a.rope + (int64_t)pos * D, i, kHalf);
-                store_row(a.c.k_tail + to, i, kHalf, k);
-                store_row(a.c.v_tail + to, i, kHalf, load_row(a.V + row * a.ldV + (int64_t)h * D, i, kHalf));
+                auto source = [&](int g) {               // heads of the group: queries, K, V
+                    return g < a.G   ? a.Q + row * a.ldQ + (int64_t)(h * a.G + g) * D
+                           : g == a.G ? a.K + row * a.ldK + (int64_t)h * D
+                                      : a.V + row * a.ldV + (int64_t)h * D;
+                };
+                const int step = kAppendThreads >> lw;
+                int g = tid >> lw;
+                HalfRow next = load_row_if(source(g), i, kHalf, g < a.G + 2);
+                Turn turn;
+                if (a.rope) turn = load_turn(a.rope + (int64_t)pos * D, i, kHalf);
+                for (; g < a.G + 2; g += step) {
+                    HalfRow v = next;
+                    next = load_row_if(source(g + step), i, kHalf, g + step < a.G + 2);
+                    if (a.rope && g <= a.G) rotate(v, turn);
+                    store_row(g < a.G   ? a.Q_out + row * a.ldQo + (int64_t)(h * a.G + g) * D
+                              : g == a.G ? a.c.k_tail + to
+                                         : a.c.v_tail + to,
+                              i, kHalf, v);
+                }
             }
         } else {
-            HalfRow k[kPer], v[kPer];
+            HalfRow k[kPer], v[kPer], x[kPer];
+            Turn turn[kPer];
+            const int page = ldcg_s32(a.b.table + (int64_t)b * a.b.max_pages + p);
+#pragma unroll
+            for (int q = 0; q < kPer; ++q) {
+                const int tok = (tid + q * kAppendThreads) / kItems, pos = p * kKvPage + tok;
+                const int64_t row = s.q0 + (pos - s.start), from = tail + (int64_t)tok * D;
+                const bool old = pos < s.start;
+                k[q] = load_row_if(old ? a.c.k_tail + from : a.K + row * a.ldK + (int64_t)h * D, i, kHalf, true);
+                v[q] = load_row_if(old ? a.c.v_tail + from : a.V + row * a.ldV + (int64_t)h * D, i, kHalf, true);
+                x[q] = load_row_if(a.Q + row * a.ldQ + (int64_t)h * a.G * D, i, kHalf, a.G > 0 && !old);
+                if (a.rope) turn[q] = load_turn(a.rope + (int64_t)pos * D, i, kHalf);
+            }
             __half2 kam = __half2half2(__ushort_as_half(0)), vam = kam;
 #pragma unroll
             for (int q = 0; q < kPer; ++q) {
-                const int it = tid + q * kAppendThreads, i = it % kItems, pos = p * kKvPage + it / kItems;
-                if (pos < s.start) {
-                    const int64_t from = tail + (int64_t)(pos % kKvPage) * D;
-                    k[q] = load_row(a.c.k_tail + from, i, kHalf);
-                    v[q] = load_row(a.c.v_tail + from, i, kHalf);
-                } else {
-                    const int64_t row = s.q0 + (pos - s.start);
-                    k[q] = load_row(a.K + row * a.ldK + (int64_t)h * D, i, kHalf);
-                    v[q] = load_row(a.V + row * a.ldV + (int64_t)h * D, i, kHalf);
-                    if (a.rope) k[q] = rotate(k[q], a.rope + (int64_t)pos * D, i, kHalf);
-                }
+                const bool old = p * kKvPage + (tid + q * kAppendThreads) / kItems < s.start;
+                if (a.rope && !old) rotate(k[q], turn[q]);
                 amax8(k[q].lo, kam);
                 amax8(k[q].hi, kam);
                 amax8(v[q].lo, vam);
                 amax8(v[q].hi, vam);
             }
+            for (int g = 0; g < a.G; ++g)
+#pragma unroll
+                for (int q = 0; q < kPer; ++q) {
+                    const int pos = p * kKvPage + (tid + q * kAppendThreads) / kItems;
+                    const bool old = pos < s.start;
+                    const int64_t row = s.q0 + (pos - s.start), at = (int64_t)(h * a.G + g) * D;
+                    HalfRow y = x[q];
+                    x[q] = load_row_if(a.Q + row * a.ldQ + at + D, i, kHalf, g + 1 < a.G && !old);
+                    if (a.rope) rotate(y, turn[q]);
+                    if (!old) store_row(a.Q_out + row * a.ldQo + at, i, kHalf, y);
+                }
             for (int o = 16; o > 0; o >>= 1) {
                 kam = __hmax2_nan(kam, __shfl_xor_sync(~0u, kam, o));
                 vam = __hmax2_nan(vam, __shfl_xor_sync(~0u, vam, o));
@@ -153,7 +222,6 @@ __global__ void __launch_bounds__(kAppendThreads) kv_append_kernel(const __grid_
             const float ks = kf ? __fdiv_rn(fmaxf(ka, 5.9604644775390625e-8f), 127.f) : nan;
             const float vs = vf ? __fdiv_rn(fmaxf(va, 5.9604644775390625e-8f), 127.f) : nan;
             const float kinv = __fdiv_rn(1.f, ks), vinv = __fdiv_rn(1.f, vs);
-            const int page = ldcg_s32(a.b.table + (int64_t)b * a.b.max_pages + p);
             if (page < 0 || page >= a.c.pages) {
                 if (tid == 0) record_status(a.status, GLOWQ_ERR_INDEX);
             } else {
@@ -166,21 +234,20 @@ __global__ void __launch_bounds__(kAppendThreads) kv_append_kernel(const __grid_
                 }
 #pragma unroll
                 for (int q = 0; q < kPer; ++q) {
-                    const int it = tid + q * kAppendThreads, i = it % kItems, tok = it / kItems;
+                    const int tok = (tid + q * kAppendThreads) / kItems;
 #pragma unroll
                     for (int e = 0; e < 2; ++e) {        // dimensions 8 i .. + 7 and the same behind the middle
                         const int dim = e * kHalf + 8 * i;
                         *reinterpret_cast<uint2*>(kc + ((dim >> 6) * kKvPage + tok) * 64 + (dim & 63)) =
                             kf ? codes8(e ? k[q].hi : k[q].lo, ks, kinv) : make_uint2(0u, 0u);
                         const uint2 c = vf ? codes8(e ? v[q].hi : v[q].lo, vs, vinv) : make_uint2(0u, 0u);
-#pragma unroll
-                        for (int r = 0; r < 8; ++r)
-                            vt[dim + r][tok] = (unsigned char)((r < 4 ? c.x >> (8 * r) : c.y >> (8 * (r - 4))) & 255u);
+                        // four tokens' lanes trade bytes: a word of four tokens of one dimension each
+                        vt.at(dim + (tok & 3), tok >> 2) = transpose4_lanes<kItems>(c.x, tok & 3);
+                        vt.at(dim + 4 + (tok & 3), tok >> 2) = transpose4_lanes<kItems>(c.y, tok & 3);
                     }
                 }
                 __syncthreads();
-                for (int it = tid; it < D * 4; it += kAppendThreads)
-                    vc[it] = *reinterpret_cast<const uint4*>(&vt[it >> 2][(it & 3) * 16]);
+                for (int it = tid; it < D * 4; it += kAppendThreads) vc[it] = vt.chunk(it >> 2, it & 3);
             }
         }
         if (j > 0 || p == p1 || !open) return;
@@ -202,10 +269,20 @@ struct KvReadArgs {
     unsigned int* status;
 };
 
+// fp16_RN(code * s) of a word's four codes: a byte with its sign bit turned is
+// 128 + q, placed in 2^23's mantissa.
+__device__ __forceinline__ uint2 values4(uint32_t w, float s) {
+    const uint32_t u = w ^ 0x80808080u;
+    auto f = [&](uint32_t sel) { return __fmul_rn(__uint_as_float(__byte_perm(u, 0x4b000000u, sel)) - 8388736.f, s); };
+    return make_uint2(h2_as_u32(__floats2half2_rn(f(0x7540), f(0x7541))), h2_as_u32(__floats2half2_rn(f(0x7542), f(0x7543))));
+}
+// One block: one page's part of a sequence and kv head.  A thread takes eight
+// dimensions of four tokens: codes of V are by dimension, and change places in
+// its registers.
 template <int D>
-__global__ void __launch_bounds__(256) kv_read_kernel(const __grid_constant__ KvReadArgs a) {
+__global__ void __launch_bounds__(2 * D) kv_read_kernel(const __grid_constant__ KvReadArgs a) {
     constexpr int kChunks = D / 8;
-    __shared__ __align__(16) unsigned char vt[D][kKvPage + 16];
+    __shared__ __align__(16) CodeTile<D> vt;
     pdl_wait();
     pdl_launch_dependents();
     const int j = blockIdx.x % a.npg, bh = blockIdx.x / a.npg;
@@ -228,37 +305,45 @@ __global__ void __launch_bounds__(256) kv_read_kernel(const __grid_constant__ Kv
     }
     if (!ok && tid == 0) record_status(a.status, GLOWQ_ERR_INDEX);
     const int64_t ph = (int64_t)page * a.c.kv_heads + h, tail = ((int64_t)slot * a.c.kv_heads + h) * kKvPage * D;
-    const bool codes = ok && complete;
-    float ks = 0.f, vs = 0.f;
-    if (codes) {
-        ks = ldcg_f32(a.c.k_scales + ph);
-        vs = ldcg_f32(a.c.v_scales + ph);
-        const uint4* vc = reinterpret_cast<const uint4*>(a.c.v_codes + ph * kKvPage * D);
-        for (int it = tid; it < D * 4; it += 256) *reinterpret_cast<uint4*>(&vt[it >> 2][(it & 3) * 16]) = ldcg_128(vc + it);
-        __syncthreads();
-    }
-    for (int it = tid; it < (t1 - t0) * kChunks; it += 256) {
-        const int c = it % kChunks, pos = t0 + it / kChunks, tok = pos - p * kKvPage, dim = 8 * c;
-        uint4 k = make_uint4(0, 0, 0, 0), v = k;
-        if (codes) {
-            const uint2 q = ldcg_64(a.c.k_codes + ph * kKvPage * D + ((dim >> 6) * kKvPage + tok) * 64 + (dim & 63));
-            uint32_t ko[4], vo[4];
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                const uint32_t w = e < 2 ? q.x >> (16 * e) : q.y >> (16 * (e - 2));
-                ko[e] = h2_as_u32(__floats2half2_rn((float)(int8_t)(w & 255) * ks, (float)(int8_t)((w >> 8) & 255) * ks));
-                vo[e] = h2_as_u32(__floats2half2_rn((float)(int8_t)vt[dim + 2 * e][tok] * vs,
-                                                    (float)(int8_t)vt[dim + 2 * e + 1][tok] * vs));
-            }
-            k = make_uint4(ko[0], ko[1], ko[2], ko[3]);
-            v = make_uint4(vo[0], vo[1], vo[2], vo[3]);
-        } else if (ok && pos < len) {
-            k = ldcg_128(a.c.k_tail + tail + (int64_t)tok * D + dim);
-            v = ldcg_128(a.c.v_tail + tail + (int64_t)tok * D + dim);
-        }
+    const int c = tid % kChunks, dim = 8 * c;
+    auto put = [&](int pos, const uint4& k, const uint4& v) {
         const int64_t to = (((int64_t)b * a.count + (pos - first)) * a.c.kv_heads + h) * D + dim;
         *reinterpret_cast<uint4*>(a.K + to) = k;
         *reinterpret_cast<uint4*>(a.V + to) = v;
+    };
+    if (ok && complete) {
+        const int t4 = tid / kChunks;                    // tokens 4 t4 .. + 3 (2 D threads: all 64)
+        const uint4* vc = reinterpret_cast<const uint4*>(a.c.v_codes + ph * kKvPage * D);
+        const int8_t* kc = a.c.k_codes + ph * kKvPage * D + ((dim >> 6) * kKvPage + 4 * t4) * 64 + (dim & 63);
+        const uint4 v0 = ldcg_128(vc + tid), v1 = ldcg_128(vc + tid + 2 * D);
+        uint2 k[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) k[e] = ldcg_64(kc + e * 64);
+        const float ks = ldcg_f32(a.c.k_scales + ph), vs = ldcg_f32(a.c.v_scales + ph);
+        vt.set_chunk(tid >> 2, tid & 3, v0);
+        vt.set_chunk((tid + 2 * D) >> 2, tid & 3, v1);
+        __syncthreads();
+        uint32_t lo[4], hi[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            lo[e] = vt.at(dim + e, t4);
+            hi[e] = vt.at(dim + 4 + e, t4);
+        }
+        transpose4(lo);
+        transpose4(hi);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            const int pos = p * kKvPage + 4 * t4 + e;
+            const uint2 ka = values4(k[e].x, ks), kb = values4(k[e].y, ks), va = values4(lo[e], vs), vb = values4(hi[e], vs);
+            if (pos >= t0 && pos < t1) put(pos, make_uint4(ka.x, ka.y, kb.x, kb.y), make_uint4(va.x, va.y, vb.x, vb.y));
+        }
+        return;
+    }
+    for (int pos = t0 + tid / kChunks; pos < t1; pos += 2 * D / kChunks) {
+        const int64_t at = tail + (int64_t)(pos - p * kKvPage) * D + dim;
+        const bool there = ok && pos < len;
+        const uint4 k = ldcg_128_if(a.c.k_tail + at, there), v = ldcg_128_if(a.c.v_tail + at, there);
+        put(pos, k, v);
     }
 }
 
@@ -279,8 +364,8 @@ cudaError_t launch_kv_read(const KvCacheView& c, const KvBatchView& b, const int
     KvReadArgs a = {c, b, first, count, kv_touched_pages(count), K, V, device_status_ptr()};
     const unsigned grid = (unsigned)((int64_t)a.npg * c.kv_heads * b.n_seq);
     void* args[] = {(void*)&a};
-    return launch_pdl(c.head_dim == 64 ? (const void*)kv_read_kernel<64> : (const void*)kv_read_kernel<128>, grid, 256,
-                      0, st, args);
+    return launch_pdl(c.head_dim == 64 ? (const void*)kv_read_kernel<64> : (const void*)kv_read_kernel<128>, grid,
+                      2 * c.head_dim, 0, st, args);
 }
 
 }  // namespace glowq
