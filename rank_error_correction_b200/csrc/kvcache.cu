@@ -48,6 +48,10 @@ __device__ __forceinline__ Turn load_turn(const float* cs, int i, int half) {
     const float4 *c = reinterpret_cast<const float4*>(cs + 8 * i), *s = reinterpret_cast<const float4*>(cs + half + 8 * i);
     return {{__ldg(c), __ldg(c + 1)}, {__ldg(s), __ldg(s + 1)}};
 }
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, uint32_t n) {   // n 16 or 0: then zeros
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(n) : "memory");
+}
+__device__ __forceinline__ void cp_async_wait_all() { asm volatile("cp.async.wait_all;" ::: "memory"); }
 // Pairs (x_i, x_{i + D/2}) turned by the position's angle: two fp32 products and
 // one sum each, unfused, rounded to fp16 once.
 __device__ __forceinline__ void rotate(HalfRow& v, const Turn& t) {
@@ -109,19 +113,23 @@ __device__ __forceinline__ uint32_t transpose4_lanes(uint32_t w, int t) {
 // the query heads that share it).  The block of the first touched page also
 // takes the last one when that stays incomplete: it reads the old tail for the
 // first and writes the new tail for the last, in this order.
-// Bound by memory: every load of a block is on its way before the first is
-// used (keys, values, the first query head and the angles, which a key and its
-// queries share).  @APPENDFIG
+// The rows of a page wait in shared memory, each thread's own, so that all of a
+// block's loads are in flight and registers leave room for three blocks an SM
+// (held in registers: two, 2 us slower at 40 heads); blocks of one page's heads
+// are neighbours, whose rows are neighbours in memory; a key and its queries
+// share their angles.  168 MB (4096 tokens of 32 heads of 128) in 45 us, 56 % of
+// the copy bandwidth: what is left is latency, the chain from the sequence's
+// numbers to its rows and to the codes (issue slots 55 %, DRAM 37 % busy).
 template <int D>
-__global__ void __launch_bounds__(kAppendThreads, 2) kv_append_kernel(const __grid_constant__ KvAppendArgs a) {
+__global__ void __launch_bounds__(kAppendThreads, 3) kv_append_kernel(const __grid_constant__ KvAppendArgs a) {
     constexpr int kHalf = D / 2, kItems = D / 16;        // items of 8 + 8 elements per row
     constexpr int kPer = kKvPage * kItems / kAppendThreads;
+    extern __shared__ __align__(16) uint4 stage[];
     __shared__ float red[2][kAppendThreads / 32];
     __shared__ __align__(16) CodeTile<D> vt;
     pdl_wait();
     pdl_launch_dependents();
-    const int j = blockIdx.x % a.npg, bh = blockIdx.x / a.npg;
-    const int h = bh % a.c.kv_heads, b = bh / a.c.kv_heads;
+    const int h = blockIdx.x % a.c.kv_heads, bj = blockIdx.x / a.c.kv_heads, j = bj % a.npg, b = bj / a.npg;
     const KvSeq s = kv_sequence(a.b, b);
     if (s.nq == 0 && s.ok) return;
     const bool bad = !s.ok || s.start < 0 || s.slot < 0 || s.slot >= a.c.slots || s.len > (int64_t)a.b.max_pages * kKvPage ||
@@ -165,40 +173,53 @@ __global__ void __launch_bounds__(kAppendThreads, 2) kv_append_kernel(const __gr
                 }
             }
         } else {
-            HalfRow k[kPer], v[kPer], x[kPer];
-            Turn turn[kPer];
+            // a thread's own rows wait in shared memory: [K, V, query][q][half][thread]
+            auto slot = [&](int what, int q) { return &stage[((what * kPer + q) * 2) * kAppendThreads + tid]; };
+            auto fetch = [&](int what, int q, const uint16_t* src, bool there) {
+                const uint32_t dst = smem_u32(slot(what, q)), n = there ? 16u : 0u;
+                cp_async16(dst, src + 8 * i, n);
+                cp_async16(dst + kAppendThreads * 16, src + kHalf + 8 * i, n);
+            };
+            auto get = [&](int what, int q) { return HalfRow{slot(what, q)[0], slot(what, q)[kAppendThreads]}; };
             const int page = ldcg_s32(a.b.table + (int64_t)b * a.b.max_pages + p);
 #pragma unroll
             for (int q = 0; q < kPer; ++q) {
                 const int tok = (tid + q * kAppendThreads) / kItems, pos = p * kKvPage + tok;
                 const int64_t row = s.q0 + (pos - s.start), from = tail + (int64_t)tok * D;
                 const bool old = pos < s.start;
-                k[q] = load_row_if(old ? a.c.k_tail + from : a.K + row * a.ldK + (int64_t)h * D, i, kHalf, true);
-                v[q] = load_row_if(old ? a.c.v_tail + from : a.V + row * a.ldV + (int64_t)h * D, i, kHalf, true);
-                x[q] = load_row_if(a.Q + row * a.ldQ + (int64_t)h * a.G * D, i, kHalf, a.G > 0 && !old);
-                if (a.rope) turn[q] = load_turn(a.rope + (int64_t)pos * D, i, kHalf);
+                fetch(0, q, old ? a.c.k_tail + from : a.K + row * a.ldK + (int64_t)h * D, true);
+                fetch(1, q, old ? a.c.v_tail + from : a.V + row * a.ldV + (int64_t)h * D, true);
+                if (a.G > 0) fetch(2, q, a.Q + row * a.ldQ + (int64_t)h * a.G * D, !old);
             }
             __half2 kam = __half2half2(__ushort_as_half(0)), vam = kam;
-#pragma unroll
             for (int q = 0; q < kPer; ++q) {
-                const bool old = p * kKvPage + (tid + q * kAppendThreads) / kItems < s.start;
-                if (a.rope && !old) rotate(k[q], turn[q]);
-                amax8(k[q].lo, kam);
-                amax8(k[q].hi, kam);
-                amax8(v[q].lo, vam);
-                amax8(v[q].hi, vam);
-            }
-            for (int g = 0; g < a.G; ++g)
-#pragma unroll
-                for (int q = 0; q < kPer; ++q) {
-                    const int pos = p * kKvPage + (tid + q * kAppendThreads) / kItems;
-                    const bool old = pos < s.start;
-                    const int64_t row = s.q0 + (pos - s.start), at = (int64_t)(h * a.G + g) * D;
-                    HalfRow y = x[q];
-                    x[q] = load_row_if(a.Q + row * a.ldQ + at + D, i, kHalf, g + 1 < a.G && !old);
-                    if (a.rope) rotate(y, turn[q]);
-                    if (!old) store_row(a.Q_out + row * a.ldQo + at, i, kHalf, y);
+                const int pos = p * kKvPage + (tid + q * kAppendThreads) / kItems;
+                const bool old = pos < s.start;
+                const int64_t row = s.q0 + (pos - s.start);
+                Turn turn;
+                if (a.rope) turn = load_turn(a.rope + (int64_t)pos * D, i, kHalf);
+                cp_async_wait_all();
+                HalfRow x = get(0, q);
+                if (a.rope && !old) {
+                    rotate(x, turn);
+                    slot(0, q)[0] = x.lo;
+                    slot(0, q)[kAppendThreads] = x.hi;
                 }
+                amax8(x.lo, kam);
+                amax8(x.hi, kam);
+                x = get(1, q);
+                amax8(x.lo, vam);
+                amax8(x.hi, vam);
+                if (old) continue;
+                for (int g = 0; g < a.G; ++g) {
+                    const int64_t at = (int64_t)(h * a.G + g) * D;
+                    cp_async_wait_all();
+                    x = get(2, q);
+                    if (g + 1 < a.G) fetch(2, q, a.Q + row * a.ldQ + at + D, true);
+                    if (a.rope) rotate(x, turn);
+                    store_row(a.Q_out + row * a.ldQo + at, i, kHalf, x);
+                }
+            }
             for (int o = 16; o > 0; o >>= 1) {
                 kam = __hmax2_nan(kam, __shfl_xor_sync(~0u, kam, o));
                 vam = __hmax2_nan(vam, __shfl_xor_sync(~0u, vam, o));
@@ -232,15 +253,14 @@ __global__ void __launch_bounds__(kAppendThreads, 2) kv_append_kernel(const __gr
                     a.c.k_scales[ph] = ks;
                     a.c.v_scales[ph] = vs;
                 }
-#pragma unroll
                 for (int q = 0; q < kPer; ++q) {
                     const int tok = (tid + q * kAppendThreads) / kItems;
 #pragma unroll
                     for (int e = 0; e < 2; ++e) {        // dimensions 8 i .. + 7 and the same behind the middle
                         const int dim = e * kHalf + 8 * i;
                         *reinterpret_cast<uint2*>(kc + ((dim >> 6) * kKvPage + tok) * 64 + (dim & 63)) =
-                            kf ? codes8(e ? k[q].hi : k[q].lo, ks, kinv) : make_uint2(0u, 0u);
-                        const uint2 c = vf ? codes8(e ? v[q].hi : v[q].lo, vs, vinv) : make_uint2(0u, 0u);
+                            kf ? codes8(slot(0, q)[e * kAppendThreads], ks, kinv) : make_uint2(0u, 0u);
+                        const uint2 c = vf ? codes8(slot(1, q)[e * kAppendThreads], vs, vinv) : make_uint2(0u, 0u);
                         // four tokens' lanes trade bytes: a word of four tokens of one dimension each
                         vt.at(dim + (tok & 3), tok >> 2) = transpose4_lanes<kItems>(c.x, tok & 3);
                         vt.at(dim + 4 + (tok & 3), tok >> 2) = transpose4_lanes<kItems>(c.y, tok & 3);
@@ -285,8 +305,7 @@ __global__ void __launch_bounds__(2 * D) kv_read_kernel(const __grid_constant__ 
     __shared__ __align__(16) CodeTile<D> vt;
     pdl_wait();
     pdl_launch_dependents();
-    const int j = blockIdx.x % a.npg, bh = blockIdx.x / a.npg;
-    const int h = bh % a.c.kv_heads, b = bh / a.c.kv_heads, tid = threadIdx.x;
+    const int h = blockIdx.x % a.c.kv_heads, bj = blockIdx.x / a.c.kv_heads, j = bj % a.npg, b = bj / a.npg, tid = threadIdx.x;
     const int len = ldcg_s32(a.b.kv_len + b), slot = ldcg_s32(a.b.slot + b), asked = a.first ? ldcg_s32(a.first + b) : 0;
     bool ok = asked >= 0 && asked <= kKvReadMax && len >= 0 && len <= (int64_t)a.b.max_pages * kKvPage;
     const int first = ok ? asked : 0;                    // (count <= kKvReadMax: no position passes 2^31)
@@ -355,8 +374,11 @@ cudaError_t launch_kv_append(const KvCacheView& c, const KvBatchView& b, const u
     a.npg = kv_touched_pages(b.max_new);
     const unsigned grid = (unsigned)((int64_t)a.npg * c.kv_heads * b.n_seq);
     void* args[] = {(void*)&a};
-    return launch_pdl(c.head_dim == 64 ? (const void*)kv_append_kernel<64> : (const void*)kv_append_kernel<128>, grid,
-                      kAppendThreads, 0, st, args);
+    const void* f = c.head_dim == 64 ? (const void*)kv_append_kernel<64> : (const void*)kv_append_kernel<128>;
+    const int smem = 3 * kKvPage * c.head_dim * 2;       // keys, values and one query head of a page
+    cudaError_t e = cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (e != cudaSuccess) return e;
+    return launch_pdl(f, grid, kAppendThreads, smem, st, args);
 }
 
 cudaError_t launch_kv_read(const KvCacheView& c, const KvBatchView& b, const int* first, int count, uint16_t* K,
