@@ -19,7 +19,8 @@
 namespace glowq {
 
 constexpr int kAttnWarps = 4;
-constexpr int kAttnRing = 3;             // half-pages (K or V of one page) in flight per warp
+constexpr int kAttnThreads = kAttnWarps * 32;
+constexpr int kAttnParts = 128;          // blocks that share one unit, at most (and the two at its ends)
 constexpr float kWeightExp = 8.f;
 
 struct KvAttnArgs {
@@ -29,16 +30,12 @@ struct KvAttnArgs {
     uint16_t* Y;
     int64_t ldQ, ldY;
     float scale_log2;        // scale log2(e)
-    int G, rt, S;
-    float* partial;          // [((b Hkv + h) rt + tile) S + s][16][D + 2]
-    unsigned int* tickets;   // [(b Hkv + h) rt + tile], zero between calls
+    int G;
+    float* partial;          // [block][2][8 RN][D + 4]
+    unsigned int* tickets;   // [block], zero between calls
     unsigned int* status;
 };
 
-__device__ __forceinline__ void attn_bulk(uint32_t dst, const void* src, uint32_t bytes, uint64_t* bar) {
-    mbar_arrive_expect_tx(bar, bytes);
-    bulk_g2s(dst, src, bytes, bar);
-}
 // Four int8 codes as fp16 pairs, exactly: bytes with the sign bit turned are 128 + q, placed in 1024's mantissa.
 __device__ __forceinline__ void cvt_codes(uint32_t w, uint32_t& lo, uint32_t& hi) {
     const uint32_t u = w ^ 0x80808080u;
@@ -58,448 +55,582 @@ __device__ __forceinline__ void ldsm4t(uint32_t addr, uint32_t (&r)[4]) {
                  : "memory");
 }
 
-// Running softmax of a warp's 16 rows: this lane's rows g and g + 8.
-template <int D>
-struct AttnState {
-    float m[2], l[2], o[D / 8][4];
-};
-
-// One tile of 64 columns.  x: scores in the C-fragment layout of eight 16 x 8
-// tiles; col(j, e): the token (within the page) of column 2 t + e of tile j;
-// lim: last visible token of each row relative to the page; lv = log2 s_V.
-// Returns the weights as A fragments.
-template <int D, class Col>
-__device__ __forceinline__ void softmax_tile(AttnState<D>& st, float (&x)[8][4], const int (&lim)[2], float xs, float lv,
-                                             float inv_sv, bool masked, Col col, uint32_t (&pf)[8][2]) {
-    float mx[2] = {st.m[0], st.m[1]};
-#pragma unroll
-    for (int j = 0; j < 8; ++j)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            float v = fmaf(x[j][e], xs, lv);
-            if (masked && col(j, e & 1) > lim[e >> 1]) v = -INFINITY;
-            x[j][e] = v;
-            mx[e >> 1] = fmaxf(mx[e >> 1], v);
-        }
-    float base[2], corr[2], sum[2] = {0.f, 0.f};
-#pragma unroll
-    for (int r = 0; r < 2; ++r) {
-        mx[r] = fmaxf(mx[r], __shfl_xor_sync(~0u, mx[r], 1));
-        mx[r] = fmaxf(mx[r], __shfl_xor_sync(~0u, mx[r], 2));
-        const float ref = mx[r] == -INFINITY ? 0.f : mx[r];   // nothing visible yet: weights 2^-inf = 0
-        corr[r] = ex2(st.m[r] - ref);
-        st.m[r] = mx[r];
-        base[r] = ref - kWeightExp;
-    }
-#pragma unroll
-    for (int j = 0; j < 8; ++j) {
-        float w[4];
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            w[e] = ex2(x[j][e] - base[e >> 1]);
-            sum[e >> 1] += w[e];
-        }
-        pf[j][0] = h2_as_u32(__floats2half2_rn(w[0], w[1]));
-        pf[j][1] = h2_as_u32(__floats2half2_rn(w[2], w[3]));
-    }
-#pragma unroll
-    for (int r = 0; r < 2; ++r) {
-        sum[r] += __shfl_xor_sync(~0u, sum[r], 1);
-        sum[r] += __shfl_xor_sync(~0u, sum[r], 2);
-        // rows that see nothing of the page take nothing from its scale (which may be NaN)
-        st.l[r] = st.l[r] * corr[r] + (sum[r] == 0.f ? 0.f : sum[r] * inv_sv);
-    }
-#pragma unroll
-    for (int n = 0; n < D / 8; ++n)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) st.o[n][e] *= corr[e >> 1];
+__device__ __forceinline__ uint32_t movm(uint32_t x) {            // 8 x 8 fp16 matrix across the warp, transposed
+    uint32_t y;
+    asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+    return y;
+}
+// Returns when this warp's loads behind x have arrived: what they read may be overwritten.
+__device__ __forceinline__ void arrived(uint32_t x) {
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\tsetp.eq.u32 p, %0, 1;\n\tvote.sync.any.pred q, p, 0xffffffff;\n\t}" ::"r"(x)
+        : "memory");
 }
 
-// One block: 16 rows (row = new token i and query head gq of the kv head's
-// group, i G + gq) of one sequence and kv head, over share s of the pages.
-// Its warps take the pages in turn, each with a ring of K and V halves filled
-// by bulk copies; lane (g, t) feeds the MMA 16 consecutive bytes of a row at a
-// time (k in the order 16 t + 4 step, the same in both operands).  The warps'
-// results meet in shared memory, the shares' in the workspace: the share that
-// counts last adds them in share order.
-template <int D>
-__global__ void __launch_bounds__(kAttnWarps * 32) kv_attention_kernel(const __grid_constant__ KvAttnArgs a) {
+// Running softmax of a warp's 8 RN rows.  Scores come as S^T = K Q^T and outputs
+// as O^T = V^T P^T: with the tokens in the MMA's rows, as few as 8 query rows
+// fill its columns (16 in its rows would be half empty for most decode steps:
+// the products took twice the instructions and the softmax twice the registers).
+// This lane: query rows 8 r + 2 t + e; tokens (dimensions) g and g + 8 of a tile.
+template <int D, int RN>
+struct AttnState {
+    float m[RN][2], l[RN][2], o[RN][D / 16][4];          // l: this lane's tokens only
+};
+
+// NT tiles of 16 tokens.  tok(i, u): token, within the page, of row g + 8 u of
+// tile i; lim: last visible token of each query row; lv = log2 s_V.  Returns the
+// weights as B fragments (k = tokens, n = query rows).
+template <int D, int RN, int NT, class Tok>
+__device__ __forceinline__ void softmax_tile(AttnState<D, RN>& st, float (&x)[RN][NT][4], const int (&lim)[RN][2], float xs,
+                                             float lv, float inv_sv, bool masked, Tok tok, uint32_t (&pf)[RN][NT][2]) {
+    float corr[RN][2];
+    bool moved = false;
+#pragma unroll
+    for (int r = 0; r < RN; ++r) {
+        float mx[2] = {-INFINITY, -INFINITY};
+#pragma unroll
+        for (int i = 0; i < NT; ++i)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                float v = fmaf(x[r][i][e], xs, lv);
+                if (masked && tok(i, e >> 1) > lim[r][e & 1]) v = -INFINITY;
+                x[r][i][e] = v;
+                mx[e & 1] = fmaxf(mx[e & 1], v);
+            }
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+            mx[e] = fmaxf(mx[e], __shfl_xor_sync(~0u, mx[e], 4));
+            mx[e] = fmaxf(mx[e], __shfl_xor_sync(~0u, mx[e], 8));
+            mx[e] = fmaxf(st.m[r][e], fmaxf(mx[e], __shfl_xor_sync(~0u, mx[e], 16)));
+            const float ref = mx[e] == -INFINITY ? 0.f : mx[e];       // nothing visible yet: weights 2^-inf = 0
+            corr[r][e] = ex2(st.m[r][e] - ref);
+            moved |= corr[r][e] != 1.f;
+            st.m[r][e] = mx[e];
+            const float base = ref - kWeightExp;
+            float sum = 0.f;
+#pragma unroll
+            for (int i = 0; i < NT; ++i) {
+                x[r][i][e] = ex2(x[r][i][e] - base);
+                x[r][i][e + 2] = ex2(x[r][i][e + 2] - base);
+                sum += x[r][i][e] + x[r][i][e + 2];
+            }
+            // tokens that are not seen take nothing from the page's scale (which may be NaN)
+            st.l[r][e] = st.l[r][e] * corr[r][e] + (sum == 0.f ? 0.f : sum * inv_sv);
+        }
+#pragma unroll
+        for (int i = 0; i < NT; ++i) {
+            pf[r][i][0] = movm(h2_as_u32(__floats2half2_rn(x[r][i][0], x[r][i][1])));
+            pf[r][i][1] = movm(h2_as_u32(__floats2half2_rn(x[r][i][2], x[r][i][3])));
+        }
+    }
+    if (__any_sync(~0u, moved)) {
+#pragma unroll
+        for (int r = 0; r < RN; ++r)
+#pragma unroll
+            for (int n = 0; n < D / 16; ++n)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) st.o[r][n][e] *= corr[r][e & 1];
+    }
+}
+
+// Units of work: 8 RN query rows (row = new token i and query head gq of the kv
+// head's group, i G + gq) of one sequence and kv head, a page at a time.
+struct AttnSpan {
+    int pages, tiles;                                    // of a sequence: pages (1 at least), tiles of rows
+};
+template <int RN>
+__device__ __forceinline__ AttnSpan attn_span(const KvSeq& s, const KvBatchView& b, int G) {
+    const int p = s.len <= (int64_t)b.max_pages * kKvPage ? (s.len + kKvPage - 1) / kKvPage : 1;
+    return {max(p, 1), (int)(((int64_t)s.nq * G + 8 * RN - 1) / (8 * RN))};
+}
+
+// The pages of all units, in a row, are cut into equal shares, one for each
+// block: sequences of any lengths keep every SM busy to the end (a block for
+// each sequence and head left half of the GPU idle behind the longest).  A block
+// takes its share unit by unit; its warps take the pages in turn, each with a
+// ring of K and V half-pages filled by bulk copies; lane (g, t) feeds the MMA 16
+// consecutive bytes of a row at a time (k in the order 16 t + 4 step, the same in
+// both operands).  The tokens of an incomplete last page are split among the
+// warps.  The warps' results meet in shared memory, the shares' in the
+// workspace: the block that counts last on a unit adds its parts in order.
+template <int D, int RN>
+__global__ void __launch_bounds__(kAttnThreads, RN == 1 ? 3 : 2) kv_attention_kernel(const __grid_constant__ KvAttnArgs a) {
     constexpr int kHalfPage = kKvPage * D;               // bytes of a page's K (or V) of one head
-    constexpr int kPanels = D / 64;
+    constexpr int kRing = 256 / D;                       // half-pages in flight per warp: 16 KB
+    constexpr int kPanels = D / 64, kRows = 8 * RN, kPart = D + 4;
     extern __shared__ __align__(128) unsigned char sm[];
-    // [4 warps][ring of 3 half-pages] (later the warps' outputs), [16][D] queries, m / l, barriers
-    uint16_t* sq = reinterpret_cast<uint16_t*>(sm + kAttnWarps * kAttnRing * kHalfPage);
-    float* sml = reinterpret_cast<float*>(sq + 16 * D);  // [warps][16][2]
-    uint64_t* bars = reinterpret_cast<uint64_t*>(sml + kAttnWarps * 32);
-    __shared__ int last_share;
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
-    const int share = blockIdx.x % a.S, tile = (blockIdx.x / a.S) % a.rt;
-    const int bh = blockIdx.x / a.S / a.rt, h = bh % a.c.kv_heads, b = bh / a.c.kv_heads;
-    if (threadIdx.x == 0) {
-        for (int i = 0; i < kAttnWarps * kAttnRing; ++i) mbar_init(bars + i, 1);
+    // [4 warps][ring] (later the warps' outputs, or the parts' factors), m / l of the warps
+    float* sml = reinterpret_cast<float*>(sm + kAttnWarps * kRing * kHalfPage);
+    __shared__ uint64_t bars[kAttnWarps * kRing];
+    __shared__ long long wsum[kAttnWarps];
+    __shared__ int wmax[kAttnWarps], first_seq, last_part;
+    __shared__ long long first_off;
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
+    if (tid == 0) {
+        for (int i = 0; i < kAttnWarps * kRing; ++i) mbar_init(bars + i, 1);
         fence_mbar_init();
     }
     pdl_wait();
     pdl_launch_dependents();
-    const KvSeq s = kv_sequence(a.b, b);
-    const int rows = s.nq * a.G, row0 = tile * 16;
-    if (!s.ok && threadIdx.x == 0) record_status(a.status, GLOWQ_ERR_INDEX);
-    if (row0 >= rows) return;
-    // a length that the table or the tails cannot hold: nothing is visible, and the rows are zero
-    const bool tailed = s.len % kKvPage != 0;
-    const bool bad = s.len > (int64_t)a.b.max_pages * kKvPage || (tailed && (s.slot < 0 || s.slot >= a.c.slots));
-    if (bad && threadIdx.x == 0) record_status(a.status, GLOWQ_ERR_INDEX);
-    const int last_tok = (min(row0 + 15, rows - 1)) / a.G;           // the tile's last new token
-    const int seen = bad ? 0 : max(0, s.start + last_tok + 1);       // tokens that the tile sees
-    const int npages = (seen + kKvPage - 1) / kKvPage;
-    const int per = (npages + a.S - 1) / a.S;
-    const int pa = min(npages, share * per), pb = min(npages, pa + per);
-    const int full = s.len / kKvPage;                                // pages held in codes
-    const int pc = min(pb, full);                                    // ... of this share: [pa, pc); a tail page may follow
-
-    for (int i = threadIdx.x; i < 16 * D / 8; i += kAttnWarps * 32) {
-        const int r = i / (D / 8), row = row0 + r;
-        reinterpret_cast<uint4*>(sq)[i] =
-            ldcg_128_if(a.Q + (int64_t)(s.q0 + row / a.G) * a.ldQ + (int64_t)(h * a.G + row % a.G) * D + (i % (D / 8)) * 8, row < rows);
+    // ---- this block's share [lo, hi) of all pages ----
+    const int each = (a.b.n_seq + kAttnThreads - 1) / kAttnThreads;
+    const int b0 = min(a.b.n_seq, tid * each), b1 = min(a.b.n_seq, b0 + each);
+    long long mine = 0;
+    int most = 0;
+    for (int b = b0; b < b1; ++b) {
+        const KvSeq s = kv_sequence(a.b, b);
+        if (!s.ok) record_status(a.status, GLOWQ_ERR_INDEX);
+        const AttnSpan w = attn_span<RN>(s, a.b, a.G);
+        mine += (long long)w.pages * w.tiles * a.c.kv_heads;
+        if (w.tiles > 0) most = max(most, w.pages);
+    }
+    long long upto = mine;                               // inclusive sum over the threads
+    for (int o = 1; o < 32; o <<= 1) {
+        const long long v = __shfl_up_sync(~0u, upto, o);
+        if (lane >= o) upto += v;
+        most = max(most, __shfl_xor_sync(~0u, most, o));
+    }
+    if (lane == 31) {
+        wsum[warp] = upto;
+        wmax[warp] = most;
     }
     __syncthreads();
-    // Q as A fragments: panel p, step q: dimensions 64 p + 16 t + 4 q .. + 3 of rows g and g + 8
-    uint32_t qf[kPanels][4][4];
+    long long total = 0;
 #pragma unroll
-    for (int p = 0; p < kPanels; ++p)
-#pragma unroll
-        for (int q = 0; q < 4; ++q) {
-            const uint2 u = *reinterpret_cast<const uint2*>(sq + g * D + 64 * p + 16 * t + 4 * q);
-            const uint2 v = *reinterpret_cast<const uint2*>(sq + (g + 8) * D + 64 * p + 16 * t + 4 * q);
-            qf[p][q][0] = u.x;
-            qf[p][q][1] = v.x;
-            qf[p][q][2] = u.y;
-            qf[p][q][3] = v.y;
-        }
-    int limit[2];                                                    // last visible position of rows g, g + 8
-#pragma unroll
-    for (int r = 0; r < 2; ++r) {
-        const int row = row0 + g + 8 * r;
-        limit[r] = row < rows ? s.start + row / a.G : -1;
+    for (int w = 0; w < kAttnWarps; ++w) {
+        if (w < warp) upto += wsum[w];
+        total += wsum[w];
+        most = max(most, wmax[w]);
     }
-    const int least = s.start + row0 / a.G;                          // smallest limit of the tile's rows
-    const bool short_tile = row0 + 16 > rows;
-
-    AttnState<D> st;
-    st.m[0] = st.m[1] = -INFINITY;
-    st.l[0] = st.l[1] = 0.f;
-#pragma unroll
-    for (int n = 0; n < D / 8; ++n)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) st.o[n][e] = 0.f;
-
-    unsigned char* ring = sm + warp * kAttnRing * kHalfPage;
-    uint64_t* wbar = bars + warp * kAttnRing;
-    const int* table = a.b.table + (int64_t)b * a.b.max_pages;
-    // half-pages in the order K, V of this warp's pages; the next one to fetch
-    int fp = pa + warp, fh = 0, fs = 0;
-    auto fetch = [&]() {
-        if (fp < pc) {
-            const int page = ldcg_s32(table + fp);
-            if (lane == 0 && page >= 0 && page < a.c.pages) {
-                const int64_t at = ((int64_t)page * a.c.kv_heads + h) * kHalfPage;
-                attn_bulk(smem_u32(ring + fs * kHalfPage), (fh ? a.c.v_codes : a.c.k_codes) + at, kHalfPage, wbar + fs);
-            }
-            if (fh) fp += kAttnWarps;
-            fh ^= 1;
+    // a page for each warp at least; a unit in kAttnParts shares at most
+    const long long per = max(max((total + gridDim.x - 1) / gridDim.x, (long long)kAttnWarps), (long long)(most + kAttnParts - 1) / kAttnParts);
+    long long lo = blockIdx.x * per;
+    const long long hi = min(total, lo + per);
+    if (lo >= hi) return;
+    if (lo >= upto - mine && lo < upto) {
+        long long off = lo - (upto - mine);
+        int b = b0;
+        for (; b < b1; ++b) {
+            const AttnSpan w = attn_span<RN>(kv_sequence(a.b, b), a.b, a.G);
+            const long long n = (long long)w.pages * w.tiles * a.c.kv_heads;
+            if (off < n) break;
+            off -= n;
         }
-        if (++fs == kAttnRing) fs = 0;
-    };
-#pragma unroll
-    for (int i = 0; i < kAttnRing; ++i) fetch();
-    int cs = 0;
-    uint32_t phases = 0;                                             // bit i: parity of ring entry i
+        first_seq = b;
+        first_off = off;
+    }
+    __syncthreads();
+    int b = first_seq;
+    long long off = first_off;                           // within the sequence's pages of all heads and tiles
+    unsigned char* ring = sm + warp * kRing * kHalfPage;
+    uint64_t* wbar = bars + warp * kRing;
+    uint32_t phases = 0;                                 // bit i: parity of ring entry i
     bool ok = true;
-    for (int p = pa + warp; p < pc; p += kAttnWarps) {
-        const int page = ldcg_s32(table + p);
-        const bool there = page >= 0 && page < a.c.pages;            // (else nothing was fetched: the page is skipped)
-        if (!there) {
-            if (lane == 0) record_status(a.status, GLOWQ_ERR_INDEX);
-            for (int i = 0; i < 2; ++i) {
-                if (++cs == kAttnRing) cs = 0;
-                fetch();
-            }
+
+    while (lo < hi) {
+        const KvSeq s = kv_sequence(a.b, b);
+        const AttnSpan w = attn_span<RN>(s, a.b, a.G);
+        if (off >= (long long)w.pages * w.tiles * a.c.kv_heads) {
+            off = 0;
+            ++b;
             continue;
         }
-        const int64_t ph = (int64_t)page * a.c.kv_heads + h;
-        const float ks = ldcg_f32(a.c.k_scales + ph), vs = ldcg_f32(a.c.v_scales + ph);
-        float x[8][4];
+        const int unit = (int)(off / w.pages), pa = (int)(off - (long long)unit * w.pages);
+        const int h = unit % a.c.kv_heads, row0 = unit / a.c.kv_heads * kRows, rows = s.nq * a.G;
+        const int take = (int)min(hi - lo, (long long)(w.pages - pa));
+        // a length that the table or the tails cannot hold: nothing is visible, and the rows are zero
+        const bool tailed = s.len % kKvPage != 0;
+        const bool bad = s.len > (int64_t)a.b.max_pages * kKvPage || (tailed && (s.slot < 0 || s.slot >= a.c.slots));
+        if (bad && tid == 0) record_status(a.status, GLOWQ_ERR_INDEX);
+        const int last_tok = min(row0 + kRows - 1, rows - 1) / a.G;  // the tile's last new token
+        const int seen = bad ? 0 : max(0, s.start + last_tok + 1);   // tokens that the tile sees
+        const int pb = min((seen + kKvPage - 1) / kKvPage, pa + take);
+        const int full = s.len / kKvPage, pc = min(pb, full);        // pages in codes: [pa, pc); a tail page may follow
+        const int ntok = s.len - full * kKvPage;                     // tokens of the tail
+        const int64_t tail = ((int64_t)s.slot * a.c.kv_heads + h) * kKvPage * D;
+        const int* table = a.b.table + (int64_t)b * a.b.max_pages;
+        const bool tails = pc < pb && warp * 16 < ntok;
+        if (tails) {                                                 // on its way while the pages are worked on
+            constexpr int kLines = 16 * D * 2 / 128;
+            if (lane < kLines && (warp * 16 + lane * 64 / D) < ntok) {
+                const char* k = reinterpret_cast<const char*>(a.c.k_tail + tail + warp * 16 * D) + lane * 128;
+                const char* v = reinterpret_cast<const char*>(a.c.v_tail + tail + warp * 16 * D) + lane * 128;
+                asm volatile("prefetch.global.L2 [%0];\n\tprefetch.global.L2 [%1];" ::"l"(k), "l"(v));
+            }
+        }
+        // Q as B fragments: panel p, step q: dimensions 64 p + 16 t + 4 q .. + 3 of query row 8 r + g
+        uint32_t qf[RN][kPanels][4][2];
 #pragma unroll
-        for (int j = 0; j < 8; ++j) x[j][0] = x[j][1] = x[j][2] = x[j][3] = 0.f;
-        if (ok) ok = mbar_wait(wbar + cs, (phases >> cs) & 1, a.status);
-        phases ^= 1u << cs;
-        const unsigned char* kp = ring + cs * kHalfPage;
+        for (int r = 0; r < RN; ++r) {
+            const int row = row0 + 8 * r + g;
+            const uint16_t* q = a.Q + (int64_t)(s.q0 + row / a.G) * a.ldQ + (int64_t)(h * a.G + row % a.G) * D + 16 * t;
 #pragma unroll
-        for (int j = 0; j < 8; ++j)
+            for (int p = 0; p < kPanels; ++p) {
+                const uint4 u = ldcg_128_if(q + 64 * p, row < rows), v = ldcg_128_if(q + 64 * p + 8, row < rows);
+                qf[r][p][0][0] = u.x;
+                qf[r][p][0][1] = u.y;
+                qf[r][p][1][0] = u.z;
+                qf[r][p][1][1] = u.w;
+                qf[r][p][2][0] = v.x;
+                qf[r][p][2][1] = v.y;
+                qf[r][p][3][0] = v.z;
+                qf[r][p][3][1] = v.w;
+            }
+        }
+        AttnState<D, RN> st;
+        int limit[RN][2];                                            // last visible position of query rows 8 r + 2 t + e
 #pragma unroll
-            for (int pn = 0; pn < kPanels; ++pn) {
-                const uint4 w = *reinterpret_cast<const uint4*>(kp + (pn * kKvPage + 16 * (g >> 1) + 2 * j + (g & 1)) * 64 + 16 * t);
-                const uint32_t ww[4] = {w.x, w.y, w.z, w.w};
+        for (int r = 0; r < RN; ++r) {
 #pragma unroll
-                for (int q = 0; q < 4; ++q) {
-                    uint32_t bf[2];
-                    cvt_codes(ww[q], bf[0], bf[1]);
-                    mma_16816(x[j], qf[pn][q], bf);
+            for (int e = 0; e < 2; ++e) {
+                const int row = row0 + 8 * r + 2 * t + e;
+                limit[r][e] = row < rows ? s.start + row / a.G : -1;
+                st.m[r][e] = -INFINITY;
+                st.l[r][e] = 0.f;
+            }
+#pragma unroll
+            for (int n = 0; n < D / 16; ++n) st.o[r][n][0] = st.o[r][n][1] = st.o[r][n][2] = st.o[r][n][3] = 0.f;
+        }
+        const int least = row0 + kRows > rows ? -1 : s.start + row0 / a.G;   // no column behind it is masked
+
+        // this warp's pages pa + warp, + 4, ...: page ids and scales of 32 at a time, one in each lane
+        for (int p0 = pa + warp; p0 < pc; p0 += 32 * kAttnWarps) {
+            const int n = min(32, (pc - p0 + kAttnWarps - 1) / kAttnWarps);
+            int id = -1;
+            float ks = 0.f, vs = 1.f;
+            if (lane < n) {
+                id = ldcg_s32(table + p0 + lane * kAttnWarps);
+                if (id < 0 || id >= a.c.pages) {
+                    record_status(a.status, GLOWQ_ERR_INDEX);
+                    id = -1;
+                } else {
+                    ks = ldcg_f32(a.c.k_scales + (int64_t)id * a.c.kv_heads + h);
+                    vs = ldcg_f32(a.c.v_scales + (int64_t)id * a.c.kv_heads + h);
                 }
             }
-        __syncwarp();
-        if (++cs == kAttnRing) cs = 0;
-        fetch();
-        const int lim[2] = {limit[0] - p * kKvPage, limit[1] - p * kKvPage};
-        uint32_t pf[8][2];
-        softmax_tile<D>(st, x, lim, ks * a.scale_log2, log2f(vs), 1.f / vs, short_tile || least < p * kKvPage + kKvPage - 1,
-                        [&](int j, int e) { return 16 * t + 2 * j + e; }, pf);
-        if (ok) ok = mbar_wait(wbar + cs, (phases >> cs) & 1, a.status);
-        phases ^= 1u << cs;
-        const unsigned char* vp = ring + cs * kHalfPage;
+            __syncwarp();
+            const float lvs = log2f(vs), ivs = 1.f / vs;
+            auto fetch = [&](int f) {                                // half-pages in the order K, V of each page
+                const int page = __shfl_sync(~0u, id, (f >> 1) & 31);
+                if (f < 2 * n && page >= 0 && lane == 0) {
+                    const int64_t at = ((int64_t)page * a.c.kv_heads + h) * kHalfPage;
+                    uint64_t* bar = wbar + f % kRing;
+                    mbar_arrive_expect_tx(bar, kHalfPage);
+                    bulk_g2s(smem_u32(ring + (f % kRing) * kHalfPage), ((f & 1) ? a.c.v_codes : a.c.k_codes) + at, kHalfPage, bar);
+                }
+            };
+            for (int f = 0; f < kRing; ++f) fetch(f);
+            for (int k = 0; k < n; ++k) {
+                if (__shfl_sync(~0u, id, k) < 0) {                   // not there: skipped, nothing was fetched
+                    fetch(2 * k + kRing);
+                    fetch(2 * k + 1 + kRing);
+                    continue;
+                }
+                const int kslot = (2 * k) % kRing, vslot = kslot + 1;
+                const int p = p0 + k * kAttnWarps;
+                float x[RN][4][4];
 #pragma unroll
-        for (int n = 0; n < D / 8; ++n) {
-            const uint4 w = *reinterpret_cast<const uint4*>(vp + (8 * n + g) * kKvPage + 16 * t);
-            const uint32_t ww[4] = {w.x, w.y, w.z, w.w};
+                for (int r = 0; r < RN; ++r)
 #pragma unroll
-            for (int q = 0; q < 4; ++q) {
-                uint32_t bf[2];
-                cvt_codes(ww[q], bf[0], bf[1]);
-                const uint32_t af[4] = {pf[2 * q][0], pf[2 * q][1], pf[2 * q + 1][0], pf[2 * q + 1][1]};
-                mma_16816(st.o[n], af, bf);
+                    for (int i = 0; i < 4; ++i) x[r][i][0] = x[r][i][1] = x[r][i][2] = x[r][i][3] = 0.f;
+                if (ok) ok = mbar_wait(wbar + kslot, (phases >> kslot) & 1, a.status);
+                phases ^= 1u << kslot;
+                const unsigned char* kp = ring + kslot * kHalfPage + (16 * (g >> 1) + (g & 1)) * 64 + 16 * t;
+                uint32_t seen_words = 0;
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+#pragma unroll
+                    for (int pn = 0; pn < kPanels; ++pn) {           // rows g and g + 8: tokens 16 (g / 2) + 4 i + g % 2 and + 2
+                        const uint4 u = *reinterpret_cast<const uint4*>(kp + (pn * kKvPage + 4 * i) * 64);
+                        const uint4 v = *reinterpret_cast<const uint4*>(kp + (pn * kKvPage + 4 * i + 2) * 64);
+                        const uint32_t uu[4] = {u.x, u.y, u.z, u.w}, vv[4] = {v.x, v.y, v.z, v.w};
+                        seen_words |= u.w | v.w;
+#pragma unroll
+                        for (int q = 0; q < 4; ++q) {
+                            uint32_t af[4];
+                            cvt_codes(uu[q], af[0], af[2]);
+                            cvt_codes(vv[q], af[1], af[3]);
+#pragma unroll
+                            for (int r = 0; r < RN; ++r) mma_16816(x[r][i], af, qf[r][pn][q]);
+                        }
+                    }
+                arrived(seen_words);
+                fetch(2 * k + kRing);
+                int lim[RN][2];
+#pragma unroll
+                for (int r = 0; r < RN; ++r)
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) lim[r][e] = limit[r][e] - p * kKvPage;
+                uint32_t pf[RN][4][2];
+                const float xs = __shfl_sync(~0u, ks, k) * a.scale_log2, lv = __shfl_sync(~0u, lvs, k), iv = __shfl_sync(~0u, ivs, k);
+                softmax_tile<D, RN, 4>(st, x, lim, xs, lv, iv, least < p * kKvPage + kKvPage - 1,
+                                       [&](int i, int u) { return 16 * (g >> 1) + 4 * i + (g & 1) + 2 * u; }, pf);
+                if (ok) ok = mbar_wait(wbar + vslot, (phases >> vslot) & 1, a.status);
+                phases ^= 1u << vslot;
+                const unsigned char* vp = ring + vslot * kHalfPage + g * kKvPage + 16 * t;
+                seen_words = 0;
+#pragma unroll
+                for (int d = 0; d < D / 16; ++d) {
+                    const uint4 u = *reinterpret_cast<const uint4*>(vp + 16 * d * kKvPage);
+                    const uint4 v = *reinterpret_cast<const uint4*>(vp + (16 * d + 8) * kKvPage);
+                    const uint32_t uu[4] = {u.x, u.y, u.z, u.w}, vv[4] = {v.x, v.y, v.z, v.w};
+                    seen_words |= u.w | v.w;
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) {
+                        uint32_t af[4];
+                        cvt_codes(uu[q], af[0], af[2]);
+                        cvt_codes(vv[q], af[1], af[3]);
+#pragma unroll
+                        for (int r = 0; r < RN; ++r) mma_16816(st.o[r][d], af, pf[r][q]);
+                    }
+                }
+                arrived(seen_words);
+                fetch(2 * k + 1 + kRing);
             }
         }
-        __syncwarp();
-        if (++cs == kAttnRing) cs = 0;
-        fetch();
-    }
-    // The incomplete last page, fp16, by the warp whose turn it is: keys and then
-    // values staged with cp.async in rows of 16-byte chunks c at c ^ (row % 8);
-    // tokens past the end are zero.
-    if (pc < pb && (pc - pa) % kAttnWarps == warp) {
-        const int ntok = s.len - full * kKvPage;
-        const int64_t tail = ((int64_t)s.slot * a.c.kv_heads + h) * kHalfPage;
-        constexpr int kCh = D / 8;                                   // 16-byte chunks of a row
-        const uint32_t rb = smem_u32(ring);
-        auto stage = [&](const uint16_t* src) {
-            for (int i = lane; i < kKvPage * kCh; i += 32) {
-                const int r = i / kCh, c = i % kCh;
-                const uint32_t n = r < ntok ? 16u : 0u;
-                asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(rb + (uint32_t)((r * kCh + (c ^ (r & 7))) * 16)),
-                             "l"(src + tail + (int64_t)r * D + 8 * c), "r"(n)
-                             : "memory");
-            }
-            asm volatile("cp.async.commit_group;\n\tcp.async.wait_group 0;" ::: "memory");
-            __syncwarp();
-        };
-        stage(a.c.k_tail);
-        float x[8][4];
+        // The incomplete last page, fp16: 16 tokens to a warp, staged with cp.async
+        // in rows of 16-byte chunks c at c ^ (row % 8); tokens past the end are zero.
+        if (tails) {
+            constexpr int kCh = D / 8;                               // 16-byte chunks of a row
+            const uint32_t kb = smem_u32(ring), vb = kb + 16 * D * 2;
+            unsigned char* vp = ring + 16 * D * 2;
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            x[j][0] = x[j][1] = x[j][2] = x[j][3] = 0.f;
-            const int r = 8 * j + g;
+            for (int i = lane; i < 16 * kCh; i += 32) {
+                const int r = i / kCh, c = i % kCh;
+                const uint32_t n = warp * 16 + r < ntok ? 16u : 0u, to = (uint32_t)((r * kCh + (c ^ (r & 7))) * 16);
+                const int64_t from = tail + (int64_t)(warp * 16 + r) * D + 8 * c;
+                asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(kb + to), "l"(a.c.k_tail + from), "r"(n) : "memory");
+                asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(vb + to), "l"(a.c.v_tail + from), "r"(n) : "memory");
+            }
+            asm volatile("cp.async.wait_all;" ::: "memory");
+            __syncwarp();
+            float x[RN][1][4];
+#pragma unroll
+            for (int r = 0; r < RN; ++r) x[r][0][0] = x[r][0][1] = x[r][0][2] = x[r][0][3] = 0.f;
 #pragma unroll
             for (int pn = 0; pn < kPanels; ++pn) {
-                const int c0 = 8 * pn + 2 * t;
-                const uint4 u = *reinterpret_cast<const uint4*>(ring + (r * kCh + (c0 ^ (r & 7))) * 16);
-                const uint4 v = *reinterpret_cast<const uint4*>(ring + (r * kCh + ((c0 + 1) ^ (r & 7))) * 16);
-                const uint32_t b0[2] = {u.x, u.y}, b1[2] = {u.z, u.w}, b2[2] = {v.x, v.y}, b3[2] = {v.z, v.w};
-                mma_16816(x[j], qf[pn][0], b0);
-                mma_16816(x[j], qf[pn][1], b1);
-                mma_16816(x[j], qf[pn][2], b2);
-                mma_16816(x[j], qf[pn][3], b3);
+                const int c0 = 8 * pn + 2 * t;                       // rows g and g + 8 (the same swizzle)
+                const uint4 u0 = *reinterpret_cast<const uint4*>(ring + (g * kCh + (c0 ^ g)) * 16);
+                const uint4 u1 = *reinterpret_cast<const uint4*>(ring + (g * kCh + ((c0 + 1) ^ g)) * 16);
+                const uint4 v0 = *reinterpret_cast<const uint4*>(ring + ((g + 8) * kCh + (c0 ^ g)) * 16);
+                const uint4 v1 = *reinterpret_cast<const uint4*>(ring + ((g + 8) * kCh + ((c0 + 1) ^ g)) * 16);
+                const uint32_t af[4][4] = {{u0.x, v0.x, u0.y, v0.y}, {u0.z, v0.z, u0.w, v0.w}, {u1.x, v1.x, u1.y, v1.y}, {u1.z, v1.z, u1.w, v1.w}};
+#pragma unroll
+                for (int q = 0; q < 4; ++q)
+#pragma unroll
+                    for (int r = 0; r < RN; ++r) mma_16816(x[r][0], af[q], qf[r][pn][q]);
             }
-        }
-        __syncwarp();
-        stage(a.c.v_tail);
-        // A value that is not finite makes NaN of the rows that see its token and
-        // must not reach the others (0 x inf): it is taken out of the product and
-        // its token's scores become NaN instead.  The others' largest magnitude
-        // gives the tail the power of two that brings it to 64 .. 128, as codes
-        // are, so that its weights share their range (2^-k plays s_V's part).
-        uint64_t poison = 0;
-        __half2 am = __half2half2(__ushort_as_half(0));
-        for (int i = lane; i < kKvPage * kCh; i += 32) {
-            const int r = i / kCh;
-            uint4* q = reinterpret_cast<uint4*>(ring + i * 16);
-            uint32_t w[4] = {q->x, q->y, q->z, q->w};
-            bool hit = false;
+            // A value that is not finite makes NaN of the rows that see its token and
+            // must not reach the others (0 x inf): it is taken out of the product and
+            // its token's scores become NaN instead.  The others' largest magnitude
+            // gives the tokens the power of two that brings it to 64 .. 128, as codes
+            // are, so that their weights share codes' range (2^-k plays s_V's part).
+            uint32_t poison = 0;
+            __half2 am = __half2half2(__ushort_as_half(0));
+            for (int i = lane; i < 16 * kCh; i += 32) {
+                uint4* q = reinterpret_cast<uint4*>(vp + i * 16);
+                uint32_t v[4] = {q->x, q->y, q->z, q->w};
+                bool hit = false;
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                const bool l = (w[e] & 0x7c00u) == 0x7c00u, u = (w[e] & 0x7c000000u) == 0x7c000000u;
-                if (l) w[e] &= 0xffff0000u;
-                if (u) w[e] &= 0x0000ffffu;
-                hit |= l || u;
-                am = __hmax2(am, __habs2(u32_as_h2(w[e])));
+                for (int e = 0; e < 4; ++e) {
+                    const bool l = (v[e] & 0x7c00u) == 0x7c00u, u = (v[e] & 0x7c000000u) == 0x7c000000u;
+                    if (l) v[e] &= 0xffff0000u;
+                    if (u) v[e] &= 0x0000ffffu;
+                    hit |= l || u;
+                    am = __hmax2(am, __habs2(u32_as_h2(v[e])));
+                }
+                if (hit) {
+                    *q = make_uint4(v[0], v[1], v[2], v[3]);
+                    poison |= 1u << (i / kCh);
+                }
             }
-            if (hit) {
-                *q = make_uint4(w[0], w[1], w[2], w[3]);
-                poison |= 1ull << r;
+            uint32_t ex = max(h2_as_u32(am) & 0x7c00u, (h2_as_u32(am) >> 16) & 0x7c00u) >> 10;   // biased by 15
+            for (int o = 16; o > 0; o >>= 1) {
+                poison |= __shfl_xor_sync(~0u, poison, o);
+                ex = max(ex, __shfl_xor_sync(~0u, ex, o));
             }
-        }
-        uint32_t ex = max(h2_as_u32(am) & 0x7c00u, (h2_as_u32(am) >> 16) & 0x7c00u) >> 10;   // biased by 15
-        for (int o = 16; o > 0; o >>= 1) {
-            poison |= __shfl_xor_sync(~0u, poison, o);
-            ex = max(ex, __shfl_xor_sync(~0u, ex, o));
-        }
-        const int k2 = min(15, 21 - (int)ex);                        // -9 .. 15: 2^k2 is a normal fp16
-        const __half2 up = __half2half2(__ushort_as_half((unsigned short)((k2 + 15) << 10)));
-        __syncwarp();
-        if (poison) {
+            const int k2 = min(15, 21 - (int)ex);                    // -9 .. 15: 2^k2 is a normal fp16
+            const __half2 up = __half2half2(__ushort_as_half((unsigned short)((k2 + 15) << 10)));
+            __syncwarp();
+            if (poison) {
 #pragma unroll
-            for (int j = 0; j < 8; ++j)
+                for (int r = 0; r < RN; ++r)
 #pragma unroll
-                for (int e = 0; e < 4; ++e)
-                    if ((poison >> (8 * j + 2 * t + (e & 1))) & 1) x[j][e] = __int_as_float(0x7fffffff);
-        }
-        const int lim[2] = {min(limit[0] - full * kKvPage, ntok - 1), min(limit[1] - full * kKvPage, ntok - 1)};
-        uint32_t pf[8][2];
-        softmax_tile<D>(st, x, lim, a.scale_log2, (float)-k2, exp2f((float)k2), true, [&](int j, int e) { return 8 * j + 2 * t + e; }, pf);
+                    for (int e = 0; e < 4; ++e)
+                        if ((poison >> (g + 8 * (e >> 1))) & 1) x[r][0][e] = __int_as_float(0x7fffffff);
+            }
+            int lim[RN][2];
 #pragma unroll
-        for (int q = 0; q < 4; ++q) {
-            const uint32_t af[4] = {pf[2 * q][0], pf[2 * q][1], pf[2 * q + 1][0], pf[2 * q + 1][1]};
+            for (int r = 0; r < RN; ++r)
 #pragma unroll
-            for (int n = 0; n < D / 16; ++n) {
-                // four 8 x 8 matrices: tokens 16 q .. + 7 and + 8 .. + 15 of dimensions 16 n .. + 7, then of + 8 .. + 15
-                const int r = 16 * q + (lane & 15), c = 2 * n + (lane >> 4);
+                for (int e = 0; e < 2; ++e) lim[r][e] = min(limit[r][e] - full * kKvPage, ntok - 1) - warp * 16;
+            uint32_t pf[RN][1][2];
+            softmax_tile<D, RN, 1>(st, x, lim, a.scale_log2, (float)-k2, exp2f((float)k2), true, [&](int, int u) { return g + 8 * u; }, pf);
+#pragma unroll
+            for (int d = 0; d < D / 16; ++d) {
+                // four 8 x 8 matrices: dimensions 16 d .. + 7 and + 8 .. + 15 of tokens 0 .. 7, then of tokens 8 .. 15
+                const int r = (lane & 7) + (lane >> 4) * 8, c = 2 * d + ((lane >> 3) & 1);
                 uint32_t v[4];
-                ldsm4t(rb + (uint32_t)((r * kCh + (c ^ (r & 7))) * 16), v);
+                ldsm4t(vb + (uint32_t)((r * kCh + (c ^ (r & 7))) * 16), v);
 #pragma unroll
                 for (int e = 0; e < 4; ++e) v[e] = h2_as_u32(__hmul2(u32_as_h2(v[e]), up));
-                const uint32_t b0[2] = {v[0], v[1]}, b1[2] = {v[2], v[3]};
-                mma_16816(st.o[2 * n], af, b0);
-                mma_16816(st.o[2 * n + 1], af, b1);
+#pragma unroll
+                for (int q = 0; q < RN; ++q) mma_16816(st.o[q][d], v, pf[q][0]);
             }
         }
-    }
-    // ---- the warps' results: [warp][16][D] over the rings, m and l beside them ----
-    __syncthreads();
-    float* so = reinterpret_cast<float*>(sm) + warp * 16 * D;
+        // ---- the warps' results: [warp][rows][D + 4] over the rings, m and l beside them ----
 #pragma unroll
-    for (int n = 0; n < D / 8; ++n) {
-        *reinterpret_cast<float2*>(so + g * D + 8 * n + 2 * t) = make_float2(st.o[n][0], st.o[n][1]);
-        *reinterpret_cast<float2*>(so + (g + 8) * D + 8 * n + 2 * t) = make_float2(st.o[n][2], st.o[n][3]);
-    }
-    if (t == 0) {
-        sml[(warp * 16 + g) * 2] = st.m[0];
-        sml[(warp * 16 + g) * 2 + 1] = st.l[0];
-        sml[(warp * 16 + g + 8) * 2] = st.m[1];
-        sml[(warp * 16 + g + 8) * 2 + 1] = st.l[1];
-    }
-    __syncthreads();
-    const int64_t unit = (int64_t)bh * a.rt + tile;
-    float* part = a.partial + unit * a.S * 16 * (D + 2);
-    // parts of one row, in order: each with its own m, l and outputs
-    auto merge = [&](int n, auto m_of, auto l_of, auto o_of, float& m, float& l, float4& o) {
-        m = -INFINITY;
-        l = 0.f;
-        o = make_float4(0.f, 0.f, 0.f, 0.f);
-        for (int w = 0; w < n; ++w) m = fmaxf(m, m_of(w));
-        const float ref = m == -INFINITY ? 0.f : m;
-        for (int w = 0; w < n; ++w) {
-            const float lw = l_of(w), f = ex2(m_of(w) - ref);
-            if (lw == 0.f) continue;                                 // saw nothing (a NaN part stays: f NaN is NaN, 0 NaN too)
-            const float4 p = o_of(w);
-            l = fmaf(f, lw, l);
-            o.x = fmaf(f, p.x, o.x);
-            o.y = fmaf(f, p.y, o.y);
-            o.z = fmaf(f, p.z, o.z);
-            o.w = fmaf(f, p.w, o.w);
+        for (int r = 0; r < RN; ++r)
+#pragma unroll
+            for (int e = 0; e < 2; ++e)
+                for (int o = 4; o < 32; o <<= 1) st.l[r][e] += __shfl_xor_sync(~0u, st.l[r][e], o);
+        __syncthreads();
+        float* all = reinterpret_cast<float*>(sm);
+#pragma unroll
+        for (int r = 0; r < RN; ++r) {
+            float* so = all + (warp * kRows + 8 * r + 2 * t) * kPart + g;
+#pragma unroll
+            for (int d = 0; d < D / 16; ++d) {
+                so[16 * d] = st.o[r][d][0];
+                so[kPart + 16 * d] = st.o[r][d][1];
+                so[16 * d + 8] = st.o[r][d][2];
+                so[kPart + 16 * d + 8] = st.o[r][d][3];
+            }
+            if (g == 0) {
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    sml[(warp * kRows + 8 * r + 2 * t + e) * 2] = st.m[r][e];
+                    sml[(warp * kRows + 8 * r + 2 * t + e) * 2 + 1] = st.l[r][e];
+                }
+            }
         }
-    };
-    auto store = [&](int r, int c, float l, const float4& o) {
-        const int row = row0 + r;
-        if (row >= rows) return;
-        const float inv = l == 0.f ? 0.f : 1.f / l;                  // a row that sees nothing is zero
-        uint2 y;
-        y.x = h2_as_u32(__floats2half2_rn(o.x * inv, o.y * inv));
-        y.y = h2_as_u32(__floats2half2_rn(o.z * inv, o.w * inv));
-        *reinterpret_cast<uint2*>(a.Y + (int64_t)(s.q0 + row / a.G) * a.ldY + (int64_t)(h * a.G + row % a.G) * D + 4 * c) = y;
-    };
-    for (int i = threadIdx.x; i < 16 * D / 4; i += kAttnWarps * 32) {
-        const int r = i / (D / 4), c = i % (D / 4);
-        float m, l;
-        float4 o;
-        merge(kAttnWarps, [&](int w) { return sml[(w * 16 + r) * 2]; }, [&](int w) { return sml[(w * 16 + r) * 2 + 1]; },
-              [&](int w) { return *reinterpret_cast<const float4*>(reinterpret_cast<const float*>(sm) + (w * 16 + r) * D + 4 * c); },
-              m, l, o);
-        if (a.S == 1) {
-            store(r, c, l, o);
-        } else {
-            float* q = part + (share * 16 + r) * (D + 2);
-            __stcg(reinterpret_cast<float2*>(q + 4 * c), make_float2(o.x, o.y));
-            __stcg(reinterpret_cast<float2*>(q + 4 * c + 2), make_float2(o.z, o.w));
-            if (c == 0) __stcg(reinterpret_cast<float2*>(q + D), make_float2(m, l));
+        __syncthreads();
+        const bool whole = pa == 0 && take == w.pages;
+        auto store = [&](int r, int c, float l, const float4& o) {
+            const int row = row0 + r;
+            if (row >= rows) return;
+            const float inv = l == 0.f ? 0.f : 1.f / l;              // a row that sees nothing is zero
+            uint2 y;
+            y.x = h2_as_u32(__floats2half2_rn(o.x * inv, o.y * inv));
+            y.y = h2_as_u32(__floats2half2_rn(o.z * inv, o.w * inv));
+            *reinterpret_cast<uint2*>(a.Y + (int64_t)(s.q0 + row / a.G) * a.ldY + (int64_t)(h * a.G + row % a.G) * D + 4 * c) = y;
+        };
+        // a part that starts its unit is its block's last, every other one its block's first
+        float* part = a.partial + ((int64_t)blockIdx.x * 2 + (pa == 0)) * kRows * kPart;
+#pragma unroll 1
+        for (int i = tid; i < kRows * D / 4; i += kAttnThreads) {
+            const int r = i / (D / 4), c = i % (D / 4);
+            float m = -INFINITY, l = 0.f;
+            float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+            for (int k = 0; k < kAttnWarps; ++k) m = fmaxf(m, sml[(k * kRows + r) * 2]);
+            const float ref = m == -INFINITY ? 0.f : m;
+#pragma unroll
+            for (int k = 0; k < kAttnWarps; ++k) {
+                const float f = ex2(sml[(k * kRows + r) * 2] - ref);
+                const float4 v = *reinterpret_cast<const float4*>(all + (k * kRows + r) * kPart + 4 * c);
+                l = fmaf(f, sml[(k * kRows + r) * 2 + 1], l);
+                o = make_float4(fmaf(f, v.x, o.x), fmaf(f, v.y, o.y), fmaf(f, v.z, o.z), fmaf(f, v.w, o.w));
+            }
+            if (whole) {
+                store(r, c, l, o);
+            } else {
+                __stcg(reinterpret_cast<float4*>(part + r * kPart + 4 * c), o);
+                if (c == 0) __stcg(reinterpret_cast<float2*>(part + r * kPart + D), make_float2(m, l));
+            }
         }
-    }
-    if (a.S == 1) return;
-    __threadfence();
-    __syncthreads();
-    if (threadIdx.x == 0) {
-        unsigned int prev;
-        asm volatile("atom.acq_rel.gpu.global.add.u32 %0, [%1], 1;" : "=r"(prev) : "l"(a.tickets + unit) : "memory");
-        last_share = prev == (unsigned)(a.S - 1);
-        if (last_share) atomicExch(a.tickets + unit, 0u);            // every share has counted: ready for the next call
-    }
-    __syncthreads();
-    if (!last_share) return;
-    __threadfence();
-    for (int i = threadIdx.x; i < 16 * D / 4; i += kAttnWarps * 32) {
-        const int r = i / (D / 4), c = i % (D / 4);
-        float m, l;
-        float4 o;
-        const float* q = part + r * (D + 2);
-        const int step = 16 * (D + 2);
-        merge(a.S, [&](int w) { return __ldcg(q + w * step + D); }, [&](int w) { return __ldcg(q + w * step + D + 1); },
-              [&](int w) {
-                  const float2 u = __ldcg(reinterpret_cast<const float2*>(q + w * step + 4 * c));
-                  const float2 v = __ldcg(reinterpret_cast<const float2*>(q + w * step + 4 * c + 2));
-                  return make_float4(u.x, u.y, v.x, v.y);
-              },
-              m, l, o);
-        store(r, c, l, o);
+        if (!whole) {
+            const long long u0 = lo - pa;                            // the unit's first page in the row of all
+            const int first = (int)(u0 / per), parts = (int)((u0 + w.pages - 1) / per) - first + 1;
+            __threadfence();
+            __syncthreads();
+            if (tid == 0) {
+                unsigned int prev;
+                asm volatile("atom.acq_rel.gpu.global.add.u32 %0, [%1], 1;" : "=r"(prev) : "l"(a.tickets + first) : "memory");
+                last_part = prev == (unsigned)(parts - 1);
+                if (last_part) atomicExch(a.tickets + first, 0u);    // every part has counted: ready for the next call
+            }
+            __syncthreads();
+            if (last_part) {
+                __threadfence();
+                auto of = [&](int k) { return a.partial + ((int64_t)(first + k) * 2 + (k == 0)) * kRows * kPart; };
+                // every part's m, then its factor 2^(m - max), [part][row] over the rings; the rows' l
+                for (int i = tid; i < parts * kRows; i += kAttnThreads) {
+                    const float2 ml = __ldcg(reinterpret_cast<const float2*>(of(i / kRows) + (i % kRows) * kPart + D));
+                    all[2 * i] = ml.x;
+                    all[2 * i + 1] = ml.y;
+                }
+                __syncthreads();
+                for (int r = warp; r < kRows; r += kAttnWarps) {
+                    float m = -INFINITY, l = 0.f;
+                    for (int k = lane; k < parts; k += 32) m = fmaxf(m, all[2 * (k * kRows + r)]);
+                    for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(~0u, m, o));
+                    const float ref = m == -INFINITY ? 0.f : m;
+                    for (int k = lane; k < parts; k += 32) {
+                        const float f = ex2(all[2 * (k * kRows + r)] - ref);
+                        all[2 * (k * kRows + r)] = f;
+                        l = fmaf(f, all[2 * (k * kRows + r) + 1], l);
+                    }
+                    for (int o = 16; o > 0; o >>= 1) l += __shfl_xor_sync(~0u, l, o);
+                    if (lane == 0) sml[r] = l;
+                }
+                __syncthreads();
+                for (int i = tid; i < kRows * D / 4; i += kAttnThreads) {
+                    const int r = i / (D / 4), c = i % (D / 4);
+                    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 8
+                    for (int k = 0; k < parts; ++k) {
+                        const float4 v = __ldcg(reinterpret_cast<const float4*>(of(k) + r * kPart + 4 * c));
+                        const float f = all[2 * (k * kRows + r)];
+                        o = make_float4(fmaf(f, v.x, o.x), fmaf(f, v.y, o.y), fmaf(f, v.z, o.z), fmaf(f, v.w, o.w));
+                    }
+                    store(r, c, sml[r], o);
+                }
+            }
+        }
+        lo += take;
+        off += take;
+        if (lo < hi) {                                               // the rings are filled again by bulk copies
+            fence_proxy_async_all();
+            __syncthreads();
+        }
     }
 }
 
-static size_t attn_smem(int D) {
-    return (size_t)kAttnWarps * kAttnRing * kKvPage * D + 16 * D * 2 + kAttnWarps * 32 * 4 + kAttnWarps * kAttnRing * 8;
-}
+static int attn_rows(int64_t rows) { return rows <= 8 ? 8 : 16; }
+static size_t attn_smem(int rows) { return (size_t)kAttnWarps * 16384 + kAttnWarps * rows * 2 * sizeof(float); }
 
 KvAttnPlan plan_kv_attention(const KvBatchView& b, int G, int kv_heads, int head_dim, int num_sms) {
-    KvAttnPlan p;
-    p.tc = (int64_t)b.max_new * G >= 64;
-    p.rt = (int)(((int64_t)b.max_new * G + 15) / 16);
-    const int64_t units = (int64_t)b.n_seq * kv_heads * p.rt;
-    p.S = 1;
-    if (units > 0 && units < 2 * num_sms) {
-        int64_t S = 2 * num_sms / units;
-        const int64_t most = b.max_pages / kAttnWarps;               // a page for each warp, at least
-        if (S > most) S = most;
-        if (S > 64) S = 64;
-        if (S > 1) p.S = (int)S;
-    }
-    if (p.tc) p.S = 1;
-    p.partial_bytes = p.S > 1 ? (size_t)units * p.S * 16 * (head_dim + 2) * sizeof(float) : 0;
+    KvAttnPlan p = {};
+    const int64_t rows = (int64_t)b.max_new * G;
+    p.tc = rows >= 64;
+    p.rows = attn_rows(rows);
+    // resident blocks, or one for every kAttnWarps pages when there cannot be more
+    const int64_t pages = (int64_t)b.n_seq * (b.max_pages > 0 ? b.max_pages : 1) * kv_heads * ((rows + p.rows - 1) / p.rows);
+    const int64_t want = (pages + kAttnWarps - 1) / kAttnWarps;
+    p.blocks = num_sms * (p.rows == 8 ? 3 : 2);
+    if (p.blocks > want) p.blocks = (int)want;
+    p.partial_bytes = p.tc ? 0 : (size_t)p.blocks * 2 * p.rows * (head_dim + 4) * sizeof(float);
     return p;
 }
 
-template <int D>
-static cudaError_t launch_attn(const KvAttnArgs& a, unsigned grid, cudaStream_t st) {
-    cudaError_t e = cudaFuncSetAttribute((const void*)kv_attention_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                         (int)attn_smem(D));
+template <int D, int RN>
+static cudaError_t launch_attn(const KvAttnArgs& a, int blocks, cudaStream_t st) {
+    const void* f = (const void*)kv_attention_kernel<D, RN>;
+    cudaError_t e = cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)attn_smem(8 * RN));
     if (e != cudaSuccess) return e;
     void* args[] = {(void*)&a};
-    return launch_pdl((const void*)kv_attention_kernel<D>, grid, kAttnWarps * 32, attn_smem(D), st, args);
+    return launch_pdl(f, (unsigned)blocks, kAttnThreads, attn_smem(8 * RN), st, args);
 }
 
 cudaError_t launch_kv_attention(const KvCacheView& c, const KvBatchView& b, const uint16_t* Q, int64_t ldQ, int q_heads,
                                 float scale, uint16_t* Y, int64_t ldY, unsigned int* tickets, float* partial,
                                 const KvAttnPlan& p, cudaStream_t st) {
     if (p.tc) return launch_kv_attention_tc(c, b, Q, ldQ, q_heads, scale, Y, ldY, st);
-    KvAttnArgs a = {c, b, Q, Y, ldQ, ldY, scale * 1.44269504088896340736f, q_heads / c.kv_heads, p.rt, p.S, partial, tickets,
+    KvAttnArgs a = {c, b, Q, Y, ldQ, ldY, scale * 1.44269504088896340736f, q_heads / c.kv_heads, partial, tickets,
                     device_status_ptr()};
-    const unsigned grid = (unsigned)((int64_t)b.n_seq * c.kv_heads * p.rt * p.S);
-    return c.head_dim == 64 ? launch_attn<64>(a, grid, st) : launch_attn<128>(a, grid, st);
+    if (c.head_dim == 64) return p.rows == 8 ? launch_attn<64, 1>(a, p.blocks, st) : launch_attn<64, 2>(a, p.blocks, st);
+    return p.rows == 8 ? launch_attn<128, 1>(a, p.blocks, st) : launch_attn<128, 2>(a, p.blocks, st);
 }
 
 }  // namespace glowq

@@ -58,8 +58,8 @@ cudaError_t launch_kv_read(const KvCacheView& c, const KvBatchView& b, const int
 // attention.cu
 struct KvAttnPlan {
     bool tc;             // many rows: attention_tc.cu
-    int rt;              // 16-row tiles of the widest sequence
-    int S;               // CTAs that share a tile's pages
+    int rows;            // query rows of a block at a time: 8 or 16
+    int blocks;
     size_t partial_bytes;
 };
 KvAttnPlan plan_kv_attention(const KvBatchView& b, int G, int kv_heads, int head_dim, int num_sms);
