@@ -20,6 +20,7 @@ namespace glowq {
 
 constexpr int kAttnWarps = 4;
 constexpr int kAttnThreads = kAttnWarps * 32;
+constexpr int kAttnRing = 4;             // chunks of 4 KB in flight per warp
 constexpr int kAttnParts = 128;          // blocks that share one unit, at most (and the two at its ends)
 constexpr float kWeightExp = 8.f;
 
@@ -156,18 +157,18 @@ __device__ __forceinline__ AttnSpan attn_span(const KvSeq& s, const KvBatchView&
 template <int D, int RN>
 __global__ void __launch_bounds__(kAttnThreads, RN == 1 ? 3 : 2) kv_attention_kernel(const __grid_constant__ KvAttnArgs a) {
     constexpr int kHalfPage = kKvPage * D;               // bytes of a page's K (or V) of one head
-    constexpr int kRing = 256 / D;                       // half-pages in flight per warp: 16 KB
+    constexpr int kChunk = kKvPage * 64;                 // what a bulk copy brings: 64 dimensions of a page's K or V
     constexpr int kPanels = D / 64, kRows = 8 * RN, kPart = D + 4;
     extern __shared__ __align__(128) unsigned char sm[];
     // [4 warps][ring] (later the warps' outputs, or the parts' factors), m / l of the warps
-    float* sml = reinterpret_cast<float*>(sm + kAttnWarps * kRing * kHalfPage);
-    __shared__ uint64_t bars[kAttnWarps * kRing];
+    float* sml = reinterpret_cast<float*>(sm + kAttnWarps * kAttnRing * kChunk);
+    __shared__ uint64_t bars[kAttnWarps * kAttnRing];
     __shared__ long long wsum[kAttnWarps];
     __shared__ int wmax[kAttnWarps], first_seq, last_part;
     __shared__ long long first_off;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
     if (tid == 0) {
-        for (int i = 0; i < kAttnWarps * kRing; ++i) mbar_init(bars + i, 1);
+        for (int i = 0; i < kAttnWarps * kAttnRing; ++i) mbar_init(bars + i, 1);
         fence_mbar_init();
     }
     pdl_wait();
@@ -222,8 +223,8 @@ __global__ void __launch_bounds__(kAttnThreads, RN == 1 ? 3 : 2) kv_attention_ke
     __syncthreads();
     int b = first_seq;
     long long off = first_off;                           // within the sequence's pages of all heads and tiles
-    unsigned char* ring = sm + warp * kRing * kHalfPage;
-    uint64_t* wbar = bars + warp * kRing;
+    unsigned char* ring = sm + warp * kAttnRing * kChunk;
+    uint64_t* wbar = bars + warp * kAttnRing;
     uint32_t phases = 0;                                 // bit i: parity of ring entry i
     bool ok = true;
 
@@ -310,39 +311,40 @@ __global__ void __launch_bounds__(kAttnThreads, RN == 1 ? 3 : 2) kv_attention_ke
             }
             __syncwarp();
             const float lvs = log2f(vs), ivs = 1.f / vs;
-            auto fetch = [&](int f) {                                // half-pages in the order K, V of each page
-                const int page = __shfl_sync(~0u, id, (f >> 1) & 31);
-                if (f < 2 * n && page >= 0 && lane == 0) {
-                    const int64_t at = ((int64_t)page * a.c.kv_heads + h) * kHalfPage;
-                    uint64_t* bar = wbar + f % kRing;
-                    mbar_arrive_expect_tx(bar, kHalfPage);
-                    bulk_g2s(smem_u32(ring + (f % kRing) * kHalfPage), ((f & 1) ? a.c.v_codes : a.c.k_codes) + at, kHalfPage, bar);
+            auto fetch = [&](int f) {                                // chunks in the order K, V of each page
+                const int page = __shfl_sync(~0u, id, f / (2 * kPanels) & 31);
+                if (f < 2 * kPanels * n && page >= 0 && lane == 0) {
+                    const int c = f % (2 * kPanels);
+                    const int64_t at = (((int64_t)page * a.c.kv_heads + h) * kPanels + c % kPanels) * kChunk;
+                    uint64_t* bar = wbar + f % kAttnRing;
+                    mbar_arrive_expect_tx(bar, kChunk);
+                    bulk_g2s(smem_u32(ring + (f % kAttnRing) * kChunk), (c < kPanels ? a.c.k_codes : a.c.v_codes) + at, kChunk, bar);
                 }
             };
-            for (int f = 0; f < kRing; ++f) fetch(f);
+            for (int f = 0; f < kAttnRing; ++f) fetch(f);
             for (int k = 0; k < n; ++k) {
+                const int f0 = 2 * kPanels * k;
                 if (__shfl_sync(~0u, id, k) < 0) {                   // not there: skipped, nothing was fetched
-                    fetch(2 * k + kRing);
-                    fetch(2 * k + 1 + kRing);
+                    for (int f = 0; f < 2 * kPanels; ++f) fetch(f0 + f + kAttnRing);
                     continue;
                 }
-                const int kslot = (2 * k) % kRing, vslot = kslot + 1;
                 const int p = p0 + k * kAttnWarps;
                 float x[RN][4][4];
 #pragma unroll
                 for (int r = 0; r < RN; ++r)
 #pragma unroll
                     for (int i = 0; i < 4; ++i) x[r][i][0] = x[r][i][1] = x[r][i][2] = x[r][i][3] = 0.f;
-                if (ok) ok = mbar_wait(wbar + kslot, (phases >> kslot) & 1, a.status);
-                phases ^= 1u << kslot;
-                const unsigned char* kp = ring + kslot * kHalfPage + (16 * (g >> 1) + (g & 1)) * 64 + 16 * t;
-                uint32_t seen_words = 0;
 #pragma unroll
-                for (int i = 0; i < 4; ++i)
+                for (int pn = 0; pn < kPanels; ++pn) {
+                    const int slot = (f0 + pn) % kAttnRing;
+                    if (ok) ok = mbar_wait(wbar + slot, (phases >> slot) & 1, a.status);
+                    phases ^= 1u << slot;
+                    const unsigned char* kp = ring + slot * kChunk + (16 * (g >> 1) + (g & 1)) * 64 + 16 * t;
+                    uint32_t seen_words = 0;
 #pragma unroll
-                    for (int pn = 0; pn < kPanels; ++pn) {           // rows g and g + 8: tokens 16 (g / 2) + 4 i + g % 2 and + 2
-                        const uint4 u = *reinterpret_cast<const uint4*>(kp + (pn * kKvPage + 4 * i) * 64);
-                        const uint4 v = *reinterpret_cast<const uint4*>(kp + (pn * kKvPage + 4 * i + 2) * 64);
+                    for (int i = 0; i < 4; ++i) {                    // rows g and g + 8: tokens 16 (g / 2) + 4 i + g % 2 and + 2
+                        const uint4 u = *reinterpret_cast<const uint4*>(kp + 4 * i * 64);
+                        const uint4 v = *reinterpret_cast<const uint4*>(kp + (4 * i + 2) * 64);
                         const uint32_t uu[4] = {u.x, u.y, u.z, u.w}, vv[4] = {v.x, v.y, v.z, v.w};
                         seen_words |= u.w | v.w;
 #pragma unroll
@@ -354,8 +356,9 @@ __global__ void __launch_bounds__(kAttnThreads, RN == 1 ? 3 : 2) kv_attention_ke
                             for (int r = 0; r < RN; ++r) mma_16816(x[r][i], af, qf[r][pn][q]);
                         }
                     }
-                arrived(seen_words);
-                fetch(2 * k + kRing);
+                    arrived(seen_words);
+                    fetch(f0 + pn + kAttnRing);
+                }
                 int lim[RN][2];
 #pragma unroll
                 for (int r = 0; r < RN; ++r)
@@ -365,27 +368,31 @@ __global__ void __launch_bounds__(kAttnThreads, RN == 1 ? 3 : 2) kv_attention_ke
                 const float xs = __shfl_sync(~0u, ks, k) * a.scale_log2, lv = __shfl_sync(~0u, lvs, k), iv = __shfl_sync(~0u, ivs, k);
                 softmax_tile<D, RN, 4>(st, x, lim, xs, lv, iv, least < p * kKvPage + kKvPage - 1,
                                        [&](int i, int u) { return 16 * (g >> 1) + 4 * i + (g & 1) + 2 * u; }, pf);
-                if (ok) ok = mbar_wait(wbar + vslot, (phases >> vslot) & 1, a.status);
-                phases ^= 1u << vslot;
-                const unsigned char* vp = ring + vslot * kHalfPage + g * kKvPage + 16 * t;
-                seen_words = 0;
 #pragma unroll
-                for (int d = 0; d < D / 16; ++d) {
-                    const uint4 u = *reinterpret_cast<const uint4*>(vp + 16 * d * kKvPage);
-                    const uint4 v = *reinterpret_cast<const uint4*>(vp + (16 * d + 8) * kKvPage);
-                    const uint32_t uu[4] = {u.x, u.y, u.z, u.w}, vv[4] = {v.x, v.y, v.z, v.w};
-                    seen_words |= u.w | v.w;
+                for (int pn = 0; pn < kPanels; ++pn) {
+                    const int slot = (f0 + kPanels + pn) % kAttnRing;
+                    if (ok) ok = mbar_wait(wbar + slot, (phases >> slot) & 1, a.status);
+                    phases ^= 1u << slot;
+                    const unsigned char* vp = ring + slot * kChunk + g * kKvPage + 16 * t;
+                    uint32_t seen_words = 0;
 #pragma unroll
-                    for (int q = 0; q < 4; ++q) {
-                        uint32_t af[4];
-                        cvt_codes(uu[q], af[0], af[2]);
-                        cvt_codes(vv[q], af[1], af[3]);
+                    for (int d = 0; d < 4; ++d) {
+                        const uint4 u = *reinterpret_cast<const uint4*>(vp + 16 * d * kKvPage);
+                        const uint4 v = *reinterpret_cast<const uint4*>(vp + (16 * d + 8) * kKvPage);
+                        const uint32_t uu[4] = {u.x, u.y, u.z, u.w}, vv[4] = {v.x, v.y, v.z, v.w};
+                        seen_words |= u.w | v.w;
 #pragma unroll
-                        for (int r = 0; r < RN; ++r) mma_16816(st.o[r][d], af, pf[r][q]);
+                        for (int q = 0; q < 4; ++q) {
+                            uint32_t af[4];
+                            cvt_codes(uu[q], af[0], af[2]);
+                            cvt_codes(vv[q], af[1], af[3]);
+#pragma unroll
+                            for (int r = 0; r < RN; ++r) mma_16816(st.o[r][4 * pn + d], af, pf[r][q]);
+                        }
                     }
+                    arrived(seen_words);
+                    fetch(f0 + kPanels + pn + kAttnRing);
                 }
-                arrived(seen_words);
-                fetch(2 * k + 1 + kRing);
             }
         }
         // The incomplete last page, fp16: 16 tokens to a warp, staged with cp.async
