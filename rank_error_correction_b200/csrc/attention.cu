@@ -3,18 +3,24 @@
 //
 //   o_i = sum_j softmax_j(scale q_i . k_j) v_j,   j <= len - n + i  (n new rows)
 //
-// Codes enter the products as the exact integers they are; the page's scales
-// meet them in fp32: s_K on the scores, and s_V inside the exponent, as
+// Products of a complete page are integer products: its codes as they are, the
+// queries as 24-bit fixed point numbers in three 8-bit digits (exact but for
+// elements below 2^-11 of their row's largest, which are off by 2^-23 of it at
+// most), the weights as 24-bit ones of the page's largest in their row (off by
+// 2^-24 of it).  Digits' sums are exact in 32 bits and joined in fp32.  (Codes
+// turned into fp16 for fp16 products cost two thirds of all instructions: 100,000
+// tokens took 109 us.)  The page's scales meet the sums in fp32, s_K on the
+// scores, and s_V inside the exponent, as
 //   w_ij = 2^(x_ij + log2 s_V - m_i),  x_ij = scale log2(e) s_K q_i . k_j
 // with m_i the running maximum of x + log2 s_V.  The numerator is then
-// sum_j w_ij v_j with integer v, and the denominator sum_pages (sum_j w_ij) / s_V,
-// so that weights stay in fp16's range however the pages' scales differ.
-// Weights are scaled by 2^8 (the factor cancels): fp16's smallest normal is
-// then 2^-22 of the largest weight.  One rounding of w to fp16 (2^-11), sums,
-// maxima and outputs in fp32.
+// sum_j w_ij v_j with integer v, and the denominator sum_pages (sum_j w_ij) / s_V.
+// An incomplete last page is fp16, and its products are: weights, scaled by 2^8
+// (the factor cancels; fp16's smallest normal is then 2^-22 of the largest), are
+// rounded to fp16 (2^-11).  Sums, maxima and outputs in fp32.
 #include "common.cuh"
 #include "internal.cuh"
 #include "kvcache.cuh"
+#include "quant8.cuh"
 
 namespace glowq {
 
@@ -37,13 +43,6 @@ struct KvAttnArgs {
     unsigned int* status;
 };
 
-// Four int8 codes as fp16 pairs, exactly: bytes with the sign bit turned are 128 + q, placed in 1024's mantissa.
-__device__ __forceinline__ void cvt_codes(uint32_t w, uint32_t& lo, uint32_t& hi) {
-    const uint32_t u = w ^ 0x80808080u;
-    const __half2 bias = u32_as_h2(0x64806480u);         // 1152
-    lo = h2_as_u32(__hsub2(u32_as_h2(__byte_perm(u, 0x64646464u, 0x4140)), bias));
-    hi = h2_as_u32(__hsub2(u32_as_h2(__byte_perm(u, 0x64646464u, 0x4342)), bias));
-}
 __device__ __forceinline__ float ex2(float x) {
     float y;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
@@ -60,6 +59,26 @@ __device__ __forceinline__ uint32_t movm(uint32_t x) {            // 8 x 8 fp16 
     uint32_t y;
     asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
     return y;
+}
+__device__ __forceinline__ void mma_s8(int (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1, const int (&c)[4]) {
+    asm("mma.sync.aligned.m16n8k32.row.col.s32.s8.s8.s32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%11,%12,%13};"
+        : "=r"(d[0]), "=r"(d[1]), "=r"(d[2]), "=r"(d[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "r"(c[0]), "r"(c[1]), "r"(c[2]), "r"(c[3]));
+}
+__device__ __forceinline__ void mma_s8u8(int (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1, const int (&c)[4]) {
+    asm("mma.sync.aligned.m16n8k32.row.col.s32.s8.u8.s32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%11,%12,%13};"
+        : "=r"(d[0]), "=r"(d[1]), "=r"(d[2]), "=r"(d[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "r"(c[0]), "r"(c[1]), "r"(c[2]), "r"(c[3]));
+}
+// Digits' sums as fp32.  A sum starts from the bits of 1.5 2^23, so that its bits
+// are the float 1.5 2^23 + sum (|sum| <= 128 * 128 * 128 < 2^22); two of them:
+// 2^16 hi + 2^8 mid + lo, the first step exact.
+constexpr int kSumBits = 0x4b400000;
+__device__ __forceinline__ uint64_t join_f2(const int* hi, const int* mid, const int* lo) {
+    const float b = 12582912.f, c = -12582912.f * 65792.f;
+    const uint64_t h = pack_f2(__int_as_float(hi[0]), __int_as_float(hi[1])), m = pack_f2(__int_as_float(mid[0]), __int_as_float(mid[1]));
+    const uint64_t l = add_f2(pack_f2(__int_as_float(lo[0]), __int_as_float(lo[1])), pack_f2(-b, -b));
+    return add_f2(fma_f2(m, pack_f2(256.f, 256.f), fma_f2(h, pack_f2(65536.f, 65536.f), pack_f2(c, c))), l);
 }
 // Returns when this warp's loads behind x have arrived: what they read may be overwritten.
 __device__ __forceinline__ void arrived(uint32_t x) {
@@ -156,7 +175,6 @@ __device__ __forceinline__ AttnSpan attn_span(const KvSeq& s, const KvBatchView&
 // workspace: the block that counts last on a unit adds its parts in order.
 template <int D, int RN>
 __global__ void __launch_bounds__(kAttnThreads, RN == 1 ? 3 : 2) kv_attention_kernel(const __grid_constant__ KvAttnArgs a) {
-    constexpr int kHalfPage = kKvPage * D;               // bytes of a page's K (or V) of one head
     constexpr int kChunk = kKvPage * 64;                 // what a bulk copy brings: 64 dimensions of a page's K or V
     constexpr int kPanels = D / 64, kRows = 8 * RN, kPart = D + 4;
     extern __shared__ __align__(128) unsigned char sm[];
@@ -259,23 +277,45 @@ __global__ void __launch_bounds__(kAttnThreads, RN == 1 ? 3 : 2) kv_attention_ke
                 asm volatile("prefetch.global.L2 [%0];\n\tprefetch.global.L2 [%1];" ::"l"(k), "l"(v));
             }
         }
-        // Q as B fragments: panel p, step q: dimensions 64 p + 16 t + 4 q .. + 3 of query row 8 r + g
-        uint32_t qf[RN][kPanels][4][2];
+        // Q's digits (lowest first) as B fragments: step q of panel p: dimensions 64 p + 16 t + 8 q .. + 7 of query
+        // row 8 r + g; xq: 2^(e - 22) scale log2(e) of rows 8 r + 2 t + e, where the largest element is below 2^e
+        uint32_t qd[RN][3][kPanels][4];
+        float xq[RN][2];
 #pragma unroll
         for (int r = 0; r < RN; ++r) {
             const int row = row0 + 8 * r + g;
             const uint16_t* q = a.Q + (int64_t)(s.q0 + row / a.G) * a.ldQ + (int64_t)(h * a.G + row % a.G) * D + 16 * t;
+            uint4 u[kPanels][2];
+            __half2 am = __half2half2(__ushort_as_half(0));
 #pragma unroll
-            for (int p = 0; p < kPanels; ++p) {
-                const uint4 u = ldcg_128_if(q + 64 * p, row < rows), v = ldcg_128_if(q + 64 * p + 8, row < rows);
-                qf[r][p][0][0] = u.x;
-                qf[r][p][0][1] = u.y;
-                qf[r][p][1][0] = u.z;
-                qf[r][p][1][1] = u.w;
-                qf[r][p][2][0] = v.x;
-                qf[r][p][2][1] = v.y;
-                qf[r][p][3][0] = v.z;
-                qf[r][p][3][1] = v.w;
+            for (int i = 0; i < 2 * kPanels; ++i) u[i >> 1][i & 1] = ldcg_128_if(q + 64 * (i >> 1) + 8 * (i & 1), row < rows);
+#pragma unroll
+            for (int i = 0; i < 2 * kPanels; ++i) amax8(u[i >> 1][i & 1], am);
+            am = __hmax2_nan(am, __shfl_xor_sync(~0u, am, 1));
+            am = __hmax2_nan(am, __shfl_xor_sync(~0u, am, 2));
+            const float amax = amax_float(am);
+            const int e = min(max((int)(__float_as_uint(amax) >> 23), 100), 143) - 126;
+            const float up = __int_as_float((22 - e + 127) << 23);
+            const float mine = amax <= 65504.f ? __int_as_float((e - 22 + 127) << 23) * a.scale_log2 : __int_as_float(0x7fffffff);
+#pragma unroll
+            for (int e2 = 0; e2 < 2; ++e2) xq[r][e2] = __shfl_sync(~0u, mine, (2 * t + e2) * 4);
+#pragma unroll
+            for (int i = 0; i < 4 * kPanels; ++i) {                  // four elements: two words of u
+                const uint4& w4 = u[i >> 2][(i >> 1) & 1];
+                const uint32_t w0 = i & 1 ? w4.z : w4.x, w1 = i & 1 ? w4.w : w4.y;
+                const float2 f0 = __half22float2(u32_as_h2(w0)), f1 = __half22float2(u32_as_h2(w1));
+                const float f[4] = {f0.x, f0.y, f1.x, f1.y};
+                uint32_t d[3][4];
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const int v = __float_as_int(fmaf(f[j], up, 12582912.f)) - kSumBits, v1 = (v + 128) >> 8;
+                    d[0][j] = v;
+                    d[1][j] = v1;
+                    d[2][j] = (v1 + 128) >> 8;
+                }
+#pragma unroll
+                for (int k = 0; k < 3; ++k)
+                    qd[r][k][i >> 2][i & 3] = __byte_perm(__byte_perm(d[k][0], d[k][1], 0x0040), __byte_perm(d[k][2], d[k][3], 0x0040), 0x5410);
             }
         }
         AttnState<D, RN> st;
@@ -329,65 +369,139 @@ __global__ void __launch_bounds__(kAttnThreads, RN == 1 ? 3 : 2) kv_attention_ke
                     continue;
                 }
                 const int p = p0 + k * kAttnWarps;
-                float x[RN][4][4];
-#pragma unroll
-                for (int r = 0; r < RN; ++r)
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) x[r][i][0] = x[r][i][1] = x[r][i][2] = x[r][i][3] = 0.f;
-#pragma unroll
-                for (int pn = 0; pn < kPanels; ++pn) {
-                    const int slot = (f0 + pn) % kAttnRing;
+                const int sums0[4] = {kSumBits, kSumBits, kSumBits, kSumBits};
+                const float ksc = __shfl_sync(~0u, ks, k), lv = __shfl_sync(~0u, lvs, k), iv = __shfl_sync(~0u, ivs, k);
+                auto wait = [&](int f) {                             // chunk f's slot of the ring
+                    const int slot = f % kAttnRing;
                     if (ok) ok = mbar_wait(wbar + slot, (phases >> slot) & 1, a.status);
                     phases ^= 1u << slot;
-                    const unsigned char* kp = ring + slot * kChunk + (16 * (g >> 1) + (g & 1)) * 64 + 16 * t;
-                    uint32_t seen_words = 0;
+                    return ring + slot * kChunk;
+                };
+                const unsigned char* kp[kPanels];
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) {                    // rows g and g + 8: tokens 16 (g / 2) + 4 i + g % 2 and + 2
-                        const uint4 u = *reinterpret_cast<const uint4*>(kp + 4 * i * 64);
-                        const uint4 v = *reinterpret_cast<const uint4*>(kp + (4 * i + 2) * 64);
-                        const uint32_t uu[4] = {u.x, u.y, u.z, u.w}, vv[4] = {v.x, v.y, v.z, v.w};
+                for (int pn = 0; pn < kPanels; ++pn) kp[pn] = wait(f0 + pn) + (16 * (g >> 1) + (g & 1)) * 64 + 16 * t;
+                float x[RN][4][4];                                   // x + log2 s_V
+                uint32_t seen_words = 0;
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {                        // rows g and g + 8: tokens 16 (g / 2) + 4 i + g % 2 and + 2
+                    int sum[RN][3][4];
+#pragma unroll
+                    for (int pn = 0; pn < kPanels; ++pn) {
+                        const uint4 u = *reinterpret_cast<const uint4*>(kp[pn] + 4 * i * 64);
+                        const uint4 v = *reinterpret_cast<const uint4*>(kp[pn] + (4 * i + 2) * 64);
+                        const uint32_t a0[4] = {u.x, v.x, u.y, v.y}, a1[4] = {u.z, v.z, u.w, v.w};
                         seen_words |= u.w | v.w;
 #pragma unroll
-                        for (int q = 0; q < 4; ++q) {
-                            uint32_t af[4];
-                            cvt_codes(uu[q], af[0], af[2]);
-                            cvt_codes(vv[q], af[1], af[3]);
+                        for (int r = 0; r < RN; ++r)
 #pragma unroll
-                            for (int r = 0; r < RN; ++r) mma_16816(x[r][i], af, qf[r][pn][q]);
-                        }
+                            for (int d = 0; d < 3; ++d) {
+                                if (pn == 0) mma_s8(sum[r][d], a0, qd[r][d][pn][0], qd[r][d][pn][1], sums0);
+                                else mma_s8(sum[r][d], a0, qd[r][d][pn][0], qd[r][d][pn][1], sum[r][d]);
+                                mma_s8(sum[r][d], a1, qd[r][d][pn][2], qd[r][d][pn][3], sum[r][d]);
+                            }
                     }
-                    arrived(seen_words);
-                    fetch(f0 + pn + kAttnRing);
+#pragma unroll
+                    for (int r = 0; r < RN; ++r) {
+                        const uint64_t xs = pack_f2(xq[r][0] * ksc, xq[r][1] * ksc), l2 = pack_f2(lv, lv);
+#pragma unroll
+                        for (int e = 0; e < 4; e += 2)
+                            unpack_f2(fma_f2(join_f2(sum[r][2] + e, sum[r][1] + e, sum[r][0] + e), xs, l2), x[r][i][e], x[r][i][e + 1]);
+                    }
                 }
-                int lim[RN][2];
+                arrived(seen_words);
 #pragma unroll
-                for (int r = 0; r < RN; ++r)
+                for (int pn = 0; pn < kPanels; ++pn) fetch(f0 + pn + kAttnRing);
+                if (least < p * kKvPage + kKvPage - 1) {
 #pragma unroll
-                    for (int e = 0; e < 2; ++e) lim[r][e] = limit[r][e] - p * kKvPage;
-                uint32_t pf[RN][4][2];
-                const float xs = __shfl_sync(~0u, ks, k) * a.scale_log2, lv = __shfl_sync(~0u, lvs, k), iv = __shfl_sync(~0u, ivs, k);
-                softmax_tile<D, RN, 4>(st, x, lim, xs, lv, iv, least < p * kKvPage + kKvPage - 1,
-                                       [&](int i, int u) { return 16 * (g >> 1) + 4 * i + (g & 1) + 2 * u; }, pf);
+                    for (int r = 0; r < RN; ++r)
+#pragma unroll
+                        for (int i = 0; i < 4; ++i)
+#pragma unroll
+                            for (int e = 0; e < 4; ++e)
+                                if (p * kKvPage + 16 * (g >> 1) + 4 * i + (g & 1) + 2 * (e >> 1) > limit[r][e & 1]) x[r][i][e] = -INFINITY;
+                }
+                // weights 2^23 of the page's largest, and their bytes as B fragments (k = tokens, n = query rows)
+                uint32_t pd[RN][3][4];
+                float to[RN][2];                                     // what one of them weighs
+                bool moved = false;
+                float corr[RN][2];
+#pragma unroll
+                for (int r = 0; r < RN; ++r) {
+                    float mx[2], base[2];
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        mx[e] = fmaxf(x[r][0][e], x[r][0][e + 2]);
+#pragma unroll
+                        for (int i = 1; i < 4; ++i) mx[e] = max3(mx[e], x[r][i][e], x[r][i][e + 2]);
+                        mx[e] = fmaxf(mx[e], __shfl_xor_sync(~0u, mx[e], 4));
+                        mx[e] = fmaxf(mx[e], __shfl_xor_sync(~0u, mx[e], 8));
+                        mx[e] = fmaxf(mx[e], __shfl_xor_sync(~0u, mx[e], 16));
+                        base[e] = 23.f - (mx[e] == -INFINITY ? 0.f : mx[e]);   // (nothing visible: weights 2^-inf = 0)
+                        const float m = fmaxf(st.m[r][e], mx[e]), ref = m == -INFINITY ? 0.f : m;
+                        corr[r][e] = ex2(st.m[r][e] - ref);
+                        to[r][e] = ex2(mx[e] - ref + (kWeightExp - 23.f));
+                        moved |= corr[r][e] != 1.f;
+                        st.m[r][e] = m;
+                    }
+                    const uint64_t b2 = pack_f2(base[0], base[1]), one = pack_f2(8388608.f, 8388608.f);
+                    uint64_t sum = 0;
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        uint32_t w[4];
+#pragma unroll
+                        for (int e = 0; e < 4; e += 2) {
+                            float w0, w1;
+                            unpack_f2(add_f2(pack_f2(x[r][i][e], x[r][i][e + 1]), b2), w0, w1);
+                            const uint64_t w2 = pack_f2(ex2(w0), ex2(w1));
+                            sum = add_f2(sum, w2);
+                            unpack_f2(add_f2(w2, one), w0, w1);      // the integer in the mantissa's low bits
+                            w[e] = __float_as_uint(w0);
+                            w[e + 1] = __float_as_uint(w1);
+                        }
+                        // digit k of tokens g, g + 8 of row 2 t, then of row 2 t + 1
+                        const uint32_t p0 = __byte_perm(w[0], w[2], 0x5140), p1 = __byte_perm(w[1], w[3], 0x5140);
+                        const uint32_t h0 = __byte_perm(w[0], w[2], 0x0062), h1 = __byte_perm(w[1], w[3], 0x0062);
+                        pd[r][0][i] = __byte_perm(movm(__byte_perm(p0, p1, 0x5410)), 0, 0x3120);
+                        pd[r][1][i] = __byte_perm(movm(__byte_perm(p0, p1, 0x7632)), 0, 0x3120);
+                        pd[r][2][i] = __byte_perm(movm(__byte_perm(h0, h1, 0x5410)), 0, 0x3120);
+                    }
+                    float l[2];
+                    unpack_f2(sum, l[0], l[1]);
+#pragma unroll
+                    for (int e = 0; e < 2; ++e)                      // tokens that are not seen take nothing from the page's scale (which may be NaN)
+                        st.l[r][e] = st.l[r][e] * corr[r][e] + (l[e] == 0.f ? 0.f : l[e] * to[r][e] * iv);
+                }
+                if (__any_sync(~0u, moved)) {
+#pragma unroll
+                    for (int r = 0; r < RN; ++r)
+#pragma unroll
+                        for (int d = 0; d < D / 16; ++d)
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) st.o[r][d][e] *= corr[r][e & 1];
+                }
 #pragma unroll
                 for (int pn = 0; pn < kPanels; ++pn) {
-                    const int slot = (f0 + kPanels + pn) % kAttnRing;
-                    if (ok) ok = mbar_wait(wbar + slot, (phases >> slot) & 1, a.status);
-                    phases ^= 1u << slot;
-                    const unsigned char* vp = ring + slot * kChunk + g * kKvPage + 16 * t;
-                    uint32_t seen_words = 0;
+                    const unsigned char* vp = wait(f0 + kPanels + pn) + g * kKvPage + 16 * t;
+                    seen_words = 0;
 #pragma unroll
                     for (int d = 0; d < 4; ++d) {
                         const uint4 u = *reinterpret_cast<const uint4*>(vp + 16 * d * kKvPage);
                         const uint4 v = *reinterpret_cast<const uint4*>(vp + (16 * d + 8) * kKvPage);
-                        const uint32_t uu[4] = {u.x, u.y, u.z, u.w}, vv[4] = {v.x, v.y, v.z, v.w};
+                        const uint32_t a0[4] = {u.x, v.x, u.y, v.y}, a1[4] = {u.z, v.z, u.w, v.w};
                         seen_words |= u.w | v.w;
 #pragma unroll
-                        for (int q = 0; q < 4; ++q) {
-                            uint32_t af[4];
-                            cvt_codes(uu[q], af[0], af[2]);
-                            cvt_codes(vv[q], af[1], af[3]);
+                        for (int r = 0; r < RN; ++r) {
+                            int sum[3][4];
 #pragma unroll
-                            for (int r = 0; r < RN; ++r) mma_16816(st.o[r][4 * pn + d], af, pf[r][q]);
+                            for (int j = 0; j < 3; ++j) {
+                                mma_s8u8(sum[j], a0, pd[r][j][0], pd[r][j][1], sums0);
+                                mma_s8u8(sum[j], a1, pd[r][j][2], pd[r][j][3], sum[j]);
+                            }
+                            float* o = st.o[r][4 * pn + d];
+                            const uint64_t to2 = pack_f2(to[r][0], to[r][1]);
+#pragma unroll
+                            for (int e = 0; e < 4; e += 2)
+                                unpack_f2(fma_f2(join_f2(sum[2] + e, sum[1] + e, sum[0] + e), to2, pack_f2(o[e], o[e + 1])), o[e], o[e + 1]);
                         }
                     }
                     arrived(seen_words);
@@ -408,6 +522,25 @@ __global__ void __launch_bounds__(kAttnThreads, RN == 1 ? 3 : 2) kv_attention_ke
                 const int64_t from = tail + (int64_t)(warp * 16 + r) * D + 8 * c;
                 asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(kb + to), "l"(a.c.k_tail + from), "r"(n) : "memory");
                 asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(vb + to), "l"(a.c.v_tail + from), "r"(n) : "memory");
+            }
+            // Q as fp16 B fragments: panel p, step q: dimensions 64 p + 16 t + 4 q .. + 3 of query row 8 r + g
+            uint32_t qf[RN][kPanels][4][2];
+    #pragma unroll
+            for (int r = 0; r < RN; ++r) {
+                const int row = row0 + 8 * r + g;
+                const uint16_t* q = a.Q + (int64_t)(s.q0 + row / a.G) * a.ldQ + (int64_t)(h * a.G + row % a.G) * D + 16 * t;
+    #pragma unroll
+                for (int p = 0; p < kPanels; ++p) {
+                    const uint4 u = ldcg_128_if(q + 64 * p, row < rows), v = ldcg_128_if(q + 64 * p + 8, row < rows);
+                    qf[r][p][0][0] = u.x;
+                    qf[r][p][0][1] = u.y;
+                    qf[r][p][1][0] = u.z;
+                    qf[r][p][1][1] = u.w;
+                    qf[r][p][2][0] = v.x;
+                    qf[r][p][2][1] = v.y;
+                    qf[r][p][3][0] = v.z;
+                    qf[r][p][3][1] = v.w;
+                }
             }
             asm volatile("cp.async.wait_all;" ::: "memory");
             __syncwarp();
