@@ -28,6 +28,8 @@ constexpr int kAttnWarps = 4;
 constexpr int kAttnThreads = kAttnWarps * 32;
 constexpr int kAttnRing = 4;             // chunks of 4 KB in flight per warp
 constexpr int kAttnParts = 128;          // blocks that share one unit, at most (and the two at its ends)
+constexpr int kAttnUnitCost = 6;         // what a unit costs beyond its pages, in pages
+constexpr int kAttnLeastShare = kAttnUnitCost + 2 * kAttnWarps;
 constexpr float kWeightExp = 8.f;
 
 struct KvAttnArgs {
@@ -157,6 +159,7 @@ __device__ __forceinline__ void softmax_tile(AttnState<D, RN>& st, float (&x)[RN
 // head's group, i G + gq) of one sequence and kv head, a page at a time.
 struct AttnSpan {
     int pages, tiles;                                    // of a sequence: pages (1 at least), tiles of rows
+    __device__ long long all(int heads) const { return (long long)(pages + kAttnUnitCost) * tiles * heads; }
 };
 template <int RN>
 __device__ __forceinline__ AttnSpan attn_span(const KvSeq& s, const KvBatchView& b, int G) {
@@ -166,8 +169,10 @@ __device__ __forceinline__ AttnSpan attn_span(const KvSeq& s, const KvBatchView&
 
 // The pages of all units, in a row, are cut into equal shares, one for each
 // block: sequences of any lengths keep every SM busy to the end (a block for
-// each sequence and head left half of the GPU idle behind the longest).  A block
-// takes its share unit by unit; its warps take the pages in turn, each with a
+// each sequence and head left half of the GPU idle behind the longest).  A unit
+// starts with kAttnUnitCost empty pages, for its queries, its tail and its results
+// (without them the shares of the shortest sequences, ten units each, took twice
+// as long as the others).  A block takes its share unit by unit; its warps take the pages in turn, each with a
 // ring of K and V half-pages filled by bulk copies; lane (g, t) feeds the MMA 16
 // consecutive bytes of a row at a time (k in the order 16 t + 4 step, the same in
 // both operands).  The tokens of an incomplete last page are split among the
@@ -200,8 +205,8 @@ __global__ void __launch_bounds__(kAttnThreads, RN == 1 ? 3 : 2) kv_attention_ke
         const KvSeq s = kv_sequence(a.b, b);
         if (!s.ok) record_status(a.status, GLOWQ_ERR_INDEX);
         const AttnSpan w = attn_span<RN>(s, a.b, a.G);
-        mine += (long long)w.pages * w.tiles * a.c.kv_heads;
-        if (w.tiles > 0) most = max(most, w.pages);
+        mine += w.all(a.c.kv_heads);
+        if (w.tiles > 0) most = max(most, w.pages + kAttnUnitCost);
     }
     long long upto = mine;                               // inclusive sum over the threads
     for (int o = 1; o < 32; o <<= 1) {
@@ -221,8 +226,8 @@ __global__ void __launch_bounds__(kAttnThreads, RN == 1 ? 3 : 2) kv_attention_ke
         total += wsum[w];
         most = max(most, wmax[w]);
     }
-    // a page for each warp at least; a unit in kAttnParts shares at most
-    const long long per = max(max((total + gridDim.x - 1) / gridDim.x, (long long)kAttnWarps), (long long)(most + kAttnParts - 1) / kAttnParts);
+    // two pages for each warp at least; a unit in kAttnParts shares at most
+    const long long per = max(max((total + gridDim.x - 1) / gridDim.x, (long long)kAttnLeastShare), (long long)(most + kAttnParts - 1) / kAttnParts);
     long long lo = blockIdx.x * per;
     const long long hi = min(total, lo + per);
     if (lo >= hi) return;
@@ -230,8 +235,7 @@ __global__ void __launch_bounds__(kAttnThreads, RN == 1 ? 3 : 2) kv_attention_ke
         long long off = lo - (upto - mine);
         int b = b0;
         for (; b < b1; ++b) {
-            const AttnSpan w = attn_span<RN>(kv_sequence(a.b, b), a.b, a.G);
-            const long long n = (long long)w.pages * w.tiles * a.c.kv_heads;
+            const long long n = attn_span<RN>(kv_sequence(a.b, b), a.b, a.G).all(a.c.kv_heads);
             if (off < n) break;
             off -= n;
         }
@@ -249,21 +253,27 @@ __global__ void __launch_bounds__(kAttnThreads, RN == 1 ? 3 : 2) kv_attention_ke
     while (lo < hi) {
         const KvSeq s = kv_sequence(a.b, b);
         const AttnSpan w = attn_span<RN>(s, a.b, a.G);
-        if (off >= (long long)w.pages * w.tiles * a.c.kv_heads) {
+        if (off >= w.all(a.c.kv_heads)) {
             off = 0;
             ++b;
             continue;
         }
-        const int unit = (int)(off / w.pages), pa = (int)(off - (long long)unit * w.pages);
+        const int unit = (int)(off / (w.pages + kAttnUnitCost)), at = (int)(off - (long long)unit * (w.pages + kAttnUnitCost));
         const int h = unit % a.c.kv_heads, row0 = unit / a.c.kv_heads * kRows, rows = s.nq * a.G;
-        const int take = (int)min(hi - lo, (long long)(w.pages - pa));
+        const int take = (int)min(hi - lo, (long long)(w.pages + kAttnUnitCost - at));
+        const int pa = max(0, at - kAttnUnitCost), pe = at + take - kAttnUnitCost;   // the share's pages of this unit
+        if (pe <= pa) {
+            lo += take;
+            off += take;
+            continue;
+        }
         // a length that the table or the tails cannot hold: nothing is visible, and the rows are zero
         const bool tailed = s.len % kKvPage != 0;
         const bool bad = s.len > (int64_t)a.b.max_pages * kKvPage || (tailed && (s.slot < 0 || s.slot >= a.c.slots));
         if (bad && tid == 0) record_status(a.status, GLOWQ_ERR_INDEX);
         const int last_tok = min(row0 + kRows - 1, rows - 1) / a.G;  // the tile's last new token
         const int seen = bad ? 0 : max(0, s.start + last_tok + 1);   // tokens that the tile sees
-        const int pb = min((seen + kKvPage - 1) / kKvPage, pa + take);
+        const int pb = min((seen + kKvPage - 1) / kKvPage, pe);
         const int full = s.len / kKvPage, pc = min(pb, full);        // pages in codes: [pa, pc); a tail page may follow
         const int ntok = s.len - full * kKvPage;                     // tokens of the tail
         const int64_t tail = ((int64_t)s.slot * a.c.kv_heads + h) * kKvPage * D;
@@ -645,7 +655,7 @@ __global__ void __launch_bounds__(kAttnThreads, RN == 1 ? 3 : 2) kv_attention_ke
             }
         }
         __syncthreads();
-        const bool whole = pa == 0 && take == w.pages;
+        const bool whole = pa == 0 && pe == w.pages;
         auto store = [&](int r, int c, float l, const float4& o) {
             const int row = row0 + r;
             if (row >= rows) return;
@@ -680,7 +690,7 @@ __global__ void __launch_bounds__(kAttnThreads, RN == 1 ? 3 : 2) kv_attention_ke
             }
         }
         if (!whole) {
-            const long long u0 = lo - pa;                            // the unit's first page in the row of all
+            const long long u0 = lo - at + kAttnUnitCost;                // the unit's first page in the row of all
             const int first = (int)(u0 / per), parts = (int)((u0 + w.pages - 1) / per) - first + 1;
             __threadfence();
             __syncthreads();
@@ -715,16 +725,47 @@ __global__ void __launch_bounds__(kAttnThreads, RN == 1 ? 3 : 2) kv_attention_ke
                     if (lane == 0) sml[r] = l;
                 }
                 __syncthreads();
-                for (int i = tid; i < kRows * D / 4; i += kAttnThreads) {
-                    const int r = i / (D / 4), c = i % (D / 4);
-                    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 8
-                    for (int k = 0; k < parts; ++k) {
-                        const float4 v = __ldcg(reinterpret_cast<const float4*>(of(k) + r * kPart + 4 * c));
-                        const float f = all[2 * (k * kRows + r)];
-                        o = make_float4(fmaf(f, v.x, o.x), fmaf(f, v.y, o.y), fmaf(f, v.z, o.z), fmaf(f, v.w, o.w));
+                // a warp adds every fourth part, eight rows at a time, two parts' loads in flight; then the warps' sums
+                constexpr int kLoads = D / 16;                       // 16-byte words of a lane: 8 rows of D / 4 words in 32 lanes
+                float* sums = all + 2 * (kAttnParts + 2) * kRows;    // [warp][rows][D], behind the factors
+#pragma unroll 1
+                for (int r0 = 0; r0 < kRows; r0 += 8) {
+                    float4 o[kLoads];
+#pragma unroll
+                    for (int i = 0; i < kLoads; ++i) o[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 1
+                    for (int k = warp; k < parts; k += 2 * kAttnWarps) {
+                        uint4 v[2][kLoads];
+#pragma unroll
+                        for (int u = 0; u < 2; ++u)
+#pragma unroll
+                            for (int i = 0; i < kLoads; ++i) {
+                                const int word = lane + 32 * i, kk = k + u * kAttnWarps;
+                                v[u][i] = ldcg_128_if(of(kk) + (r0 + word / (D / 4)) * kPart + word % (D / 4) * 4, kk < parts);
+                            }
+#pragma unroll
+                        for (int u = 0; u < 2; ++u)
+#pragma unroll
+                            for (int i = 0; i < kLoads; ++i) {
+                                const int kk = min(k + u * kAttnWarps, parts - 1);
+                                const float f = all[2 * (kk * kRows + r0 + (lane + 32 * i) / (D / 4))];
+                                o[i] = make_float4(fmaf(f, __uint_as_float(v[u][i].x), o[i].x), fmaf(f, __uint_as_float(v[u][i].y), o[i].y),
+                                                   fmaf(f, __uint_as_float(v[u][i].z), o[i].z), fmaf(f, __uint_as_float(v[u][i].w), o[i].w));
+                            }
                     }
-                    store(r, c, sml[r], o);
+#pragma unroll
+                    for (int i = 0; i < kLoads; ++i)
+                        reinterpret_cast<float4*>(sums)[(warp * kRows + r0) * (D / 4) + lane + 32 * i] = o[i];
+                }
+                __syncthreads();
+                for (int i = tid; i < kRows * D / 4; i += kAttnThreads) {
+                    float4 o = reinterpret_cast<const float4*>(sums)[i];
+#pragma unroll
+                    for (int k = 1; k < kAttnWarps; ++k) {
+                        const float4 v = reinterpret_cast<const float4*>(sums)[k * kRows * (D / 4) + i];
+                        o = make_float4(o.x + v.x, o.y + v.y, o.z + v.z, o.w + v.w);
+                    }
+                    store(i / (D / 4), i % (D / 4), sml[i / (D / 4)], o);
                 }
             }
         }
@@ -745,9 +786,9 @@ KvAttnPlan plan_kv_attention(const KvBatchView& b, int G, int kv_heads, int head
     const int64_t rows = (int64_t)b.max_new * G;
     p.tc = rows >= 64;
     p.rows = attn_rows(rows);
-    // resident blocks, or one for every kAttnWarps pages when there cannot be more
-    const int64_t pages = (int64_t)b.n_seq * (b.max_pages > 0 ? b.max_pages : 1) * kv_heads * ((rows + p.rows - 1) / p.rows);
-    const int64_t want = (pages + kAttnWarps - 1) / kAttnWarps;
+    // the blocks that are resident, or as many as there can be shares
+    const int64_t units = (int64_t)b.n_seq * kv_heads * ((rows + p.rows - 1) / p.rows);
+    const int64_t want = (units * ((b.max_pages > 0 ? b.max_pages : 1) + kAttnUnitCost) + kAttnLeastShare - 1) / kAttnLeastShare;
     p.blocks = num_sms * (p.rows == 8 ? 3 : 2);
     if (p.blocks > want) p.blocks = (int)want;
     p.partial_bytes = p.tc ? 0 : (size_t)p.blocks * 2 * p.rows * (head_dim + 4) * sizeof(float);
