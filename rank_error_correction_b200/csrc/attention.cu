@@ -26,7 +26,7 @@ namespace glowq {
 
 constexpr int kAttnWarps = 4;
 constexpr int kAttnThreads = kAttnWarps * 32;
-constexpr int kAttnRing = 4;             // chunks of 4 KB in flight per warp
+constexpr int kAttnRing = 4;             // chunks of 4 KB of a warp's ring
 constexpr int kAttnParts = 128;          // blocks that share one unit, at most (and the two at its ends)
 constexpr int kAttnUnitCost = 6;         // what a unit costs beyond its pages, in pages
 constexpr int kAttnLeastShare = kAttnUnitCost + 2 * kAttnWarps;
@@ -39,7 +39,7 @@ struct KvAttnArgs {
     uint16_t* Y;
     int64_t ldQ, ldY;
     float scale_log2;        // scale log2(e)
-    int G;
+    int G, sms;
     float* partial;          // [block][2][8 RN][D + 4]
     unsigned int* tickets;   // [block], zero between calls
     unsigned int* status;
@@ -228,6 +228,10 @@ __global__ void __launch_bounds__(kAttnThreads, RN == 1 ? 3 : 2) kv_attention_ke
     }
     // two pages for each warp at least; a unit in kAttnParts shares at most
     const long long per = max(max((total + gridDim.x - 1) / gridDim.x, (long long)kAttnLeastShare), (long long)(most + kAttnParts - 1) / kAttnParts);
+    // Chunks in flight: with three blocks on an SM two of a warp's are 96 KB on the SM
+    // and keep memory busy; four only queue up (100,000 tokens: 125 us against 115).
+    // Fewer blocks need the four (one sequence: 14.3 us against 16.4).
+    const int depth = total > 2 * a.sms * per ? 2 : kAttnRing;
     long long lo = blockIdx.x * per;
     const long long hi = min(total, lo + per);
     if (lo >= hi) return;
@@ -371,11 +375,11 @@ __global__ void __launch_bounds__(kAttnThreads, RN == 1 ? 3 : 2) kv_attention_ke
                     bulk_g2s(smem_u32(ring + (f % kAttnRing) * kChunk), (c < kPanels ? a.c.k_codes : a.c.v_codes) + at, kChunk, bar);
                 }
             };
-            for (int f = 0; f < kAttnRing; ++f) fetch(f);
+            for (int f = 0; f < depth; ++f) fetch(f);
             for (int k = 0; k < n; ++k) {
                 const int f0 = 2 * kPanels * k;
                 if (__shfl_sync(~0u, id, k) < 0) {                   // not there: skipped, nothing was fetched
-                    for (int f = 0; f < 2 * kPanels; ++f) fetch(f0 + f + kAttnRing);
+                    for (int f = 0; f < 2 * kPanels; ++f) fetch(f0 + f + depth);
                     continue;
                 }
                 const int p = p0 + k * kAttnWarps;
@@ -420,7 +424,7 @@ __global__ void __launch_bounds__(kAttnThreads, RN == 1 ? 3 : 2) kv_attention_ke
                 }
                 arrived(seen_words);
 #pragma unroll
-                for (int pn = 0; pn < kPanels; ++pn) fetch(f0 + pn + kAttnRing);
+                for (int pn = 0; pn < kPanels; ++pn) fetch(f0 + pn + depth);
                 if (least < p * kKvPage + kKvPage - 1) {
 #pragma unroll
                     for (int r = 0; r < RN; ++r)
@@ -515,7 +519,7 @@ __global__ void __launch_bounds__(kAttnThreads, RN == 1 ? 3 : 2) kv_attention_ke
                         }
                     }
                     arrived(seen_words);
-                    fetch(f0 + kPanels + pn + kAttnRing);
+                    fetch(f0 + kPanels + pn + depth);
                 }
             }
         }
@@ -789,6 +793,7 @@ KvAttnPlan plan_kv_attention(const KvBatchView& b, int G, int kv_heads, int head
     // the blocks that are resident, or as many as there can be shares
     const int64_t units = (int64_t)b.n_seq * kv_heads * ((rows + p.rows - 1) / p.rows);
     const int64_t want = (units * ((b.max_pages > 0 ? b.max_pages : 1) + kAttnUnitCost) + kAttnLeastShare - 1) / kAttnLeastShare;
+    p.sms = num_sms;
     p.blocks = num_sms * (p.rows == 8 ? 3 : 2);
     if (p.blocks > want) p.blocks = (int)want;
     p.partial_bytes = p.tc ? 0 : (size_t)p.blocks * 2 * p.rows * (head_dim + 4) * sizeof(float);
@@ -808,7 +813,7 @@ cudaError_t launch_kv_attention(const KvCacheView& c, const KvBatchView& b, cons
                                 float scale, uint16_t* Y, int64_t ldY, unsigned int* tickets, float* partial,
                                 const KvAttnPlan& p, cudaStream_t st) {
     if (p.tc) return launch_kv_attention_tc(c, b, Q, ldQ, q_heads, scale, Y, ldY, st);
-    KvAttnArgs a = {c, b, Q, Y, ldQ, ldY, scale * 1.44269504088896340736f, q_heads / c.kv_heads, partial, tickets,
+    KvAttnArgs a = {c, b, Q, Y, ldQ, ldY, scale * 1.44269504088896340736f, q_heads / c.kv_heads, p.sms, partial, tickets,
                     device_status_ptr()};
     if (c.head_dim == 64) return p.rows == 8 ? launch_attn<64, 1>(a, p.blocks, st) : launch_attn<64, 2>(a, p.blocks, st);
     return p.rows == 8 ? launch_attn<128, 1>(a, p.blocks, st) : launch_attn<128, 2>(a, p.blocks, st);

@@ -59,7 +59,7 @@ cudaError_t launch_kv_read(const KvCacheView& c, const KvBatchView& b, const int
 struct KvAttnPlan {
     bool tc;             // many rows: attention_tc.cu
     int rows;            // query rows of a block at a time: 8 or 16
-    int blocks;
+    int blocks, sms;
     size_t partial_bytes;
 };
 KvAttnPlan plan_kv_attention(const KvBatchView& b, int G, int kv_heads, int head_dim, int num_sms);
