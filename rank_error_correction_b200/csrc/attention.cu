@@ -787,8 +787,16 @@ static size_t attn_smem(int rows) { return (size_t)kAttnWarps * 16384 + kAttnWar
 
 KvAttnPlan plan_kv_attention(const KvBatchView& b, int G, int kv_heads, int head_dim, int num_sms) {
     KvAttnPlan p = {};
-    const int64_t rows = (int64_t)b.max_new * G;
-    p.tc = rows >= 64;
+    const int64_t rows = (int64_t)b.max_new * G, heads = (int64_t)b.n_seq * kv_heads, P = b.max_pages;
+    // The kernel of attention_tc.cu takes 256 rows to a block and 1.35 us a page for
+    // each wave of blocks, whatever rows and SMs stay empty; here 16 rows and a page
+    // take 3.6 ns of the whole GPU, and 22 us more go to the start and the joins:
+    //   1350 waves P <= 3.6 heads (rows / 16) P + 22000  (ns; P pages at most).
+    // 8 kv heads, 64 rows each, 32768 tokens: 84 us here, 692 there, and for eight such
+    // sequences 473 and 702; 128 rows of eight sequences: 918 here, 598 there; after
+    // 2048 tokens 107 and 55.  Below 64 rows this kernel is faster but for a few us.
+    const int64_t waves = (kv_tc_blocks(b, G, kv_heads) + num_sms - 1) / num_sms;
+    p.tc = rows >= 64 && (375 * waves - heads * ((rows + 15) / 16)) * P <= 6100;
     p.rows = attn_rows(rows);
     // the blocks that are resident, or as many as there can be shares
     const int64_t units = (int64_t)b.n_seq * kv_heads * ((rows + p.rows - 1) / p.rows);

@@ -172,6 +172,58 @@ def test_longer_caches(Hq, Hkv, D, cached, new):
     assert np.array_equal(first, sv.check_attention(b, Q, qr, new))          # the same bits again
 
 
+@pytest.mark.parametrize("Hq,Hkv,D,cached,new", [
+    (8, 1, 128, [1500], [16]), (8, 1, 64, [2000, 0, 900], [9, 30, 70]), (4, 2, 128, [4000, 3000], [33, 1]),
+])
+def test_many_rows_over_long_tables(Hq, Hkv, D, cached, new):
+    """Enough rows for matrix tiles, but too few blocks of them: pages are shared instead."""
+    test_longer_caches(Hq, Hkv, D, cached, new)
+
+
+def test_hundreds_of_uneven_sequences():
+    """More sequences than a block has threads, many of a page or less, some without new tokens."""
+    g = np.random.default_rng(11)
+    n = 300
+    sv = Server(n, 6, 2, 64, 6, seed=11)
+    sv.step([int(x) for x in g.choice([0, 1, 40, 63, 64, 65, 128, 200, 320], n)])
+    for new in ([1] * n, [int(x) for x in g.integers(0, 3, n)], [int(i == 299) for i in range(n)]):
+        b, Q, qr = sv.step(new)
+        first = sv.check_attention(b, Q, qr, new)
+        assert np.array_equal(first, sv.check_attention(b, Q, qr, new))
+
+
+def test_one_sequence_in_the_most_parts():
+    sv = Server(1, 2, 1, 64, 1880, seed=12)
+    sv.step([120000])
+    b, Q, qr = sv.step([1])
+    sv.check_attention(b, Q, qr, [1])
+    b, Q, qr = sv.step([6])
+    sv.check_attention(b, Q, qr, [6])
+
+
+@pytest.mark.parametrize("Hq,Hkv,D,cached,new", [
+    (4, 2, 64, [300], [700]), (4, 2, 128, [300], [700]), (8, 2, 64, [900, 30, 500], [1, 1, 1]),
+    (8, 2, 128, [900, 30, 500], [1, 1, 1]),
+])
+def test_the_same_bits_every_time(Hq, Hkv, D, cached, new):
+    """Many calls, alone and two at once on two streams, each with its own workspace: no result depends on time."""
+    import torch
+    sv = Server(len(new), Hq, Hkv, D, (max(cached) + max(new)) // PAGE + 2, seed=D)
+    sv.step(cached)
+    b, Q, qr = sv.step(new)
+    want = torch.from_numpy(sv.check_attention(b, Q, qr, new)[:, :-8].copy()).cuda()
+    plans = [glowq.KVAttentionPlan(sv.cache, b, Q) for _ in range(2)]
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    for s in streams:
+        s.wait_stream(torch.cuda.current_stream())
+    for _ in range(100):
+        for p, s in zip(plans, streams):
+            p.outputs.record_stream(s)
+            p(stream=s)
+        torch.cuda.synchronize()
+        assert all(torch.equal(p.outputs, want) for p in plans)
+
+
 @pytest.mark.parametrize("D", [64, 128])
 @pytest.mark.parametrize("spread", [64.0, 2000.0])
 def test_scales_far_apart(D, spread):
