@@ -788,15 +788,15 @@ static size_t attn_smem(int rows) { return (size_t)kAttnWarps * 16384 + kAttnWar
 KvAttnPlan plan_kv_attention(const KvBatchView& b, int G, int kv_heads, int head_dim, int num_sms) {
     KvAttnPlan p = {};
     const int64_t rows = (int64_t)b.max_new * G, heads = (int64_t)b.n_seq * kv_heads, P = b.max_pages;
-    // The kernel of attention_tc.cu takes 256 rows to a block and 1.35 us a page for
-    // each wave of blocks, whatever rows and SMs stay empty; here 16 rows and a page
-    // take 3.6 ns of the whole GPU, and 22 us more go to the start and the joins:
-    //   1350 waves P <= 3.6 heads (rows / 16) P + 22000  (ns; P pages at most).
-    // 8 kv heads, 64 rows each, 32768 tokens: 84 us here, 692 there, and for eight such
-    // sequences 473 and 702; 128 rows of eight sequences: 918 here, 598 there; after
-    // 2048 tokens 107 and 55.  Below 64 rows this kernel is faster but for a few us.
-    const int64_t waves = (kv_tc_blocks(b, G, kv_heads) + num_sms - 1) / num_sms;
-    p.tc = rows >= 64 && (375 * waves - heads * ((rows + 15) / 16)) * P <= 6100;
+    // Here 16 rows and a page take 3.6 ns of the whole GPU, beside 30 us for the
+    // start and the joins; attention_tc.cu takes 256 rows to a block, whatever rows
+    // stay empty, and expects its own time.  8 kv heads and 32768 tokens: 64 rows of
+    // one sequence 84 us here, 126 there, 128 rows 139 and 109; of eight sequences 918
+    // and 396; after 2048 tokens 107 and 45.  Below 64 rows this kernel is faster but
+    // for a few us.
+    const KvTcShares tc = kv_tc_shares(b, G, kv_heads, num_sms);
+    p.S = tc.S;
+    p.tc = rows >= 64 && tc.us <= 0.0036 * heads * ((rows + 15) / 16) * P + 30.;
     p.rows = attn_rows(rows);
     // the blocks that are resident, or as many as there can be shares
     const int64_t units = (int64_t)b.n_seq * kv_heads * ((rows + p.rows - 1) / p.rows);
@@ -804,7 +804,7 @@ KvAttnPlan plan_kv_attention(const KvBatchView& b, int G, int kv_heads, int head
     p.sms = num_sms;
     p.blocks = num_sms * (p.rows == 8 ? 3 : 2);
     if (p.blocks > want) p.blocks = (int)want;
-    p.partial_bytes = p.tc ? 0 : (size_t)p.blocks * 2 * p.rows * (head_dim + 4) * sizeof(float);
+    p.partial_bytes = p.tc ? kv_tc_partial_bytes(b, G, kv_heads, p.S, head_dim) : (size_t)p.blocks * 2 * p.rows * (head_dim + 4) * sizeof(float);
     return p;
 }
 
@@ -820,7 +820,7 @@ static cudaError_t launch_attn(const KvAttnArgs& a, int blocks, cudaStream_t st)
 cudaError_t launch_kv_attention(const KvCacheView& c, const KvBatchView& b, const uint16_t* Q, int64_t ldQ, int q_heads,
                                 float scale, uint16_t* Y, int64_t ldY, unsigned int* tickets, float* partial,
                                 const KvAttnPlan& p, cudaStream_t st) {
-    if (p.tc) return launch_kv_attention_tc(c, b, Q, ldQ, q_heads, scale, Y, ldY, st);
+    if (p.tc) return launch_kv_attention_tc(c, b, Q, ldQ, q_heads, scale, Y, ldY, tickets, partial, p.S, st);
     KvAttnArgs a = {c, b, Q, Y, ldQ, ldY, scale * 1.44269504088896340736f, q_heads / c.kv_heads, p.sms, partial, tickets,
                     device_status_ptr()};
     if (c.head_dim == 64) return p.rows == 8 ? launch_attn<64, 1>(a, p.blocks, st) : launch_attn<64, 2>(a, p.blocks, st);

@@ -24,6 +24,7 @@
 namespace glowq {
 
 constexpr int kTcRows = 256, kTcTokens = 128, kTcThreads = 512, kTcMeta = 4;
+constexpr int kTcLeastTiles = 4, kTcMostShares = 16, kTcMostTickets = 16384, kTcMostPairs = 256;
 constexpr float kTcWeightExp = 8.f, kTcSlack = 6.f;
 
 struct KvTcArgs {
@@ -34,6 +35,9 @@ struct KvTcArgs {
     int64_t ldQ, ldY;
     float scale_log2;
     int G, rt;               // query heads per kv head, row tiles of the widest sequence
+    int S;                   // shares of a unit's tokens, at most
+    float* partial;          // [row tile of the batch][kv head][share][D + 2][256 rows]: O by column, m, l
+    unsigned int* tickets;   // [unit of the grid], zero between calls
     unsigned int* status;
 };
 
@@ -49,6 +53,8 @@ struct __align__(8) KvTcShared {
     uint64_t codes[2];                   // the staged codes of K, of V
     KvTcMeta meta[kTcMeta];
     unsigned int tail_max, tail_poison[2];
+    int last;                            // this block joins its unit's shares
+    int pair;                            // its row tile and sequence
     uint32_t tmem;
 };
 
@@ -131,9 +137,8 @@ __global__ void __launch_bounds__(kTcThreads, 1) kv_attention_tc_kernel(const __
     unsigned char* sc = sv + 2 * L::kVBytes;
     KvTcShared* sh = reinterpret_cast<KvTcShared*>(sc + 2 * L::kCodes);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int nbh = a.b.n_seq * a.c.kv_heads;
-    const int tile = a.rt - 1 - (int)(blockIdx.x / nbh);             // the longest rows first
-    const int bh = blockIdx.x % nbh, h = bh % a.c.kv_heads, b = bh / a.c.kv_heads;
+    const int share = blockIdx.x % a.S, unit = blockIdx.x / a.S, h = unit % a.c.kv_heads;
+    int pair = unit / a.c.kv_heads;                                  // (row tile, sequence), the last rows first
     if (threadIdx.x == 0) {
         mbar_init(&sh->q_full, 8);
         for (int i = 0; i < 2; ++i) {
@@ -149,6 +154,28 @@ __global__ void __launch_bounds__(kTcThreads, 1) kv_attention_tc_kernel(const __
         fence_mbar_init();
     }
     pdl_wait();
+    const int pairs = a.rt * a.b.n_seq;
+    if (a.b.n_seq > 1 && pairs <= kTcMostPairs) {
+        // The longest first, whatever the sequences' lengths: the pair of this block's rank (four uneven
+        // chunks: 103 us instead of 126).
+        int* len = reinterpret_cast<int*>(sk);
+        const int i = threadIdx.x;
+        int mine = 0, rank = 0;
+        if (i < pairs) {
+            const KvSeq q = kv_sequence(a.b, i % a.b.n_seq);
+            const int first = (a.rt - 1 - i / a.b.n_seq) * kTcRows, n = q.nq * a.G;
+            mine = first < n ? max(0, q.start + (min(first + kTcRows, n) - 1) / a.G) / kTcTokens + 1 : 0;
+            len[i] = mine;
+        }
+        __syncthreads();
+        if (i < pairs) {
+            for (int k = 0; k < pairs; ++k) rank += len[k] > mine || (len[k] == mine && k < i);
+            if (rank == pair) sh->pair = i;
+        }
+        __syncthreads();
+        pair = sh->pair;
+    }
+    const int tile = a.rt - 1 - pair / a.b.n_seq, b = pair % a.b.n_seq;
     const KvSeq s = kv_sequence(a.b, b);
     const int rows = s.nq * a.G, row0 = tile * kTcRows;
     if (!s.ok && threadIdx.x == 0) record_status(a.status, GLOWQ_ERR_INDEX);
@@ -164,7 +191,14 @@ __global__ void __launch_bounds__(kTcThreads, 1) kv_attention_tc_kernel(const __
         const int seen = bad || first >= rows ? 0 : max(0, s.start + last / a.G + 1);
         nt[t] = (seen + kTcTokens - 1) / kTcTokens;
     }
-    const int nmax = max(nt[0], nt[1]);
+    // this block's share of the token tiles; from here on tiles, pages and positions count from its first
+    int nmax = max(nt[0], nt[1]);
+    const int per = max((nmax + a.S - 1) / a.S, kTcLeastTiles), shares = max(1, (nmax + per - 1) / per);
+    if (share >= shares) return;
+    const int ja = share * per;
+#pragma unroll
+    for (int t = 0; t < 2; ++t) nt[t] = max(0, min(nt[t] - ja, per));
+    nmax = max(nt[0], nt[1]);
     if (warp == 12) tmem_alloc(&sh->tmem, 512);
     tc_fence_before();
     __syncthreads();
@@ -202,8 +236,8 @@ __global__ void __launch_bounds__(kTcThreads, 1) kv_attention_tc_kernel(const __
         fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) mbar_arrive(&sh->q_full);
-        const int limit = there ? s.start + tok : -1;
-        const int least = s.start + (row0 + t * 128) / a.G;          // the tile's first row sees least
+        const int limit = (there ? s.start + tok : -1) - ja * kTcTokens;
+        const int least = s.start + (row0 + t * 128) / a.G - ja * kTcTokens;   // the tile's first row sees least
         float ref = -INFINITY, l = 0.f;
         for (int j = 0; j < nt[t]; ++j) {
             if (ok) ok = mbar_wait(&sh->s_full[t], j & 1, a.status);
@@ -293,48 +327,111 @@ __global__ void __launch_bounds__(kTcThreads, 1) kv_attention_tc_kernel(const __
             if (ok) ok = mbar_wait(&sh->o_done[t], (nt[t] - 1) & 1, a.status);
             tc_fence_after();
         }
-        const float inv = l == 0.f ? 0.f : 1.f / l;                  // a row that sees nothing is zero
-        // (the tile's products are complete, so its queries' buffer takes the outputs; a warp's rows are its own)
-        unsigned char* out = sq + t * L::kQBytes;
-#pragma unroll 1
-        for (int c = 0; c < D / 32; ++c) {
-            uint32_t v[32];
+        // With several shares, each leaves its O, m and l in the workspace (a column's
+        // rows side by side), and the last to count joins them, in the shares' order.
+        bool last = true;
+        const int mrow = t * 128 + r;
+        // (row tiles of the batch: no more than T G / 256 + n, however uneven the sequences)
+        const int64_t tiles_before = (int64_t)s.q0 * a.G / kTcRows + b;
+        float* parts = a.partial + ((tiles_before + tile) * a.c.kv_heads + h) * a.S * (D + 2) * kTcRows + mrow;
+        auto column = [&](int c, uint32_t (&v)[32]) {                // O's columns from 32 c: zero where nothing was seen
             if (nt[t] > 0) {
                 tmem_ld32(to + c * 32, v);
-            }
+            } else {
 #pragma unroll
-            for (int i = 0; i < 32; i += 8) {
-                uint4 y = make_uint4(0, 0, 0, 0);
-                if (nt[t] > 0 && l != 0.f) {
-                    y.x = h2_as_u32(__floats2half2_rn(__uint_as_float(v[i]) * inv, __uint_as_float(v[i + 1]) * inv));
-                    y.y = h2_as_u32(__floats2half2_rn(__uint_as_float(v[i + 2]) * inv, __uint_as_float(v[i + 3]) * inv));
-                    y.z = h2_as_u32(__floats2half2_rn(__uint_as_float(v[i + 4]) * inv, __uint_as_float(v[i + 5]) * inv));
-                    y.w = h2_as_u32(__floats2half2_rn(__uint_as_float(v[i + 6]) * inv, __uint_as_float(v[i + 7]) * inv));
+                for (int i = 0; i < 32; ++i) v[i] = 0u;
+            }
+        };
+        if (shares > 1) {
+            float* part = parts + (int64_t)share * (D + 2) * kTcRows;
+#pragma unroll 1
+            for (int c = 0; c < D / 32; ++c) {
+                uint32_t v[32];
+                column(c, v);
+#pragma unroll
+                for (int i = 0; i < 32; ++i) __stcg(part + (c * 32 + i) * kTcRows, __uint_as_float(v[i]));
+            }
+            __stcg(part + D * kTcRows, ref);
+            __stcg(part + (D + 1) * kTcRows, l);
+            __threadfence();
+            named_barrier_sync(2, 256);
+            if (threadIdx.x == 0) {
+                unsigned int prev;
+                asm volatile("atom.acq_rel.gpu.global.add.u32 %0, [%1], 1;" : "=r"(prev) : "l"(a.tickets + unit) : "memory");
+                sh->last = prev == (unsigned)(shares - 1);
+                if (sh->last) atomicExch(a.tickets + unit, 0u);      // every share has counted: ready for the next call
+            }
+            named_barrier_sync(2, 256);
+            last = sh->last;
+            __threadfence();
+            if (last) {
+                ref = -INFINITY;
+                for (int k = 0; k < shares; ++k) ref = fmaxf(ref, __ldcg(parts + ((int64_t)k * (D + 2) + D) * kTcRows));
+                if (ref == -INFINITY) ref = 0.f;
+                l = 0.f;
+                for (int k = 0; k < shares; ++k) {
+                    const float* p = parts + ((int64_t)k * (D + 2) + D) * kTcRows;
+                    l = fmaf(tc_ex2(__ldcg(p) - ref), __ldcg(p + kTcRows), l);
                 }
-                const int x = c * 4 + (i >> 3);
-                *reinterpret_cast<uint4*>(out + (x >> 3) * 16384 + sw128(r, x & 7)) = y;
             }
         }
-        __syncwarp();
+        if (last) {
+            const float inv = l == 0.f ? 0.f : 1.f / l;                  // a row that sees nothing is zero
+            // (the tile's products are complete, so its queries' buffer takes the outputs; a warp's rows are its own)
+            unsigned char* out = sq + t * L::kQBytes;
 #pragma unroll 1
-        for (int i = 0; i < 32; i += 4 * kAtOnce) {
-            uint4 y[4];
+            for (int c = 0; c < D / 32; ++c) {
+                uint32_t v[32];
+                if (shares == 1) {
+                    column(c, v);
+                } else {
 #pragma unroll
-            for (int k = 0; k < 4; ++k)
-                y[k] = *reinterpret_cast<const uint4*>(mine + sw128((warp & 3) * 32 + i + k * kAtOnce + sub, ch & 7));
+                    for (int i = 0; i < 32; ++i) v[i] = 0u;
+#pragma unroll 1
+                    for (int k = 0; k < shares; ++k) {
+                        const float* p = parts + (int64_t)k * (D + 2) * kTcRows;
+                        const float f = tc_ex2(__ldcg(p + D * kTcRows) - ref);
+                        uint32_t u[32];
 #pragma unroll
-            for (int k = 0; k < 4; ++k) {
-                const int from = i + k * kAtOnce + sub, ft = __shfl_sync(~0u, tok, from), fg = __shfl_sync(~0u, gq, from);
-                if (row0 + t * 128 + (warp & 3) * 32 + from < rows)
-                    *reinterpret_cast<uint4*>(a.Y + (int64_t)(s.q0 + ft) * a.ldY + head + (int64_t)fg * D) = y[k];
+                        for (int i = 0; i < 32; ++i) u[i] = __float_as_uint(__ldcg(p + (c * 32 + i) * kTcRows));
+#pragma unroll
+                        for (int i = 0; i < 32; ++i) v[i] = __float_as_uint(fmaf(f, __uint_as_float(u[i]), __uint_as_float(v[i])));
+                    }
+                }
+#pragma unroll
+                for (int i = 0; i < 32; i += 8) {
+                    uint4 y = make_uint4(0, 0, 0, 0);
+                    if (l != 0.f) {
+                        y.x = h2_as_u32(__floats2half2_rn(__uint_as_float(v[i]) * inv, __uint_as_float(v[i + 1]) * inv));
+                        y.y = h2_as_u32(__floats2half2_rn(__uint_as_float(v[i + 2]) * inv, __uint_as_float(v[i + 3]) * inv));
+                        y.z = h2_as_u32(__floats2half2_rn(__uint_as_float(v[i + 4]) * inv, __uint_as_float(v[i + 5]) * inv));
+                        y.w = h2_as_u32(__floats2half2_rn(__uint_as_float(v[i + 6]) * inv, __uint_as_float(v[i + 7]) * inv));
+                    }
+                    const int x = c * 4 + (i >> 3);
+                    *reinterpret_cast<uint4*>(out + (x >> 3) * 16384 + sw128(r, x & 7)) = y;
+                }
+            }
+            __syncwarp();
+#pragma unroll 1
+            for (int i = 0; i < 32; i += 4 * kAtOnce) {
+                uint4 y[4];
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+                    y[k] = *reinterpret_cast<const uint4*>(mine + sw128((warp & 3) * 32 + i + k * kAtOnce + sub, ch & 7));
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    const int from = i + k * kAtOnce + sub, ft = __shfl_sync(~0u, tok, from), fg = __shfl_sync(~0u, gq, from);
+                    if (row0 + t * 128 + (warp & 3) * 32 + from < rows)
+                        *reinterpret_cast<uint4*>(a.Y + (int64_t)(s.q0 + ft) * a.ldY + head + (int64_t)fg * D) = y[k];
+                }
             }
         }
     } else if (warp < 12) {
         // ---------------- pages to operands (128 threads) ----------------
         const int tid = threadIdx.x - 256;
-        const int full = s.len / kKvPage, ntok = s.len - full * kKvPage;
+        const int full = s.len / kKvPage - 2 * ja, ntok = s.len % kKvPage;
         const int64_t tail = ((int64_t)s.slot * a.c.kv_heads + h) * kKvPage * D;
-        const int* table = a.b.table + (int64_t)b * a.b.max_pages;
+        const int* table = a.b.table + (int64_t)b * a.b.max_pages + 2 * ja;
         constexpr int kPieces = kKvPage * D / 16 / 128;              // 16-byte pieces of a page's K (or V) per thread
         // the table's entry for page p (loaded a tile ahead of its use), and what it
         // says: the page's id, -1 absent (or out of range), -2 the tail
@@ -596,17 +693,39 @@ static cudaError_t launch_tc(const KvTcArgs& a, unsigned grid, cudaStream_t st) 
     return launch_pdl((const void*)kv_attention_tc_kernel<D>, grid, kTcThreads, KvTc<D>::kSmem, st, args);
 }
 
-int64_t kv_tc_blocks(const KvBatchView& b, int G, int kv_heads) {
-    return ((int64_t)b.max_new * G + kTcRows - 1) / kTcRows * b.n_seq * kv_heads;
+// Shares of a unit's tokens: what their number is expected to take, the tables
+// being full, is 2.7 us for a tile of 128 tokens and 6.4 us for the rest of a block,
+// in waves of a block for each SM; with shares 8 us more of a block and 2 us for
+// each part of the join.  (512 rows of one sequence and 8 kv heads after 32768
+// tokens: 635 us whole, 112 us in nine shares; of eight sequences after 2048
+// tokens, where each SM has a block: 61 us whole, 87 us in three.)
+KvTcShares kv_tc_shares(const KvBatchView& b, int G, int kv_heads, int num_sms) {
+    const int64_t rt = ((int64_t)b.max_new * G + kTcRows - 1) / kTcRows, grid = rt * b.n_seq * kv_heads;
+    // units: no more than T G / 256 + n row tiles, however uneven the sequences
+    const int64_t all = ((int64_t)b.T * G / kTcRows + b.n_seq) * kv_heads, units = grid < all ? grid : all;
+    const double tiles = ((int64_t)b.max_pages * kKvPage + kTcTokens - 1) / kTcTokens;
+    KvTcShares best = {1, 0.};
+    for (int S = 1; S <= kTcMostShares; ++S) {
+        if (S > 1 && (tiles < (double)S * kTcLeastTiles || grid > kTcMostTickets)) break;
+        const double waves = (double)((units * S + num_sms - 1) / num_sms);
+        const double us = waves * (tiles / S * 2.7 + 6.4 + (S > 1 ? 8. : 0.)) + (S > 1 ? 2. * S : 0.);
+        if (S == 1 || us < best.us) best = {S, us};
+    }
+    return best;
+}
+size_t kv_tc_partial_bytes(const KvBatchView& b, int G, int kv_heads, int S, int head_dim) {
+    const int64_t tiles = (int64_t)b.T * G / kTcRows + b.n_seq;
+    return S > 1 ? (size_t)tiles * kv_heads * S * (head_dim + 2) * kTcRows * sizeof(float) : 0;
 }
 cudaError_t launch_kv_attention_tc(const KvCacheView& c, const KvBatchView& b, const uint16_t* Q, int64_t ldQ, int q_heads,
-                                   float scale, uint16_t* Y, int64_t ldY, cudaStream_t st) {
+                                   float scale, uint16_t* Y, int64_t ldY, unsigned int* tickets, float* partial, int S,
+                                   cudaStream_t st) {
     const int G = q_heads / c.kv_heads;
     // above zero, so that a masked score of -inf stays one (below 1e-25 every score is zero beside fp32's steps)
     const float scale_log2 = scale > 1e-25f ? scale * 1.44269504088896340736f : 1e-25f;
     const KvTcArgs a = {c, b, Q, Y, ldQ, ldY, scale_log2, G,
-                        (int)(((int64_t)b.max_new * G + kTcRows - 1) / kTcRows), device_status_ptr()};
-    const unsigned grid = (unsigned)kv_tc_blocks(b, G, c.kv_heads);
+                        (int)(((int64_t)b.max_new * G + kTcRows - 1) / kTcRows), S, partial, tickets, device_status_ptr()};
+    const unsigned grid = (unsigned)((int64_t)a.rt * b.n_seq * c.kv_heads * S);
     return c.head_dim == 64 ? launch_tc<64>(a, grid, st) : launch_tc<128>(a, grid, st);
 }
 

@@ -60,6 +60,7 @@ struct KvAttnPlan {
     bool tc;             // many rows: attention_tc.cu
     int rows;            // query rows of a block at a time: 8 or 16
     int blocks, sms;
+    int S;               // tc: shares of a unit's tokens
     size_t partial_bytes;
 };
 KvAttnPlan plan_kv_attention(const KvBatchView& b, int G, int kv_heads, int head_dim, int num_sms);
@@ -67,9 +68,15 @@ cudaError_t launch_kv_attention(const KvCacheView& c, const KvBatchView& b, cons
                                 float scale, uint16_t* Y, int64_t ldY, unsigned int* tickets, float* partial,
                                 const KvAttnPlan& p, cudaStream_t st);
 
-// attention_tc.cu: many rows on the tensor cores (no workspace)
-int64_t kv_tc_blocks(const KvBatchView& b, int G, int kv_heads);
+// attention_tc.cu: many rows on the tensor cores
+struct KvTcShares {
+    int S;               // of a unit's tokens
+    double us;           // expected
+};
+KvTcShares kv_tc_shares(const KvBatchView& b, int G, int kv_heads, int num_sms);
+size_t kv_tc_partial_bytes(const KvBatchView& b, int G, int kv_heads, int S, int head_dim);
 cudaError_t launch_kv_attention_tc(const KvCacheView& c, const KvBatchView& b, const uint16_t* Q, int64_t ldQ, int q_heads,
-                                   float scale, uint16_t* Y, int64_t ldY, cudaStream_t st);
+                                   float scale, uint16_t* Y, int64_t ldY, unsigned int* tickets, float* partial, int S,
+                                   cudaStream_t st);
 
 }  // namespace glowq

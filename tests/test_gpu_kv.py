@@ -165,7 +165,8 @@ def test_the_cut_into_steps_does_not_matter(cuts):
 ])
 def test_longer_caches(Hq, Hkv, D, cached, new):
     sv = Server(len(new), Hq, Hkv, D, (max(cached) + max(new)) // PAGE + 2, seed=sum(cached) + D)
-    sv.step(cached)
+    if any(cached):
+        sv.step(cached)
     b, Q, qr = sv.step(new)
     sv.check_held(b)
     first = sv.check_attention(b, Q, qr, new)
@@ -177,6 +178,14 @@ def test_longer_caches(Hq, Hkv, D, cached, new):
 ])
 def test_many_rows_over_long_tables(Hq, Hkv, D, cached, new):
     """Enough rows for matrix tiles, but too few blocks of them: pages are shared instead."""
+    test_longer_caches(Hq, Hkv, D, cached, new)
+
+
+@pytest.mark.parametrize("Hq,Hkv,D,cached,new", [
+    (8, 2, 128, [5000, 10, 2600], [70, 129, 1]), (2, 2, 64, [0], [1500]), (4, 1, 128, [9000], [65]), (8, 1, 64, [3000, 2999], [100, 100]),
+])
+def test_matrix_tiles_in_shares(Hq, Hkv, D, cached, new):
+    """Few blocks of many rows: their tokens in shares, some of which the first rows do not see."""
     test_longer_caches(Hq, Hkv, D, cached, new)
 
 
@@ -203,7 +212,7 @@ def test_one_sequence_in_the_most_parts():
 
 @pytest.mark.parametrize("Hq,Hkv,D,cached,new", [
     (4, 2, 64, [300], [700]), (4, 2, 128, [300], [700]), (8, 2, 64, [900, 30, 500], [1, 1, 1]),
-    (8, 2, 128, [900, 30, 500], [1, 1, 1]),
+    (8, 2, 128, [900, 30, 500], [1, 1, 1]), (8, 2, 64, [2000, 10], [70, 129]),
 ])
 def test_the_same_bits_every_time(Hq, Hkv, D, cached, new):
     """Many calls, alone and two at once on two streams, each with its own workspace: no result depends on time."""
