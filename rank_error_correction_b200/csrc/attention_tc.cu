@@ -270,8 +270,9 @@ __global__ void __launch_bounds__(kTcThreads, 1) kv_attention_tc_kernel(const __
                     m[i & 3] = max3(m[i & 3], __uint_as_float(v[2 * i]), __uint_as_float(v[2 * i + 1]));
                 cand = fmaxf(cand, fmaf(fmaxf(fmaxf(m[0], m[1]), fmaxf(m[2], m[3])), q == 0 ? sa[0] : sa[1], q == 0 ? slv[0] : slv[1]));
             }
-            if (__any_sync(~0u, cand > ref + kTcSlack || (ref == -INFINITY && cand > -INFINITY))) {
-                const float next = fmaxf(ref, cand);
+            const bool move = cand > ref + kTcSlack || (ref == -INFINITY && cand > -INFINITY);
+            if (__any_sync(~0u, move)) {
+                const float next = move ? cand : ref;    // (no row depends on its neighbours)
                 if (j > 0) {
                     const float f = ref == next ? 1.f : tc_ex2(ref - next);
                     if (ok) ok = mbar_wait(&sh->o_done[t], (j - 1) & 1, a.status);
