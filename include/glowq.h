@@ -637,10 +637,13 @@ GLOWQ_API glowq_status glowq_kv_read(const glowq_kv_cache* cache, const glowq_kv
  * of kv head h / (q_heads / kv_heads) at positions up to its own,
  *   Y = fp16( sum_j softmax_j(scale q . k_j) v_j ).
  * Keys and values are what glowq_kv_read gives before its rounding to fp16.
- * Scores, softmax statistics and sums are fp32; weights are rounded to fp16
- * for the product with the values.  A row that sees nothing (kv_len below its
- * sequence's new tokens) is zero.  A key, value or page scale that is not
- * finite makes NaN of the rows that see it, and of no other.
+ * Scores, softmax statistics and sums are fp32; for the product with the
+ * values weights are rounded to fp16, or where a sequence has few new tokens to
+ * 2^-23 of the largest of their row and page.  A row that sees nothing (kv_len
+ * below its sequence's new tokens) is zero.  A key, value or page scale that is
+ * not finite makes NaN of the rows that see it, and of no other (an infinite
+ * key that is still in a tail: unless its score is -infinity); so does a query
+ * that is not finite of its own row.
  *   Q  device fp16, rows x q_heads D (pitch ldQ); q_heads % kv_heads == 0
  *   Y  device fp16, rows x q_heads D (pitch ldY); may not overlap Q
  *   workspace  glowq_kv_attention_workspace_bytes bytes: its first 65536 must

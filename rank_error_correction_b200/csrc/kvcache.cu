@@ -115,7 +115,7 @@ __device__ __forceinline__ uint32_t transpose4_lanes(uint32_t w, int t) {
 // first and writes the new tail for the last, in this order.
 // The rows of a page wait in shared memory, each thread's own, so that all of a
 // block's loads are in flight and registers leave room for three blocks an SM
-// (held in registers: two, 2 us slower at 40 heads); blocks of one page's heads
+// (held in registers: two; six prompts of 40 heads took 63 us instead of 58); blocks of one page's heads
 // are neighbours, whose rows are neighbours in memory; a key and its queries
 // share their angles.  168 MB (4096 tokens of 32 heads of 128) in 45 us, 56 % of
 // the copy bandwidth: what is left is latency, the chain from the sequence's
