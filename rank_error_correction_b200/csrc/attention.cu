@@ -28,7 +28,7 @@ constexpr int kAttnWarps = 4;
 constexpr int kAttnThreads = kAttnWarps * 32;
 constexpr int kAttnRing = 4;             // chunks of 4 KB of a warp's ring
 constexpr int kAttnParts = 128;          // blocks that share one unit, at most (and the two at its ends)
-constexpr int kAttnUnitCost = 6;         // what a unit costs beyond its pages, in pages
+constexpr int kAttnUnitCost = 10;        // what a unit costs beyond its pages, in pages
 constexpr int kAttnLeastShare = kAttnUnitCost + 2 * kAttnWarps;
 constexpr float kWeightExp = 8.f;
 
@@ -179,8 +179,8 @@ __device__ __forceinline__ AttnSpan attn_span(const KvSeq& s, const KvBatchView&
 // warps.  The warps' results meet in shared memory, the shares' in the
 // workspace: the block that counts last on a unit adds its parts in order.
 // Bound by memory where there is enough of it: two sequences of 116,000 and
-// 126,000 tokens, 8 kv heads of 128: 497 MB in 97 us, 78 % of the copy bandwidth;
-// 64 sequences of 1 to 4096 tokens: 252 MB in 63 us, 61 % (each of 2.2 units of a
+// 126,000 tokens, 8 kv heads of 128: 497 MB in 94 us, 81 % of the copy bandwidth;
+// 64 sequences of 1 to 4096 tokens: 252 MB in 61 us, 64 % (each of 2.2 units of a
 // block drains its ring, and pays its tail and its merge).  One sequence of 500
 // tokens takes 11 us, all of it latency: lengths, page ids, codes, tail, results.
 template <int D, int RN>
