@@ -816,7 +816,8 @@ KvAttnPlan plan_kv_attention(const KvBatchView& b, int G, int kv_heads, int head
 template <int D, int RN>
 static cudaError_t launch_attn(const KvAttnArgs& a, int blocks, cudaStream_t st) {
     const void* f = (const void*)kv_attention_kernel<D, RN>;
-    cudaError_t e = cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)attn_smem(8 * RN));
+    static SmemLimit limit;
+    cudaError_t e = limit.raise(f, (int)attn_smem(8 * RN));
     if (e != cudaSuccess) return e;
     void* args[] = {(void*)&a};
     return launch_pdl(f, (unsigned)blocks, kAttnThreads, attn_smem(8 * RN), st, args);

@@ -695,8 +695,8 @@ __global__ void __launch_bounds__(kTcThreads, 1) kv_attention_tc_kernel(const __
 
 template <int D>
 static cudaError_t launch_tc(const KvTcArgs& a, unsigned grid, cudaStream_t st) {
-    cudaError_t e = cudaFuncSetAttribute((const void*)kv_attention_tc_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                         KvTc<D>::kSmem);
+    static SmemLimit limit;
+    cudaError_t e = limit.raise((const void*)kv_attention_tc_kernel<D>, KvTc<D>::kSmem);
     if (e != cudaSuccess) return e;
     void* args[] = {(void*)&a};
     return launch_pdl((const void*)kv_attention_tc_kernel<D>, grid, kTcThreads, KvTc<D>::kSmem, st, args);

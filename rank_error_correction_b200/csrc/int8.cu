@@ -555,7 +555,8 @@ Int8GemvPlan plan_int8_gemv(int64_t T, int64_t d, int64_t tiles, int r, int num_
 template <int NT>
 static cudaError_t launch_int8_gemv_t(const Int8GemvArgs& a, const Int8GemvPlan& p, cudaStream_t st) {
     const void* fn = (const void*)int8_gemv_kernel<NT>;
-    cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, 227 * 1024);
+    static SmemLimit limit;
+    cudaError_t e = limit.raise(fn, 227 * 1024);
     if (e != cudaSuccess) return e;
     void* args[] = {(void*)&a};
     return launch_pdl(fn, (unsigned)p.grid, kGemvWarps * 32, (size_t)p.smem, st, args);

@@ -729,8 +729,8 @@ cudaError_t launch_int8_project(const uint16_t* X, const uint16_t* B, int64_t T,
     const int most = 104 * 1024 / proj_stage_bytes(a.rn);        // two blocks an SM: 4 stages at r = 64, 2 at r = 256
     a.stages = most > kProjStages ? kProjStages : most;
     uint32_t ring = (uint32_t)proj_ring_bytes(a.rn, a.stages);
-    cudaError_t e = cudaFuncSetAttribute((const void*)int8_project_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                         kI8SmemMax);
+    static SmemLimit limit;
+    cudaError_t e = limit.raise((const void*)int8_project_kernel, kI8SmemMax);
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)((T + 127) / 128 * kProjParts));
@@ -787,8 +787,8 @@ I8GemmPlan plan_int8_gemm(int64_t T, int64_t d, int64_t mtiles, int num_sms) {
 
 template <int BN>
 static cudaError_t launch_int8_gemm_t(const I8GemmArgs& a, int pairs, cudaStream_t st) {
-    cudaError_t e = cudaFuncSetAttribute((const void*)int8_gemm_kernel<BN>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                         I8Tile<BN>::kSmem);
+    static SmemLimit limit;
+    cudaError_t e = limit.raise((const void*)int8_gemm_kernel<BN>, I8Tile<BN>::kSmem);
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)(2 * pairs));

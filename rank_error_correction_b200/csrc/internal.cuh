@@ -6,6 +6,8 @@
 #include <stddef.h>
 #include <stdint.h>
 
+#include <atomic>
+
 #include "glowq.h"
 
 namespace glowq {
@@ -76,6 +78,22 @@ cudaError_t launch_dequant_fp4(int fmt, const uint32_t* codes, const uint8_t* sc
                                int64_t O, int64_t d, uint16_t* out, cudaStream_t st);
 // A launch that may begin while the preceding kernel of the stream ends (the
 // kernel waits for it with pdl_wait before it touches anything it wrote).
+// A kernel's limit of dynamic shared memory, raised once per device: the call
+// takes 2.4 us of the host, as much as a launch.  One object for each kernel.
+class SmemLimit {
+    std::atomic<uint64_t> raised_{0};
+
+public:
+    cudaError_t raise(const void* fn, int bytes) {
+        int dev = 0;
+        cudaError_t e = cudaGetDevice(&dev);
+        if (e != cudaSuccess) return e;
+        if (dev < 64 && (raised_.load(std::memory_order_acquire) >> dev & 1)) return cudaSuccess;
+        e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+        if (e == cudaSuccess && dev < 64) raised_.fetch_or((uint64_t)1 << dev, std::memory_order_release);
+        return e;
+    }
+};
 cudaError_t launch_pdl(const void* fn, unsigned grid, unsigned block, size_t smem, cudaStream_t st, void** args);
 
 // int8.cu: 8-bit integer weights and activations

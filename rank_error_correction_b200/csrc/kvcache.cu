@@ -376,7 +376,8 @@ cudaError_t launch_kv_append(const KvCacheView& c, const KvBatchView& b, const u
     void* args[] = {(void*)&a};
     const void* f = c.head_dim == 64 ? (const void*)kv_append_kernel<64> : (const void*)kv_append_kernel<128>;
     const int smem = 3 * kKvPage * c.head_dim * 2;       // keys, values and one query head of a page
-    cudaError_t e = cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    static SmemLimit limits[2];
+    cudaError_t e = limits[c.head_dim == 128].raise(f, smem);
     if (e != cudaSuccess) return e;
     return launch_pdl(f, grid, kAppendThreads, smem, st, args);
 }

@@ -578,6 +578,13 @@ def _on(stream):
     return contextlib.nullcontext() if stream is None else torch.cuda.stream(stream)
 
 
+def _raw_stream(device) -> int:
+    """Handle of the device's current stream."""
+    import torch
+    get = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+    return get(device.index) if get is not None else torch.cuda.current_stream(device).cuda_stream
+
+
 class _Call:
     """A library call with its arguments marshalled once.  Calling it enqueues
     the kernels on `stream` (default: the current stream of the tensors'
@@ -590,13 +597,13 @@ class _Call:
 
     def __call__(self, stream=None):
         import torch
-        if stream is None:
-            stream = torch.cuda.current_stream(self._device)
+        # (the raw handle: a Stream object takes longer to make than the launch)
+        raw = _raw_stream(self._device) if stream is None else stream.cuda_stream
         if torch.cuda.current_device() == self._device.index:
-            rc = self._fn(*self._args, C.c_void_p(stream.cuda_stream))
+            rc = self._fn(*self._args, C.c_void_p(raw))
         else:
             with torch.cuda.device(self._device):
-                rc = self._fn(*self._args, C.c_void_p(stream.cuda_stream))
+                rc = self._fn(*self._args, C.c_void_p(raw))
         if rc != 0:
             raise GlowQError(rc, self._name)
         return self.outputs
