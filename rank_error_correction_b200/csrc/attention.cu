@@ -544,11 +544,11 @@ __global__ void __launch_bounds__(kAttnThreads, RN == 1 ? 3 : 2) kv_attention_ke
             }
             // Q as fp16 B fragments: panel p, step q: dimensions 64 p + 16 t + 4 q .. + 3 of query row 8 r + g
             uint32_t qf[RN][kPanels][4][2];
-    #pragma unroll
+#pragma unroll
             for (int r = 0; r < RN; ++r) {
                 const int row = row0 + 8 * r + g;
                 const uint16_t* q = a.Q + (int64_t)(s.q0 + row / a.G) * a.ldQ + (int64_t)(h * a.G + row % a.G) * D + 16 * t;
-    #pragma unroll
+#pragma unroll
                 for (int p = 0; p < kPanels; ++p) {
                     const uint4 u = ldcg_128_if(q + 64 * p, row < rows), v = ldcg_128_if(q + 64 * p + 8, row < rows);
                     qf[r][p][0][0] = u.x;
