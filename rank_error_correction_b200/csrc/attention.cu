@@ -99,51 +99,34 @@ struct AttnState {
     float m[RN][2], l[RN][2], o[RN][D / 16][4];          // l: this lane's tokens only
 };
 
-// NT tiles of 16 tokens.  tok(i, u): token, within the page, of row g + 8 u of
-// tile i; lim: last visible token of each query row; lv = log2 s_V.  Returns the
+// One tile of 16 tokens of a tail, at column g and g + 8 in this lane; lim: last
+// visible token of each query row; lv = log2 of the tail's unit.  Returns the
 // weights as B fragments (k = tokens, n = query rows).
-template <int D, int RN, int NT, class Tok>
-__device__ __forceinline__ void softmax_tile(AttnState<D, RN>& st, float (&x)[RN][NT][4], const int (&lim)[RN][2], float xs,
-                                             float lv, float inv_sv, bool masked, Tok tok, uint32_t (&pf)[RN][NT][2]) {
+template <int D, int RN>
+__device__ __forceinline__ void softmax_tail(AttnState<D, RN>& st, float (&x)[RN][4], const int (&lim)[RN][2], float xs, float lv,
+                                             float inv_sv, int g, uint32_t (&pf)[RN][2]) {
     float corr[RN][2];
     bool moved = false;
 #pragma unroll
     for (int r = 0; r < RN; ++r) {
-        float mx[2] = {-INFINITY, -INFINITY};
 #pragma unroll
-        for (int i = 0; i < NT; ++i)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                float v = fmaf(x[r][i][e], xs, lv);
-                if (masked && tok(i, e >> 1) > lim[r][e & 1]) v = -INFINITY;
-                x[r][i][e] = v;
-                mx[e & 1] = fmaxf(mx[e & 1], v);
-            }
+        for (int e = 0; e < 4; ++e) x[r][e] = g + 8 * (e >> 1) > lim[r][e & 1] ? -INFINITY : fmaf(x[r][e], xs, lv);
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
-            mx[e] = fmaxf(mx[e], __shfl_xor_sync(~0u, mx[e], 4));
-            mx[e] = fmaxf(mx[e], __shfl_xor_sync(~0u, mx[e], 8));
-            mx[e] = fmaxf(st.m[r][e], fmaxf(mx[e], __shfl_xor_sync(~0u, mx[e], 16)));
-            const float ref = mx[e] == -INFINITY ? 0.f : mx[e];       // nothing visible yet: weights 2^-inf = 0
+            float m = fmaxf(x[r][e], x[r][e + 2]);
+            m = fmaxf(m, __shfl_xor_sync(~0u, m, 4));
+            m = fmaxf(m, __shfl_xor_sync(~0u, m, 8));
+            m = fmaxf(st.m[r][e], fmaxf(m, __shfl_xor_sync(~0u, m, 16)));
+            const float ref = m == -INFINITY ? 0.f : m;               // nothing visible yet: weights 2^-inf = 0
             corr[r][e] = ex2(st.m[r][e] - ref);
             moved |= corr[r][e] != 1.f;
-            st.m[r][e] = mx[e];
-            const float base = ref - kWeightExp;
-            float sum = 0.f;
-#pragma unroll
-            for (int i = 0; i < NT; ++i) {
-                x[r][i][e] = ex2(x[r][i][e] - base);
-                x[r][i][e + 2] = ex2(x[r][i][e + 2] - base);
-                sum += x[r][i][e] + x[r][i][e + 2];
-            }
-            // tokens that are not seen take nothing from the page's scale (which may be NaN)
-            st.l[r][e] = st.l[r][e] * corr[r][e] + (sum == 0.f ? 0.f : sum * inv_sv);
+            st.m[r][e] = m;
+            x[r][e] = ex2(x[r][e] - (ref - kWeightExp));
+            x[r][e + 2] = ex2(x[r][e + 2] - (ref - kWeightExp));
+            st.l[r][e] = fmaf(x[r][e] + x[r][e + 2], inv_sv, st.l[r][e] * corr[r][e]);
         }
-#pragma unroll
-        for (int i = 0; i < NT; ++i) {
-            pf[r][i][0] = movm(h2_as_u32(__floats2half2_rn(x[r][i][0], x[r][i][1])));
-            pf[r][i][1] = movm(h2_as_u32(__floats2half2_rn(x[r][i][2], x[r][i][3])));
-        }
+        pf[r][0] = movm(h2_as_u32(__floats2half2_rn(x[r][0], x[r][1])));
+        pf[r][1] = movm(h2_as_u32(__floats2half2_rn(x[r][2], x[r][3])));
     }
     if (__any_sync(~0u, moved)) {
 #pragma unroll
@@ -563,9 +546,9 @@ __global__ void __launch_bounds__(kAttnThreads, RN == 1 ? 3 : 2) kv_attention_ke
             }
             asm volatile("cp.async.wait_all;" ::: "memory");
             __syncwarp();
-            float x[RN][1][4];
+            float x[RN][4];
 #pragma unroll
-            for (int r = 0; r < RN; ++r) x[r][0][0] = x[r][0][1] = x[r][0][2] = x[r][0][3] = 0.f;
+            for (int r = 0; r < RN; ++r) x[r][0] = x[r][1] = x[r][2] = x[r][3] = 0.f;
 #pragma unroll
             for (int pn = 0; pn < kPanels; ++pn) {
                 const int c0 = 8 * pn + 2 * t;                       // rows g and g + 8 (the same swizzle)
@@ -577,7 +560,7 @@ __global__ void __launch_bounds__(kAttnThreads, RN == 1 ? 3 : 2) kv_attention_ke
 #pragma unroll
                 for (int q = 0; q < 4; ++q)
 #pragma unroll
-                    for (int r = 0; r < RN; ++r) mma_16816(x[r][0], af[q], qf[r][pn][q]);
+                    for (int r = 0; r < RN; ++r) mma_16816(x[r], af[q], qf[r][pn][q]);
             }
             // A value that is not finite makes NaN of the rows that see its token and
             // must not reach the others (0 x inf): it is taken out of the product and
@@ -616,15 +599,15 @@ __global__ void __launch_bounds__(kAttnThreads, RN == 1 ? 3 : 2) kv_attention_ke
                 for (int r = 0; r < RN; ++r)
 #pragma unroll
                     for (int e = 0; e < 4; ++e)
-                        if ((poison >> (g + 8 * (e >> 1))) & 1) x[r][0][e] = __int_as_float(0x7fffffff);
+                        if ((poison >> (g + 8 * (e >> 1))) & 1) x[r][e] = __int_as_float(0x7fffffff);
             }
             int lim[RN][2];
 #pragma unroll
             for (int r = 0; r < RN; ++r)
 #pragma unroll
                 for (int e = 0; e < 2; ++e) lim[r][e] = min(limit[r][e] - full * kKvPage, ntok - 1) - warp * 16;
-            uint32_t pf[RN][1][2];
-            softmax_tile<D, RN, 1>(st, x, lim, a.scale_log2, (float)-k2, exp2f((float)k2), true, [&](int, int u) { return g + 8 * u; }, pf);
+            uint32_t pf[RN][2];
+            softmax_tail<D, RN>(st, x, lim, a.scale_log2, (float)-k2, exp2f((float)k2), g, pf);
 #pragma unroll
             for (int d = 0; d < D / 16; ++d) {
                 // four 8 x 8 matrices: dimensions 16 d .. + 7 and + 8 .. + 15 of tokens 0 .. 7, then of tokens 8 .. 15
@@ -634,7 +617,7 @@ __global__ void __launch_bounds__(kAttnThreads, RN == 1 ? 3 : 2) kv_attention_ke
 #pragma unroll
                 for (int e = 0; e < 4; ++e) v[e] = h2_as_u32(__hmul2(u32_as_h2(v[e]), up));
 #pragma unroll
-                for (int q = 0; q < RN; ++q) mma_16816(st.o[q][d], v, pf[q][0]);
+                for (int q = 0; q < RN; ++q) mma_16816(st.o[q][d], v, pf[q]);
             }
         }
         // ---- the warps' results: [warp][rows][D + 4] over the rings, m and l beside them ----
