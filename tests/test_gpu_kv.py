@@ -397,6 +397,41 @@ def test_in_place_rotation_streams_and_graphs():
     sv.check_held(b)
 
 
+def test_one_workspace_for_every_call_and_a_graph():
+    """8-bit products of all token counts and attention of few and of many rows, whole and in shares, one after another on
+    the same workspace, alone and in a graph: the same bits, and its head left zero."""
+    import torch
+    import test_gpu_w8a8 as w
+    sv = Server(2, 8, 2, 64, 40, seed=13)
+    sv.step([2000, 10])
+    ws, calls = torch.zeros(1 << 26, dtype=torch.uint8, device="cuda"), []
+    many, Qm, qm = sv.step([70, 129])
+    few, Qf, qf = sv.step([1, 1])
+    lens = [[2070, 139], [2071, 140]]
+    for b, Q, n in ((many, Qm, 0), (few, Qf, 1)):
+        calls.append(glowq.KVAttentionPlan(sv.cache, sv.batch([70, 129] if n == 0 else [1, 1], lens=lens[n]), Q, workspace=ws))
+    for T in (1, 40, 300):
+        mods, B, X = w.make(T, 512, [512, 128], 64, seed=T)
+        calls.append(glowq.Int8ForwardPlan(w.dev_mods(mods), cuda(B), cuda(X), workspace=ws))
+    flat = lambda c: torch.cat([y.reshape(-1) for y in (c.outputs if isinstance(c.outputs, (list, tuple)) else [c.outputs])])
+    want = []
+    for c in calls:
+        c()
+        want.append(flat(c).clone())
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        for c in calls + calls[::-1]:
+            c()
+    for _ in range(3):
+        for c in calls:
+            for y in c.outputs if isinstance(c.outputs, (list, tuple)) else [c.outputs]:
+                y.zero_()
+        g.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(flat(c), x) for c, x in zip(calls, want))
+    assert int(ws[:65536].max()) == 0
+
+
 def test_a_layers_attention_half():
     """The Q/K/V group, append, attention and o_proj as one step after another, 8-bit throughout, on the same buffers:
     each stage against its plain form from the stage's own inputs."""
