@@ -608,8 +608,8 @@ typedef struct glowq_kv_batch {
  *            (elements, % 8 == 0): e.g. column slices of a Q/K/V group's output
  *   Q        device fp16, rows x q_heads D (pitch ldQ), or NULL (q_heads 0):
  *            rotated into Q_out (pitch ldQ_out), which may be Q itself
- *   rope     device fp32 [rope_len][D]: cosines of the D/2 pairs of the row's
- *            position, then their sines; pair i is (x_i, x_{i + D/2}) ->
+ *   rope     device fp32 [rope_len][D], 16-byte aligned: cosines of the D/2 pairs
+ *            of the row's position, then their sines; pair i is (x_i, x_{i + D/2}) ->
  *            (x_i cos - x_{i+D/2} sin, x_{i+D/2} cos + x_i sin), two fp32
  *            products and a sum, unfused, rounded to fp16.  NULL: no rotation
  *            (Q, if given, is copied).  Positions from rope_len on are out of range.

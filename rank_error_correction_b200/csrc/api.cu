@@ -649,7 +649,7 @@ glowq_status glowq_kv_append(const glowq_kv_cache* cache, const glowq_kv_batch* 
     if (Q && ((v = kv_array(Q, ldQ, q_heads, c.head_dim)) != GLOWQ_OK ||
               (v = kv_array(Q_out, ldQ_out, q_heads, c.head_dim)) != GLOWQ_OK))
         return v;
-    if (reinterpret_cast<uintptr_t>(rope) & 7u) return GLOWQ_ERR_ALIGN;
+    if (!aligned16(rope)) return GLOWQ_ERR_ALIGN;            // angles are loaded four at a time
     if (!fits_grid((int64_t)kv_touched_pages(b.max_new) * b.n_seq) ||
         !fits_grid((int64_t)kv_touched_pages(b.max_new) * b.n_seq * c.kv_heads))
         return GLOWQ_ERR_SHAPE;

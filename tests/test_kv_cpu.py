@@ -97,3 +97,9 @@ def test_binding_refuses():
     with pytest.raises(ValueError, match="CUDA"):
         i = lambda *s: torch.zeros(*s, dtype=torch.int32)
         glowq.KVBatch(i(3), i(2), i(2, 4), i(2), 2, 1)
+
+
+@pytest.mark.parametrize("off", [4, 8, 12])
+def test_rotation_table_is_read_16_bytes_at_a_time(L, off):
+    """A view of a larger table may begin at any float: only 16-byte boundaries are taken."""
+    assert _append(L, rope=0xb000 + off) == ALIGN
