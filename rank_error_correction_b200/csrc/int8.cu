@@ -231,8 +231,11 @@ __device__ __forceinline__ void prep_rows(const Int8PrepArgs& a) {
 }
 
 __global__ void __launch_bounds__(kQuantThreads) int8_prep_kernel(const Int8PrepArgs a) {
-    pdl_launch_dependents();                     // the product may take its SMs and fetch weights
     pdl_wait();                                  // X is final; the previous call's readers of xq, xs, R are done
+    // Only now may the product take its SMs: it fetches weights before it waits
+    // itself, and a module's codes may come from a kernel that lets its dependents
+    // start early (the token quantiser's codes and scales have a module's format).
+    pdl_launch_dependents();
     if ((int)blockIdx.x < a.r / kPrepRows) {
         if (a.T <= 4) prep_rows<4>(a);
         else prep_rows<kPrepTokens>(a);
@@ -258,7 +261,8 @@ __global__ void __launch_bounds__(kQuantThreads) int8_prep_kernel(const Int8Prep
 // between copy and use.  mma.m16n8k32 takes k in any order as long as both
 // operands agree: lane (g, t) holds the 16 bytes k = 64 h + 16 t .. + 15 of
 // rows g and g + 8, and of token g of the staged activations.
-// The first blocks of W are in flight while the first launch runs.
+// The first blocks of W are in flight while the first launch runs, which has
+// waited for everything before the call.
 // ---------------------------------------------------------------------------
 constexpr int kGemvWarps = 8;
 constexpr int kGemvStages = 4;

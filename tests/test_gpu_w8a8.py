@@ -199,3 +199,43 @@ def test_shared_workspace_across_shapes_streams_and_graphs(T):
     g.replay()
     torch.cuda.synchronize()
     check(plan.outputs, plan.R, *plain8.w8a8(X[::-1].copy(), mods, B))
+
+
+@pytest.mark.parametrize("T", [1, 5, 16, 40])
+@pytest.mark.parametrize("r", [0, 64])
+def test_weights_written_by_the_call_before(T, r):
+    """A module whose codes and scales the token quantiser, or the weight quantiser, writes on the same stream directly
+    ahead of the forward call, which may fetch nothing of them early."""
+    import torch
+    O, d = 4096, 2048
+    g = np.random.default_rng(T)
+    L, stream = glowq.lib(), torch.cuda.current_stream()
+    Ws = [cuda((g.standard_normal((O, d)) * 0.02).astype(np.float16)) for _ in range(2)]
+    _, B, X = make(T, d, [16], r, seed=T)
+    A = cuda((g.standard_normal((O, r)) * 0.005).astype(np.float16)) if r else None
+    mod = glowq.Int8Module(torch.zeros((O, d), dtype=torch.int8, device="cuda"), torch.zeros(O, device="cuda"), A)
+    plan = glowq.Int8ForwardPlan([mod], cuda(B), cuda(X))
+
+    def write(W, packs):
+        if packs:
+            rc = L.glowq_pack_int8(W.data_ptr(), O, d, mod.codes.data_ptr(), mod.scales.data_ptr(), stream.cuda_stream)
+        else:
+            rc = L.glowq_quantize_act_int8(W.data_ptr(), O, d, mod.codes.data_ptr(), mod.scales.data_ptr(), stream.cuda_stream)
+        assert rc == 0
+
+    want, full = [], [W.float() for W in Ws]
+    for W in Ws:
+        write(W, False)
+        torch.cuda.synchronize()
+        plan()
+        q, s = plain8.quantize_rows(W.cpu().numpy())
+        check(plan.outputs, plan.R, *plain8.w8a8(X, [(q, s, None if A is None else A.cpu().numpy())], B))
+        want.append(plan.outputs[0].clone())
+    assert not torch.equal(*want)
+    for packs in (False, True):
+        for i in range(20):
+            torch.cuda._sleep(200000)            # all of what follows is enqueued before it begins
+            write((full if packs else Ws)[i % 2], packs)
+            plan()
+            torch.cuda.synchronize()
+            assert torch.equal(plan.outputs[0], want[i % 2])
