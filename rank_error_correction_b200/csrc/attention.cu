@@ -121,8 +121,8 @@ __device__ __forceinline__ void softmax_tail(AttnState<D, RN>& st, float (&x)[RN
             corr[r][e] = ex2(st.m[r][e] - ref);
             moved |= corr[r][e] != 1.f;
             st.m[r][e] = m;
-            x[r][e] = ex2(x[r][e] - (ref - kWeightExp));
-            x[r][e + 2] = ex2(x[r][e + 2] - (ref - kWeightExp));
+            x[r][e] = ex2(x[r][e] - ref + kWeightExp);               // (x - ref is exact where it matters, however large they are)
+            x[r][e + 2] = ex2(x[r][e + 2] - ref + kWeightExp);
             st.l[r][e] = fmaf(x[r][e] + x[r][e + 2], inv_sv, st.l[r][e] * corr[r][e]);
         }
         pf[r][0] = movm(h2_as_u32(__floats2half2_rn(x[r][0], x[r][1])));
@@ -422,30 +422,33 @@ __global__ void __launch_bounds__(kAttnThreads, RN == 1 ? 3 : 2) kv_attention_ke
                             for (int e = 0; e < 4; ++e)
                                 if (p * kKvPage + 16 * (g >> 1) + 4 * i + (g & 1) + 2 * (e >> 1) > limit[r][e & 1]) x[r][i][e] = -INFINITY;
                 }
-                // weights 2^23 of the page's largest, and their bytes as B fragments (k = tokens, n = query rows)
+                // Weights 2^23 of the page's largest, and their bytes as B fragments (k = tokens, n = query rows).
+                // What 2^23 stands for is base = mx - 23 rounded up, of which the joining factor `to` is made too:
+                // x - base is exact near the maximum and never above 23, so that no weight passes its 24 bits
+                // however large the scores are (23 - mx, rounded, did from 2^24 on: x + 23 - mx could be 24 or more).
                 uint32_t pd[RN][3][4];
                 float to[RN][2];                                     // what one of them weighs
                 bool moved = false;
                 float corr[RN][2];
 #pragma unroll
                 for (int r = 0; r < RN; ++r) {
-                    float mx[2], base[2];
+                    float base[2];
 #pragma unroll
                     for (int e = 0; e < 2; ++e) {
-                        mx[e] = fmaxf(x[r][0][e], x[r][0][e + 2]);
+                        float mx = fmaxf(x[r][0][e], x[r][0][e + 2]);
 #pragma unroll
-                        for (int i = 1; i < 4; ++i) mx[e] = max3(mx[e], x[r][i][e], x[r][i][e + 2]);
-                        mx[e] = fmaxf(mx[e], __shfl_xor_sync(~0u, mx[e], 4));
-                        mx[e] = fmaxf(mx[e], __shfl_xor_sync(~0u, mx[e], 8));
-                        mx[e] = fmaxf(mx[e], __shfl_xor_sync(~0u, mx[e], 16));
-                        base[e] = 23.f - (mx[e] == -INFINITY ? 0.f : mx[e]);   // (nothing visible: weights 2^-inf = 0)
-                        const float m = fmaxf(st.m[r][e], mx[e]), ref = m == -INFINITY ? 0.f : m;
+                        for (int i = 1; i < 4; ++i) mx = max3(mx, x[r][i][e], x[r][i][e + 2]);
+                        mx = fmaxf(mx, __shfl_xor_sync(~0u, mx, 4));
+                        mx = fmaxf(mx, __shfl_xor_sync(~0u, mx, 8));
+                        mx = fmaxf(mx, __shfl_xor_sync(~0u, mx, 16));
+                        base[e] = mx == -INFINITY ? 0.f : __fadd_ru(mx, -23.f);   // (nothing visible: weights 2^-inf = 0)
+                        const float m = fmaxf(st.m[r][e], mx), ref = m == -INFINITY ? 0.f : m;
                         corr[r][e] = ex2(st.m[r][e] - ref);
-                        to[r][e] = ex2(mx[e] - ref + (kWeightExp - 23.f));
+                        to[r][e] = mx == -INFINITY ? 0.f : ex2(base[e] - ref + kWeightExp);
                         moved |= corr[r][e] != 1.f;
                         st.m[r][e] = m;
                     }
-                    const uint64_t b2 = pack_f2(base[0], base[1]), one = pack_f2(8388608.f, 8388608.f);
+                    const uint64_t b2 = pack_f2(-base[0], -base[1]), one = pack_f2(8388608.f, 8388608.f);
                     uint64_t sum = 0;
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {

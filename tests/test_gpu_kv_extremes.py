@@ -1,0 +1,91 @@
+"""Attention over the 8-bit cache where single precision is at its ends, on both
+kernels: which of them a call runs is read off the workspace that it asks for."""
+import numpy as np
+import pytest
+
+from rank_error_correction_b200 import build, glowq
+
+import plain8
+from test_gpu_kv import PAGE, Server, cuda
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _lib():
+    import torch
+    assert torch.cuda.is_available(), "GPU tests need a CUDA device"
+    build.build()
+    glowq.lib()
+    yield
+    assert glowq.device_status() == 0
+
+
+def kernel_of(cache, batch, Hq):
+    """'pages' (few rows), 'tiles' or 'shares' (matrix tiles, whole or with a unit's tokens in shares), by the scratch
+    behind the workspace's head: [block][2][8 or 16 rows][D + 4] floats, none, or [..][head][share][D + 2][256 rows]."""
+    D = cache.head_dim
+    n = glowq.kv_attention_workspace(cache, batch, Hq).numel() - 65536
+    if n == 0:
+        return "tiles"
+    few, many = n % (2 * 8 * (D + 4) * 4) == 0, n % (cache.kv_heads * (D + 2) * 256 * 4) == 0
+    assert few != many, n
+    return "pages" if few else "shares"
+
+
+def one_page_softmax(q, k, v, start, scale):
+    """Rows whose weight is all in one page or the tail, with scores apart from the others' by far more than fp32's
+    steps: (Y, bound, which rows).  There equal scores have equal weights and all others none, whatever the scores' size."""
+    n, Hq, D = q.shape
+    L, G = len(k), Hq // k.shape[1]
+    Y, bound, ok = np.zeros((n, Hq, D)), np.ones((n, Hq, D)), np.zeros((n, Hq), bool)
+    u16, u32 = 2.0 ** -11, 2.0 ** -23
+    for i in range(n):
+        m = min(L, start + i + 1)
+        for h in range(Hq):
+            s = k[:m, h // G] @ q[i, h].astype(np.float64) * scale
+            top = s == s.max()
+            # fp32 sums of D products and what is applied to them: off by no more than (D + 10) steps of the largest score
+            gap = 100.0 + 2 * (D + 10) * u32 * np.abs(s).max()
+            if np.any(~top & (s > s.max() - gap)) or len(set(np.nonzero(top)[0] // PAGE)) > 1:
+                continue
+            ok[i, h] = True
+            Y[i, h] = v[:m, h // G][top].mean(0)
+            # equal weights, each rounded to fp16 at most once and summed unrounded; sums in fp32; the output's rounding
+            b = (u16 + (top.sum() + 8) * u32) * np.abs(v[:m, h // G][top]).mean(0)
+            bound[i, h] = b + u16 * (np.abs(Y[i, h]) + b) + 2.0 ** -25
+    return Y, bound, ok
+
+
+@pytest.mark.parametrize("size,scale", [(300.0, None), (1000.0, None), (4000.0, 1.0), (20000.0, None),
+                                        (30000.0, 1.0), (60000.0, 1e6)])
+@pytest.mark.parametrize("kernel,Hq,Hkv,D,cached,new", [
+    ("pages", 4, 2, 128, [1000, 130], [1, 3]), ("pages", 2, 2, 64, [640, 63], [1, 1]), ("pages", 2, 1, 128, [9000], [6]),
+    ("pages", 16, 1, 64, [0, 300], [1, 1]), ("tiles", 4, 2, 128, [100, 0], [300, 70]), ("tiles", 4, 2, 64, [300, 64], [128, 200]),
+    ("shares", 4, 2, 64, [4000], [200]),
+])
+def test_scores_of_any_size(kernel, Hq, Hkv, D, cached, new, size, scale):
+    """Queries and keys along one direction, so that scores are as large as fp16 allows (past 2^36, past the steps at
+    which single precision still counts ones), and the softmax is a choice."""
+    sv = Server(len(new), Hq, Hkv, D, (max(cached) + max(new)) // PAGE + 2, seed=D + len(new))
+
+    def data(counts):
+        q, k, v = sv.draw(counts)
+        T = sum(counts)
+        k = np.broadcast_to(sv.g.uniform(0.2, 1.0, (T, Hkv, 1)) * size, k.shape).astype(np.float16)
+        q = np.broadcast_to(sv.g.choice([-1.0, 1.0], (T, Hq, 1)) * sv.g.uniform(0.5, 1.0, (T, Hq, 1)) * size, q.shape)
+        return q.astype(np.float16), k, v
+
+    if any(cached):
+        sv.step(cached, rope=False, data=data(cached))
+    b, Q, qr = sv.step(new, rope=False, data=data(new))
+    assert kernel_of(sv.cache, b, Hq) == kernel
+    got = glowq.kv_attention(sv.cache, b, Q, scale=scale, workspace=sv.ws).cpu().numpy().reshape(-1, Hq, D)
+    at, rows, worst = 0, 0, 0.0
+    for s, n in zip(sv.seq, new):
+        y, bound, ok = one_page_softmax(qr[at:at + n], *s.held(), len(s.k) - n, D ** -0.5 if scale is None else scale)
+        worst = max(worst, plain8.within(got[at:at + n][ok], y[ok], bound[ok]))
+        rows += ok.sum()
+        at += n
+    assert worst <= 1.0, worst
+    assert rows >= sum(new) * Hq // 2, rows
