@@ -308,14 +308,17 @@ __global__ void __launch_bounds__(kTcThreads, 1) kv_attention_tc_kernel(const __
             const float less = base == -INFINITY ? 0.f : base;
             float off[2] = {slv[0] - less, slv[1] - less};
             if (apart) {
-                // here first the scores become x - base, and then the weights are of them as they are
+                // here first the scores become x - base, and then the weights are of them as they are; a row whose
+                // own scores are ordinary gets the same bits as without such neighbours
+                const bool mine = fabsf(less) >= kTcApart;
+                const float then = mine ? less : 0.f;
 #pragma unroll 1
                 for (int c = 0; c < 4; ++c) {
-                    const float a1 = c < 2 ? sa[0] : sa[1], lv = c < 2 ? slv[0] : slv[1];
+                    const float a1 = c < 2 ? sa[0] : sa[1], add = c < 2 ? (mine ? slv[0] : off[0]) : (mine ? slv[1] : off[1]);
                     uint32_t v[32];
                     tmem_ld32(ts + c * 32, v);
 #pragma unroll
-                    for (int i = 0; i < 32; ++i) v[i] = __float_as_uint(fmaf(__uint_as_float(v[i]), a1, lv) - less);
+                    for (int i = 0; i < 32; ++i) v[i] = __float_as_uint(fmaf(__uint_as_float(v[i]), a1, add) - then);
                     tmem_st32(ts + c * 32, v);
                 }
                 sa[0] = sa[1] = 1.f;

@@ -89,3 +89,23 @@ def test_scores_of_any_size(kernel, Hq, Hkv, D, cached, new, size, scale):
         at += n
     assert worst <= 1.0, worst
     assert rows >= sum(new) * Hq // 2, rows
+
+
+@pytest.mark.parametrize("kernel,Hq,Hkv,D,cached,new", [
+    ("pages", 4, 2, 128, 300, 3), ("tiles", 4, 2, 128, 100, 150), ("tiles", 2, 1, 64, 0, 200), ("shares", 4, 2, 64, 4000, 200),
+])
+def test_a_row_does_not_depend_on_the_scores_beside_it(kernel, Hq, Hkv, D, cached, new):
+    """Every third query's scores pass 2^24 (and so does what a warp does with them): the others keep their bits."""
+    sv = Server(1, Hq, Hkv, D, (cached + new) // PAGE + 2, seed=3)
+    if cached:
+        sv.step([cached])
+    b, Q, _ = sv.step([new])
+    assert kernel_of(sv.cache, b, Hq) == kernel
+    want = glowq.kv_attention(sv.cache, b, Q, scale=500.0, workspace=sv.ws)
+    Q2 = Q.clone()
+    Q2[::3] *= 6000.0
+    assert bool(Q2.isfinite().all())
+    got = glowq.kv_attention(sv.cache, b, Q2, scale=500.0, workspace=sv.ws)
+    rest = np.arange(new) % 3 != 0
+    assert bool(got.isfinite().all())
+    assert np.array_equal(got.cpu().numpy()[rest], want.cpu().numpy()[rest])
