@@ -642,8 +642,9 @@ GLOWQ_API glowq_status glowq_kv_read(const glowq_kv_cache* cache, const glowq_kv
  * 2^-23 of the largest of their row and page.  A row that sees nothing (kv_len
  * below its sequence's new tokens) is zero.  A key, value or page scale that is
  * not finite makes NaN of the rows that see it, and of no other (an infinite
- * key that is still in a tail: unless its score is -infinity); so does a query
- * that is not finite of its own row.
+ * key that is still in a tail has no weight where its score is -infinity; a
+ * row with no other score is NaN); so does a query that is not finite of its
+ * own row.
  *   Q  device fp16, rows x q_heads D (pitch ldQ); q_heads % kv_heads == 0
  *   Y  device fp16, rows x q_heads D (pitch ldY); may not overlap Q
  *   workspace  glowq_kv_attention_workspace_bytes bytes: its first 65536 must

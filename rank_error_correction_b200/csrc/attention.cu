@@ -17,6 +17,8 @@
 // An incomplete last page is fp16, and its products are: weights, scaled by 2^8
 // (the factor cancels; fp16's smallest normal is then 2^-22 of the largest), are
 // rounded to fp16 (2^-11).  Sums, maxima and outputs in fp32.
+#include <climits>
+
 #include "common.cuh"
 #include "internal.cuh"
 #include "kvcache.cuh"
@@ -335,6 +337,7 @@ __global__ void __launch_bounds__(kAttnThreads, RN == 1 ? 3 : 2) kv_attention_ke
             for (int n = 0; n < D / 16; ++n) st.o[r][n][0] = st.o[r][n][1] = st.o[r][n][2] = st.o[r][n][3] = 0.f;
         }
         const int least = row0 + kRows > rows ? -1 : s.start + row0 / a.G;   // no column behind it is masked
+        int from = INT_MAX;                                          // the first position that this warp's tokens have
 
         // this warp's pages pa + warp, + 4, ...: page ids and scales of 32 at a time, one in each lane
         for (int p0 = pa + warp; p0 < pc; p0 += 32 * kAttnWarps) {
@@ -351,7 +354,8 @@ __global__ void __launch_bounds__(kAttnThreads, RN == 1 ? 3 : 2) kv_attention_ke
                     vs = ldcg_f32(a.c.v_scales + (int64_t)id * a.c.kv_heads + h);
                 }
             }
-            __syncwarp();
+            const unsigned present = __ballot_sync(~0u, id >= 0);
+            if (from == INT_MAX && present) from = (p0 + (__ffs(present) - 1) * kAttnWarps) * kKvPage;
             const float lvs = log2f(vs), ivs = 1.f / vs;
             auto fetch = [&](int f) {                                // chunks in the order K, V of each page
                 const int page = __shfl_sync(~0u, id, f / (2 * kPanels) & 31);
@@ -623,7 +627,13 @@ __global__ void __launch_bounds__(kAttnThreads, RN == 1 ? 3 : 2) kv_attention_ke
                 for (int q = 0; q < RN; ++q) mma_16816(st.o[q][d], v, pf[q]);
             }
         }
+        if (tails) from = min(from, full * kKvPage + warp * 16);
         // ---- the warps' results: [warp][rows][D + 4] over the rings, m and l beside them ----
+#pragma unroll
+        for (int r = 0; r < RN; ++r)
+#pragma unroll
+            for (int e = 0; e < 2; ++e)
+                if (limit[r][e] >= from) st.m[r][e] = fmaxf(st.m[r][e], kLeastScore);
 #pragma unroll
         for (int r = 0; r < RN; ++r)
 #pragma unroll
@@ -651,10 +661,11 @@ __global__ void __launch_bounds__(kAttnThreads, RN == 1 ? 3 : 2) kv_attention_ke
         }
         __syncthreads();
         const bool whole = pa == 0 && pe == w.pages;
-        auto store = [&](int r, int c, float l, const float4& o) {
+        auto store = [&](int r, int c, float m, float l, const float4& o) {
             const int row = row0 + r;
             if (row >= rows) return;
-            const float inv = l == 0.f ? 0.f : 1.f / l;              // a row that sees nothing is zero
+            // a row that sees nothing is zero, one whose scores are all -inf NaN
+            const float inv = l != 0.f ? 1.f / l : m == -INFINITY ? 0.f : __int_as_float(0x7fffffff);
             uint2 y;
             y.x = h2_as_u32(__floats2half2_rn(o.x * inv, o.y * inv));
             y.y = h2_as_u32(__floats2half2_rn(o.z * inv, o.w * inv));
@@ -678,7 +689,7 @@ __global__ void __launch_bounds__(kAttnThreads, RN == 1 ? 3 : 2) kv_attention_ke
                 o = make_float4(fmaf(f, v.x, o.x), fmaf(f, v.y, o.y), fmaf(f, v.z, o.z), fmaf(f, v.w, o.w));
             }
             if (whole) {
-                store(r, c, l, o);
+                store(r, c, m, l, o);
             } else {
                 __stcg(reinterpret_cast<float4*>(part + r * kPart + 4 * c), o);
                 if (c == 0) __stcg(reinterpret_cast<float2*>(part + r * kPart + D), make_float2(m, l));
@@ -717,7 +728,10 @@ __global__ void __launch_bounds__(kAttnThreads, RN == 1 ? 3 : 2) kv_attention_ke
                         l = fmaf(f, all[2 * (k * kRows + r) + 1], l);
                     }
                     for (int o = 16; o > 0; o >>= 1) l += __shfl_xor_sync(~0u, l, o);
-                    if (lane == 0) sml[r] = l;
+                    if (lane == 0) {
+                        sml[2 * r] = m;
+                        sml[2 * r + 1] = l;
+                    }
                 }
                 __syncthreads();
                 // a warp adds every fourth part, eight rows at a time, two parts' loads in flight; then the warps' sums
@@ -760,7 +774,7 @@ __global__ void __launch_bounds__(kAttnThreads, RN == 1 ? 3 : 2) kv_attention_ke
                         const float4 v = reinterpret_cast<const float4*>(sums)[k * kRows * (D / 4) + i];
                         o = make_float4(o.x + v.x, o.y + v.y, o.z + v.z, o.w + v.w);
                     }
-                    store(i / (D / 4), i % (D / 4), sml[i / (D / 4)], o);
+                    store(i / (D / 4), i % (D / 4), sml[i / (D / 4) * 2], sml[i / (D / 4) * 2 + 1], o);
                 }
             }
         }

@@ -273,7 +273,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) kv_attention_tc_kernel(const __
                     for (int i = 0; i < 64; ++i) v[i] = i < n ? v[i] : 0xff800000u;
                 }
             };
-            float cand = -INFINITY;
+            float cand = see[0] > 0 || see[1] > 0 ? kLeastScore : -INFINITY;   // (a row that sees something has a maximum)
 #pragma unroll 1
             for (int q = 0; q < 2; ++q) {
                 uint32_t v[64];
@@ -402,15 +402,17 @@ __global__ void __launch_bounds__(kTcThreads, 1) kv_attention_tc_kernel(const __
             if (last) {
                 base = -INFINITY;
                 for (int k = 0; k < shares; ++k) base = fmaxf(base, __ldcg(parts + ((int64_t)k * (D + 2) + D) * kTcRows));
-                if (base == -INFINITY) base = 0.f;
+                const float ref = base == -INFINITY ? 0.f : base;
                 l = 0.f;
                 for (int k = 0; k < shares; ++k) {
                     const float* p = parts + ((int64_t)k * (D + 2) + D) * kTcRows;
-                    l = fmaf(tc_ex2(__ldcg(p) - base), __ldcg(p + kTcRows), l);
+                    l = fmaf(tc_ex2(__ldcg(p) - ref), __ldcg(p + kTcRows), l);
                 }
             }
         }
         if (last) {
+            const float ref = base == -INFINITY ? 0.f : base;
+            if (l == 0.f && base > -INFINITY) l = __int_as_float(0x7fffffff);   // every score is -inf
             const float inv = l == 0.f ? 0.f : 1.f / l;                  // a row that sees nothing is zero
             // (the tile's products are complete, so its queries' buffer takes the outputs; a warp's rows are its own)
             unsigned char* out = sq + t * L::kQBytes;
@@ -425,7 +427,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) kv_attention_tc_kernel(const __
 #pragma unroll 1
                     for (int k = 0; k < shares; ++k) {
                         const float* p = parts + (int64_t)k * (D + 2) * kTcRows;
-                        const float f = tc_ex2(__ldcg(p + D * kTcRows) - base);
+                        const float f = tc_ex2(__ldcg(p + D * kTcRows) - ref);
                         uint32_t u[32];
 #pragma unroll
                         for (int i = 0; i < 32; ++i) u[i] = __float_as_uint(__ldcg(p + (c * 32 + i) * kTcRows));

@@ -55,6 +55,11 @@ cudaError_t launch_kv_append(const KvCacheView& c, const KvBatchView& b, const u
 cudaError_t launch_kv_read(const KvCacheView& c, const KvBatchView& b, const int* first, int count, uint16_t* K,
                            uint16_t* V, cudaStream_t st);
 
+// A row whose scores are all -infinity (an infinite query, say) has no softmax
+// and becomes NaN, unlike one that sees nothing, which is zero: to tell them
+// apart, a row that sees something takes this as its maximum.
+constexpr float kLeastScore = -3e38f;
+
 // attention.cu
 struct KvAttnPlan {
     bool tc;             // many rows: attention_tc.cu

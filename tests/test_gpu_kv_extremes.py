@@ -109,3 +109,47 @@ def test_a_row_does_not_depend_on_the_scores_beside_it(kernel, Hq, Hkv, D, cache
     rest = np.arange(new) % 3 != 0
     assert bool(got.isfinite().all())
     assert np.array_equal(got.cpu().numpy()[rest], want.cpu().numpy()[rest])
+
+
+INFINITE = [
+    ("pages", 4, 2, 64, 0, 1, 0), ("pages", 4, 2, 128, 5, 1, 0), ("pages", 2, 1, 128, 63, 1, 0), ("pages", 2, 2, 64, 100, 3, 1),
+    ("pages", 2, 1, 64, 6000, 2, 0), ("tiles", 4, 2, 128, 0, 150, 0), ("tiles", 4, 2, 64, 0, 150, 127),
+    ("tiles", 2, 1, 128, 100, 150, 149), ("shares", 4, 2, 64, 4000, 200, 7),
+]
+
+
+@pytest.mark.parametrize("sign", [1.0, -1.0])
+@pytest.mark.parametrize("what,kernel,Hq,Hkv,D,cached,new,row", [("query", *c) for c in INFINITE] +
+                         [("keys", *c) for c in INFINITE if c[4] + c[5] < PAGE])   # (a page's scale makes NaN of them)
+def test_a_row_whose_scores_are_all_minus_infinity(what, kernel, Hq, Hkv, D, cached, new, row, sign):
+    """An infinite query where every key has the other sign, or keys of a tail: there is no softmax, and the row is NaN, not
+    the zero of a row that sees nothing; no other row changes."""
+    out = []
+    for value in (None, -sign * np.inf):
+        sv = Server(1, Hq, Hkv, D, (cached + new) // PAGE + 2, seed=D + cached)
+        (q0, k0, v0), (q1, k1, v1) = sv.draw([cached]), sv.draw([new])
+        for k in (k0, k1):
+            k[:, 0, 7] = sign * (0.5 + np.abs(k[:, 0, 7]))           # kv head 0: one sign in dimension 7
+        q1[:, 0, 7] = sign * (0.5 + np.abs(q1[:, 0, 7]))
+        if value is not None:
+            if what == "query":
+                q1[row, 0, 7] = value
+            else:
+                k0[:, 0, 7] = k1[:, 0, 7] = value
+        if cached:
+            sv.step([cached], rope=False, data=(q0, k0, v0))
+        b, Q, _ = sv.step([new], rope=False, data=(q1, k1, v1))
+        assert kernel_of(sv.cache, b, Hq) == kernel
+        out.append(glowq.kv_attention(sv.cache, b, Q, workspace=sv.ws).cpu().numpy().reshape(new, Hq, D))
+        assert int(sv.ws[:65536].max()) == 0
+    clean, got = out
+    hit = np.zeros((new, Hq), bool)
+    hit[row, 0] = True
+    if what == "keys":
+        hit[:, 0] = True
+        clean, got = clean[:, Hq // Hkv:], got[:, Hq // Hkv:]        # (the group's other queries have either sign)
+        assert np.isnan(out[1][hit]).all()
+        assert np.array_equal(got, clean)
+        return
+    assert np.isnan(got[hit]).all()
+    assert np.isfinite(got[~hit]).all() and np.array_equal(got[~hit], clean[~hit])
