@@ -691,7 +691,7 @@ class Int8ForwardPlan(_Call):
             raise ValueError("a solo call has one module")
         if Ys is None:
             Ys = [torch.empty((T, m.out_features), dtype=f16, device=dev) for m in mods]
-        items = []
+        items, keep = [], [B, X]                # the tensors themselves: a module's fields may be set anew
         for m, Y in zip(mods, Ys, strict=True):
             _require(m.codes, "codes", torch.int8, dev, 2)
             _require(m.scales, "scales", torch.float32, dev, 1)
@@ -709,6 +709,7 @@ class Int8ForwardPlan(_Call):
             ld = Y.stride(0) if Y.shape[0] > 1 else max(Y.stride(0), (O + 7) // 8 * 8)
             items.append(_Int8Module(m.codes.data_ptr(), m.scales.data_ptr(), _ptr(m.A) if r > 0 else None, O,
                                      Y.data_ptr(), ld))
+            keep += [m.codes, m.scales, m.A, Y]
         outs = [m.out_features for m in mods]
         if workspace is None:
             workspace = w8a8_workspace(T, d, r, outs, dev)
@@ -728,7 +729,7 @@ class Int8ForwardPlan(_Call):
             name, args = "glowq_solo_forward_w8a8", (arr, d, _ptr(B), r, _ptr(X), T) + tail
         else:
             name, args = "glowq_group_forward_w8a8", (arr, len(items), d, _ptr(B), r, _ptr(X), T, _ptr(R_out)) + tail
-        super().__init__(name, dev, args, list(Ys), (list(mods), B, X, workspace, R_out))
+        super().__init__(name, dev, args, list(Ys), keep + [workspace, R_out])
 
 
 def group_forward_w8a8(mods: Sequence[Int8Module], B, X, Ys=None, R_out=None, workspace=None, stream=None):
@@ -774,6 +775,7 @@ class KVCache:
         self.k_codes, self.v_codes, self.k_scales, self.v_scales = k_codes, v_codes, k_scales, v_scales
         self.k_tail, self.v_tail = k_tail, v_tail
         self.pages, self.slots, self.kv_heads, self.head_dim, self.device = P, S, H, D, dev
+        self._keep = (k_codes, v_codes, k_scales, v_scales, k_tail, v_tail)
         self._c = _KVCache(_ptr(k_codes), _ptr(v_codes), _ptr(k_scales), _ptr(v_scales), _ptr(k_tail), _ptr(v_tail),
                            P, S, H, D)
 
@@ -843,7 +845,7 @@ class KVAppendPlan(_Call):
                 raise ValueError("rope must be positions x D: cosines of the D/2 pairs, then sines")
         args = (C.byref(cache._c), C.byref(batch._c), _ptr(Q), ldQ, hq, _ptr(K), ldK, _ptr(V), ldV, _ptr(rope),
                 0 if rope is None else int(rope.shape[0]), _ptr(Q_out), ldO)
-        super().__init__("glowq_kv_append", dev, args, Q_out, (cache, batch, K, V, Q, rope))
+        super().__init__("glowq_kv_append", dev, args, Q_out, (cache, batch, K, V, Q, Q_out, rope))
 
 
 def kv_append(cache: KVCache, batch: KVBatch, K, V, Q=None, Q_out=None, rope=None, stream=None):
@@ -877,7 +879,7 @@ class KVReadPlan(_Call):
                 raise ValueError(f"{name} must be n_seq x count x kv_heads D")
             out.append(t)
         args = (C.byref(cache._c), C.byref(batch._c), _ptr(first), int(count), _ptr(out[0]), _ptr(out[1]))
-        super().__init__("glowq_kv_read", dev, args, tuple(out), (cache, batch, first))
+        super().__init__("glowq_kv_read", dev, args, tuple(out), (cache, batch, first, *out))
 
 
 def kv_read(cache: KVCache, batch: KVBatch, count: int, first=None, K=None, V=None, stream=None):
@@ -914,7 +916,7 @@ class KVAttentionPlan(_Call):
         _require(workspace, "workspace", torch.uint8, dev)
         args = (C.byref(cache._c), C.byref(batch._c), _ptr(Q), ldQ, hq, D ** -0.5 if scale is None else float(scale),
                 _ptr(Y), ldY, _ptr(workspace), workspace.numel())
-        super().__init__("glowq_kv_attention", dev, args, Y, (cache, batch, Q, workspace))
+        super().__init__("glowq_kv_attention", dev, args, Y, (cache, batch, Q, Y, workspace))
 
 
 def kv_attention(cache: KVCache, batch: KVBatch, Q, scale: Optional[float] = None, Y=None, workspace=None,

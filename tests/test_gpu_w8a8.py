@@ -239,3 +239,29 @@ def test_weights_written_by_the_call_before(T, r):
             plan()
             torch.cuda.synchronize()
             assert torch.equal(plan.outputs[0], want[i % 2])
+
+
+def test_a_plan_holds_the_tensors_whose_addresses_it_has():
+    """Fields of modules and caches that are set anew afterwards free nothing that a plan still uses."""
+    import gc
+    import weakref
+    import torch
+    mods, B, X = make(2, 256, [32, 16], 8, seed=1)
+    dm = dev_mods(mods)
+    plan = glowq.Int8ForwardPlan(dm, cuda(B), cuda(X))
+    held = [weakref.ref(t) for m in dm for t in (m.codes, m.scales, m.A)] + [weakref.ref(t) for t in plan.outputs]
+    for m in dm:
+        m.codes = m.scales = m.A = None
+    plan.outputs = None
+    cache = glowq.KVCache.alloc(2, 1, 1, 64)
+    i32 = lambda *v: torch.tensor(v, dtype=torch.int32, device="cuda")
+    batch = glowq.KVBatch(i32(0, 1), i32(1), i32(0).reshape(1, 1), i32(0), 1, 1)
+    plans = [glowq.KVAttentionPlan(cache, batch, torch.zeros((1, 64), dtype=torch.float16, device="cuda")),
+             glowq.KVReadPlan(cache, batch, 1)]
+    held += [weakref.ref(getattr(cache, f)) for f in ("k_codes", "v_codes", "k_scales", "v_scales", "k_tail", "v_tail")]
+    held += [weakref.ref(t) for t in (plans[0].outputs, *plans[1].outputs)]
+    cache.k_codes = cache.v_codes = cache.k_scales = cache.v_scales = cache.k_tail = cache.v_tail = None
+    for p in plans:
+        p.outputs = None
+    gc.collect()
+    assert all(r() is not None for r in held)
