@@ -80,3 +80,16 @@ def test_binding_refuses_what_is_not_on_a_gpu():
         glowq.pack_int8(torch.zeros(16, 128))
     with pytest.raises(ValueError, match="CUDA"):
         glowq.Int8ForwardPlan([], None, torch.zeros(1, 128, dtype=torch.float16))
+
+
+@pytest.mark.parametrize("T", [1, 8, 9, 16, 17, 64, 65, 300, 4096])
+@pytest.mark.parametrize("d,r,outs", [(128, 0, [16]), (4096, 64, [4096] * 3), (14336, 256, [4096])])
+def test_workspace_holds_what_a_call_keeps_there(L, T, d, r, outs):
+    """The head, the codes, a scale per token and a solo module's R at least, and beside them the sums of split tiles: of 74
+    CTA pairs and fewer tiles than pairs, cut into shares of 8 k-blocks or more, there are 296 segments of two times 128
+    rows x 256 tokens at most."""
+    n = glowq.w8a8_workspace_bytes(T, d, r, outs)
+    least = 65536 + T * d + 4 * T + 2 * T * r
+    assert least <= n <= least + 16 * d + 4096 + 296 * 2 * 128 * 256 * 4
+    assert n >= glowq.w8a8_workspace_bytes(T, d, 0, outs)
+    assert glowq.w8a8_workspace_bytes(T, d, r, outs + [16]) > 65536
