@@ -21,6 +21,7 @@ HEADER_PATH = os.path.join(os.path.dirname(_PKG), "include", "glowq.h")
 
 GROUP_SIZE = 128
 KV_PAGE = 64
+WORKSPACE8_HEAD = 65536         # bytes at the start of the 8-bit calls' workspaces that must be zero
 MAX_RANK = 256
 MAX_MODULES = 8
 
@@ -661,11 +662,18 @@ def w8a8_workspace_bytes(T: int, d: int, r: int, out_features: Sequence[int]) ->
     return int(lib().glowq_w8a8_workspace_bytes(T, d, r, outs, len(out_features)))
 
 
-def w8a8_workspace(T: int, d: int, r: int, out_features: Sequence[int], device="cuda"):
-    """Zero-filled (the tickets at its start must begin at zero; every call leaves them so)."""
+def _workspace8(n: int, device):
+    """Its head is zero: the tickets there must begin so, and every call leaves them so.  What is behind it, tens of
+    megabytes for some calls, may hold anything."""
     import torch
-    n = max(w8a8_workspace_bytes(T, d, r, out_features), 16)
-    return torch.zeros(n, dtype=torch.uint8, device=device)
+    ws = torch.empty(max(n, 16), dtype=torch.uint8, device=device)
+    ws[:WORKSPACE8_HEAD].zero_()
+    return ws
+
+
+def w8a8_workspace(T: int, d: int, r: int, out_features: Sequence[int], device="cuda"):
+    """Scratch of a W8A8 call, its first 65536 bytes zero."""
+    return _workspace8(w8a8_workspace_bytes(T, d, r, out_features), device)
 
 
 class Int8ForwardPlan(_Call):
@@ -890,10 +898,9 @@ def kv_read(cache: KVCache, batch: KVBatch, count: int, first=None, K=None, V=No
 
 
 def kv_attention_workspace(cache: KVCache, batch: KVBatch, q_heads: int):
-    """Zero-filled (the tickets at its start must begin at zero; every call leaves them so)."""
-    import torch
+    """Scratch of an attention call, its first 65536 bytes zero."""
     n = int(lib().glowq_kv_attention_workspace_bytes(C.byref(cache._c), C.byref(batch._c), int(q_heads)))
-    return torch.zeros(max(n, 16), dtype=torch.uint8, device=cache.device)
+    return _workspace8(n, cache.device)
 
 
 class KVAttentionPlan(_Call):
