@@ -207,8 +207,10 @@ static glowq_status int8_views(const glowq_int8_module* mods, int32_t m, int64_t
         if (!f.scales) return GLOWQ_ERR_ARG;
         if (reinterpret_cast<uintptr_t>(f.scales) & 3u) return GLOWQ_ERR_ALIGN;
         // the shared checks of the INT4 path (zeros are not used: any non-null value)
+        // (and outputs without rows may have no address)
+        uint16_t* Y = T == 0 && !f.Y ? reinterpret_cast<uint16_t*>(16) : f.Y;
         tmp[i] = {reinterpret_cast<const uint32_t*>(f.codes), reinterpret_cast<const uint16_t*>(f.scales),
-                  reinterpret_cast<const uint8_t*>(f.scales), f.A, f.out_features, f.Y, f.ldY};
+                  reinterpret_cast<const uint8_t*>(f.scales), f.A, f.out_features, Y, f.ldY};
     }
     glowq_status v = validate_forward(tmp, m, d, B, r, X, T);
     if (v != GLOWQ_OK) return v;
@@ -641,9 +643,10 @@ glowq_status glowq_kv_append(const glowq_kv_cache* cache, const glowq_kv_batch* 
     KvBatchView b;
     glowq_status v = kv_views(cache, batch, &c, &b);
     if (v != GLOWQ_OK) return v;
-    if (q_heads < 0 || rope_len < 0 || (!Q && q_heads > 0) || (rope_len > 0 && !rope)) return GLOWQ_ERR_ARG;
+    const bool empty = b.n_seq == 0 || b.max_new == 0;           // (arrays without rows may have no address)
+    if (q_heads < 0 || rope_len < 0 || (!empty && !Q && q_heads > 0) || (rope_len > 0 && !rope)) return GLOWQ_ERR_ARG;
     if (q_heads > 65536 || q_heads % c.kv_heads != 0) return GLOWQ_ERR_SHAPE;
-    if (b.n_seq == 0 || b.max_new == 0) return GLOWQ_OK;
+    if (empty) return GLOWQ_OK;
     if ((v = kv_array(K, ldK, c.kv_heads, c.head_dim)) != GLOWQ_OK) return v;
     if ((v = kv_array(V, ldV, c.kv_heads, c.head_dim)) != GLOWQ_OK) return v;
     if (Q && ((v = kv_array(Q, ldQ, q_heads, c.head_dim)) != GLOWQ_OK ||

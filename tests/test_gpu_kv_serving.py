@@ -347,3 +347,19 @@ def test_products_on_two_streams(Ts):
                 p(stream=s)
         torch.cuda.synchronize()
         assert all(torch.equal(y, x) for p, w in zip(plans, want) for y, x in zip(p.outputs, w))
+
+
+def test_empty_batches():
+    import torch
+    cache = glowq.KVCache.alloc(2, 1, 2, 64)
+    i32 = lambda *v: torch.tensor(v, dtype=torch.int32, device="cuda")
+    f16 = lambda *s: torch.empty(*s, dtype=torch.float16, device="cuda")
+    for b in (glowq.KVBatch(i32(0), i32(), i32().reshape(0, 1), i32(), 0, 0), glowq.KVBatch(i32(0, 0), i32(0), i32(0).reshape(1, 1), i32(0), 0, 1),
+              glowq.KVBatch(i32(0, 0), i32(0), i32(0).reshape(1, 1), i32(0), 4, 2)):
+        Q = glowq.kv_append(cache, b, f16(b.rows, 128), f16(b.rows, 128), Q=f16(b.rows, 256))
+        assert glowq.kv_attention(cache, b, Q).shape == (b.rows, 256)
+        assert all(float(x.abs().sum()) == 0 for x in glowq.kv_read(cache, b, 3))
+    mods, B, X = w8.make(0, 256, [32, 16], 8, seed=0)
+    Ys, R = glowq.group_forward_w8a8(w8.dev_mods(mods), cuda(B), cuda(X))
+    assert [tuple(y.shape) for y in (*Ys, R)] == [(0, 32), (0, 16), (0, 8)]
+    assert glowq.solo_forward_w8a8(w8.dev_mods(mods)[0], cuda(B), cuda(X)).shape == (0, 32)

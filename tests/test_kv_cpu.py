@@ -103,3 +103,10 @@ def test_binding_refuses():
 def test_rotation_table_is_read_16_bytes_at_a_time(L, off):
     """A view of a larger table may begin at any float: only 16-byte boundaries are taken."""
     assert _append(L, rope=0xb000 + off) == ALIGN
+
+
+def test_a_step_without_rows_needs_no_arrays(L):
+    for b in (_batch(rows=0), _batch(max_new=0), _batch(n_seq=0)):
+        assert _append(L, b=b, Q=None, K=None, V=None, Qo=None, ldQ=512) == 0
+        assert _attend(L, b=b, Q=None, Y=None) == 0
+    assert _append(L, b=_batch(rows=0), Q=None, hq=3) == SHAPE

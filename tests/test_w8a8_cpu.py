@@ -93,3 +93,10 @@ def test_workspace_holds_what_a_call_keeps_there(L, T, d, r, outs):
     assert least <= n <= least + 16 * d + 4096 + 296 * 2 * 128 * 256 * 4
     assert n >= glowq.w8a8_workspace_bytes(T, d, 0, outs)
     assert glowq.w8a8_workspace_bytes(T, d, r, outs + [16]) > 65536
+
+
+def test_a_product_of_no_tokens_needs_no_arrays(L):
+    assert _group(L, _mods(Y=None), T=0, X=None, R=None, ws=None, n=0) == 0
+    assert _group(L, _mods(Y=None, q=None), T=0) == ARG
+    assert _group(L, _mods(Y=None, ldY=120), T=0) == ALIGN
+    assert L.glowq_solo_forward_w8a8(_mods(Y=None), 256, 0x5000, 16, None, 0, None, 0, None) == 0
