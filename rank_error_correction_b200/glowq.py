@@ -815,6 +815,8 @@ class KVBatch:
         n = int(kv_len.shape[0])
         if q_start.shape[0] != n + 1 or page_table.shape[0] != n or slot.shape[0] != n:
             raise ValueError("q_start has one more value than kv_len; page_table and slot one row per sequence")
+        if not (0 <= int(rows) < 1 << 31 and 0 <= int(max_new) < 1 << 31):
+            raise ValueError("rows and max_new must be from 0 to 2^31 - 1")
         self.n_seq, self.rows, self.max_new, self.device = n, int(rows), int(max_new), dev
         self._keep = (q_start, kv_len, page_table, slot)
         self._c = _KVBatch(_ptr(q_start), _ptr(kv_len), _ptr(page_table), _ptr(slot), n, int(page_table.shape[1]),
@@ -841,15 +843,17 @@ class KVAppendPlan(_Call):
         ldK = _heads(K, "K", n, cache.kv_heads * D, dev)
         ldV = _heads(V, "V", n, cache.kv_heads * D, dev)
         ldQ = ldO = hq = 0
+        if Q is None and Q_out is not None:
+            raise ValueError("Q_out without Q")
         if Q is not None:
-            hq = int(Q.shape[1]) // D
+            hq = int(Q.shape[1]) // D if Q.dim() == 2 else 0
             ldQ = _heads(Q, "Q", n, hq * D, dev)
             if Q_out is None:
                 Q_out = torch.empty((Q.shape[0], hq * D), dtype=torch.float16, device=dev)
             ldO = _heads(Q_out, "Q_out", n, hq * D, dev)
         if rope is not None:
             _require(rope, "rope", torch.float32, dev, 2)
-            if rope.shape[1] != D:
+            if rope.shape[0] == 0 or rope.shape[1] != D:      # (no rows: no address, which means no rotation)
                 raise ValueError("rope must be positions x D: cosines of the D/2 pairs, then sines")
         args = (C.byref(cache._c), C.byref(batch._c), _ptr(Q), ldQ, hq, _ptr(K), ldK, _ptr(V), ldV, _ptr(rope),
                 0 if rope is None else int(rope.shape[0]), _ptr(Q_out), ldO)

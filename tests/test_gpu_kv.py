@@ -463,3 +463,32 @@ def test_a_layers_attention_half():
         att = sv.check_attention(b, Ys[0], qr, new)[:, :-8]
         out = glowq.solo_forward_w8a8(ds[0], cuda(Bo), cuda(att))
         w.check([out], None, *plain8.w8a8(att, solo, Bo))
+
+
+def test_binding_refuses():
+    import torch
+    cache = glowq.KVCache.alloc(2, 1, 2, 64)
+    i32 = lambda *v: torch.tensor(v, dtype=torch.int32, device="cuda")
+    f16 = lambda *s: torch.zeros(*s, dtype=torch.float16, device="cuda")
+    step = (i32(0, 1), i32(1), i32(0).reshape(1, 1), i32(0))
+    b = glowq.KVBatch(*step, 1, 1)
+    table = torch.zeros((4, 64), dtype=torch.float32, device="cuda")
+    for rope in (table[:0], table[:, :32].contiguous(), table.half()):
+        with pytest.raises(ValueError, match="rope"):
+            glowq.kv_append(cache, b, f16(1, 128), f16(1, 128), rope=rope)
+    with pytest.raises(glowq.GlowQError, match="ALIGN"):
+        glowq.kv_append(cache, b, f16(1, 128), f16(1, 128), rope=torch.zeros(2 + 4 * 64, device="cuda")[2:].reshape(4, 64))
+    for Q in (f16(128), f16(1, 100), f16(1, 2, 64), table):
+        with pytest.raises(ValueError, match="Q"):
+            glowq.kv_append(cache, b, f16(1, 128), f16(1, 128), Q=Q)
+        with pytest.raises(ValueError, match="Q"):
+            glowq.kv_attention(cache, b, Q)
+    with pytest.raises(ValueError, match="Q_out"):
+        glowq.kv_append(cache, b, f16(1, 128), f16(1, 128), Q_out=f16(1, 128))
+    for rows, most in ((-1, 1), (1, -1), (1 << 31, 1), (1, 1 << 32)):
+        with pytest.raises(ValueError, match="rows"):
+            glowq.KVBatch(*step, rows, most)
+    with pytest.raises(ValueError, match="Y"):
+        glowq.kv_attention(cache, b, f16(1, 128), Y=f16(1, 64))
+    with pytest.raises(ValueError, match="K"):
+        glowq.kv_append(cache, b, f16(0, 128), f16(1, 128))
