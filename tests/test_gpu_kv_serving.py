@@ -363,3 +363,20 @@ def test_empty_batches():
     Ys, R = glowq.group_forward_w8a8(w8.dev_mods(mods), cuda(B), cuda(X))
     assert [tuple(y.shape) for y in (*Ys, R)] == [(0, 32), (0, 16), (0, 8)]
     assert glowq.solo_forward_w8a8(w8.dev_mods(mods)[0], cuda(B), cuda(X)).shape == (0, 32)
+
+
+@pytest.mark.parametrize("T", [9, 16])
+def test_more_tiles_than_the_scratch_counts(T):
+    """Few tokens, whose activations need k in shares, and more tiles than the head has tickets for: left to the tensor-core
+    product."""
+    import torch
+    O, d = 140032, 16384
+    mods, B, X = w8.make(T, d, [48, 64], 0, seed=T)
+    codes = torch.zeros((O, d), dtype=torch.int8, device="cuda")
+    scales = torch.ones(O, device="cuda")
+    for at, (q, s, _) in ((0, mods[0]), (O - 64, mods[1])):
+        codes[at:at + len(q)] = cuda(q)
+        scales[at:at + len(q)] = cuda(s)
+    Y = glowq.solo_forward_w8a8(glowq.Int8Module(codes, scales), None, cuda(X))
+    w8.check([Y[:, :48], Y[:, O - 64:]], None, plain8.w8a8(X, mods, None)[0], (None, None))
+    assert float(Y[:, 48:O - 64].abs().max()) == 0.0
