@@ -639,7 +639,7 @@ GLOWQ_API glowq_status glowq_kv_read(const glowq_kv_cache* cache, const glowq_kv
  * Keys and values are what glowq_kv_read gives before its rounding to fp16.
  * Scores, softmax statistics and sums are fp32; for the product with the
  * values weights are rounded to fp16, or where a sequence has few new tokens to
- * 2^-23 of the largest of their row and page.  A row that sees nothing (kv_len
+ * 2^-23 of the largest of their row and page (to 2^-23 of themselves in a tail).  A row that sees nothing (kv_len
  * below its sequence's new tokens) is zero.  A key, value or page scale that is
  * not finite makes NaN of the rows that see it, and of no other (an infinite
  * key that is still in a tail has no weight where its score is -infinity; a

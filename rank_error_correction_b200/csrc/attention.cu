@@ -16,7 +16,8 @@
 // sum_j w_ij v_j with integer v, and the denominator sum_pages (sum_j w_ij) / s_V.
 // An incomplete last page is fp16, and its products are: weights, scaled by 2^8
 // (the factor cancels; fp16's smallest normal is then 2^-22 of the largest), are
-// rounded to fp16 (2^-11).  Sums, maxima and outputs in fp32.
+// the sum of two fp16 numbers (off by 2^-24 of themselves and 2^-33 of the
+// largest).  Sums, maxima and outputs in fp32.
 #include <climits>
 
 #include "common.cuh"
@@ -103,10 +104,11 @@ struct AttnState {
 
 // One tile of 16 tokens of a tail, at column g and g + 8 in this lane; lim: last
 // visible token of each query row; lv = log2 of the tail's unit.  Returns the
-// weights as B fragments (k = tokens, n = query rows).
+// weights as B fragments (k = tokens, n = query rows), each in two fp16 terms:
+// what the first is off by (2^-12 of the weight), to another 2^-12.
 template <int D, int RN>
 __device__ __forceinline__ void softmax_tail(AttnState<D, RN>& st, float (&x)[RN][4], const int (&lim)[RN][2], float xs, float lv,
-                                             float inv_sv, int g, uint32_t (&pf)[RN][2]) {
+                                             float inv_sv, int g, uint32_t (&pf)[RN][2][2]) {
     float corr[RN][2];
     bool moved = false;
 #pragma unroll
@@ -127,8 +129,13 @@ __device__ __forceinline__ void softmax_tail(AttnState<D, RN>& st, float (&x)[RN
             x[r][e + 2] = ex2(x[r][e + 2] - ref + kWeightExp);
             st.l[r][e] = fmaf(x[r][e] + x[r][e + 2], inv_sv, st.l[r][e] * corr[r][e]);
         }
-        pf[r][0] = movm(h2_as_u32(__floats2half2_rn(x[r][0], x[r][1])));
-        pf[r][1] = movm(h2_as_u32(__floats2half2_rn(x[r][2], x[r][3])));
+#pragma unroll
+        for (int e = 0; e < 4; e += 2) {
+            const __half2 h = __floats2half2_rn(x[r][e], x[r][e + 1]);
+            const float2 f = __half22float2(h);
+            pf[r][0][e >> 1] = movm(h2_as_u32(h));
+            pf[r][1][e >> 1] = movm(h2_as_u32(__floats2half2_rn(x[r][e] - f.x, x[r][e + 1] - f.y)));
+        }
     }
     if (__any_sync(~0u, moved)) {
 #pragma unroll
@@ -613,7 +620,7 @@ __global__ void __launch_bounds__(kAttnThreads, RN == 1 ? 3 : 2) kv_attention_ke
             for (int r = 0; r < RN; ++r)
 #pragma unroll
                 for (int e = 0; e < 2; ++e) lim[r][e] = min(limit[r][e] - full * kKvPage, ntok - 1) - warp * 16;
-            uint32_t pf[RN][2];
+            uint32_t pf[RN][2][2];
             softmax_tail<D, RN>(st, x, lim, a.scale_log2, (float)-k2, exp2f((float)k2), g, pf);
 #pragma unroll
             for (int d = 0; d < D / 16; ++d) {
@@ -624,7 +631,10 @@ __global__ void __launch_bounds__(kAttnThreads, RN == 1 ? 3 : 2) kv_attention_ke
 #pragma unroll
                 for (int e = 0; e < 4; ++e) v[e] = h2_as_u32(__hmul2(u32_as_h2(v[e]), up));
 #pragma unroll
-                for (int q = 0; q < RN; ++q) mma_16816(st.o[q][d], v, pf[q]);
+                for (int q = 0; q < RN; ++q) {
+                    mma_16816(st.o[q][d], v, pf[q][0]);
+                    mma_16816(st.o[q][d], v, pf[q][1]);
+                }
             }
         }
         if (tails) from = min(from, full * kKvPage + warp * 16);

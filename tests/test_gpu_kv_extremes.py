@@ -153,3 +153,33 @@ def test_a_row_whose_scores_are_all_minus_infinity(what, kernel, Hq, Hkv, D, cac
         return
     assert np.isnan(got[hit]).all()
     assert np.isfinite(got[~hit]).all() and np.array_equal(got[~hit], clean[~hit])
+
+
+@pytest.mark.parametrize("code", [121, 100, 60, 0, -5, -20])
+@pytest.mark.parametrize("D", [64, 128])
+def test_weights_of_a_tail_have_22_bits(D, code):
+    """Two tokens of nearly equal weight and opposite values beside a heavier one, all in a decoding sequence's tail: what is
+    left shows the weights themselves.  Sums of D equal fp16 numbers are exact, so the scores are."""
+    sv = Server(1, 2, 2, D, 2, seed=5)
+    k = np.full((40, 2, D), -1.0, np.float16)
+    v = np.zeros((40, 2, D), np.float16)
+    k[3] = 1.0
+    k[10] = k[20] = np.float16(code / 127)
+    k[20, :, 5] = np.float16((code - 1) / 127)
+    v[10], v[20] = 1.0, -1.0
+    q = np.ones((40, 2, D), np.float16)
+    sv.step([39], rope=False, data=(q[:39], k[:39], v[:39]))
+    b, Q, qr = sv.step([1], rope=False, data=(q[39:], k[39:], v[39:]))
+    assert kernel_of(sv.cache, b, 2) == "pages"
+    got = glowq.kv_attention(sv.cache, b, Q, workspace=sv.ws).cpu().numpy().reshape(2, D).astype(np.float64)
+    kk, vv = sv.seq[0].held()
+    s = kk[:, 0] @ np.ones(D) * D ** -0.5
+    p = np.exp(s - s.max())
+    y = p @ vv[:, 0, 0] / p.sum()
+    # the exponent in log2 units: four roundings of the score, the values' power of two added (2^15 at most), the distance
+    # to the largest; 2^x itself 2^-22; a weight 2^-23 of itself and 2^-32 of the largest; then the output's rounding
+    u24 = 2.0 ** -24
+    x = np.abs(s) * np.log2(np.e)
+    rel = np.log(2) * u24 * (6 * (x + x.max()) + 15 + 24) + 2.0 ** -22 + 2.0 ** -23
+    b1 = (p[[10, 20]] @ rel[[10, 20]] + 2 * 2.0 ** -32) / p.sum() + 80 * 2 * u24 * abs(y)
+    assert abs(y) < 0.01 and np.abs(got - y).max() <= b1 + 2.0 ** -11 * (abs(y) + b1) + 2.0 ** -25
