@@ -579,7 +579,15 @@ typedef struct glowq_kv_cache {
  *               (read for complete pages only)
  *   slot        device int32 [n_seq], the sequence's tail
  *   max_new     no sequence has more new tokens (host bound that sizes the launch)
- * Rows from q_start[n_seq] on are padding: neither read nor written.  No two
+ * Rows before q_start[0] and from q_start[n_seq] on are padding: neither read nor
+ * written, so that a step may be taken in several calls over parts of its arrays.
+ * Attention chooses one kernel for a call, by max_new, and cuts a call by
+ * max_pages: bounds far above the step's own numbers are right but cost time and
+ * scratch, and a step that mixes a prompt's chunk with many decoding sequences
+ * is faster as two calls.  (8 kv heads, 32 query heads of 128: 64 sequences of up
+ * to 4096 tokens take 65 us and a chunk of 512 behind 1024 tokens 34 us, both in
+ * one call 279 us.  A prompt of 4096 tokens of 32 heads: 187 us with a table of 64
+ * pages, 242 us with one of 512.)  No two
  * sequences of a batch share a slot; they may share complete pages that the
  * step does not write.  The device data are checked where they are used: a
  * value out of range records GLOWQ_ERR_INDEX in the device status word
@@ -613,6 +621,8 @@ typedef struct glowq_kv_batch {
  *            (x_i cos - x_{i+D/2} sin, x_{i+D/2} cos + x_i sin), two fp32
  *            products and a sum, unfused, rounded to fp16.  NULL: no rotation
  *            (Q, if given, is copied).  Positions from rope_len on are out of range.
+ * kv_len may also go back (rejected draft tokens), but not below the last
+ * complete page's end: a completed page's tokens are no longer in the tail.
  * Running the same step again writes the same values, unless the step began
  * inside a page, completed it and left another page incomplete (the tail that
  * it began with is then overwritten).

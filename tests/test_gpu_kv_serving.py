@@ -380,3 +380,41 @@ def test_more_tiles_than_the_scratch_counts(T):
     Y = glowq.solo_forward_w8a8(glowq.Int8Module(codes, scales), None, cuda(X))
     w8.check([Y[:, :48], Y[:, O - 64:]], None, plain8.w8a8(X, mods, None)[0], (None, None))
     assert float(Y[:, 48:O - 64].abs().max()) == 0.0
+
+
+def test_a_mixed_step_as_two_calls():
+    """Decoding sequences and a prompt's chunk of one step, attended to by a call each over parts of the step's arrays: each
+    by its own kernel, rows outside a call's sequences untouched."""
+    import torch
+    sv = Server(4, 8, 2, 128, 16, seed=9)
+    sv.step([700, 64, 5, 300])
+    new = [1, 1, 1, 400]
+    b, Q, qr = sv.step(new)
+    q_start, kv_len, table, slot = b._keep
+    few = glowq.KVBatch(q_start[:4], kv_len[:3], table[:3], slot[:3], 3, 1)
+    many = glowq.KVBatch(q_start[3:], kv_len[3:], table[3:], slot[3:], 403, 400)
+    assert kernel_of(sv.cache, few, 8) == "pages" and kernel_of(sv.cache, many, 8) in ("tiles", "shares")
+    Y = torch.full((403, 8 * 128), 3.0, dtype=torch.float16, device="cuda")
+    glowq.kv_attention(sv.cache, many, Q, Y=Y)
+    assert bool((Y[:3] == 3).all())
+    chunk = Y[3:].clone()
+    glowq.kv_attention(sv.cache, few, Q, Y=Y)
+    assert torch.equal(Y[3:], chunk)
+    got, at = Y.cpu().numpy().reshape(403, 8, 128), 0
+    for s, n in zip(sv.seq, new):
+        y, bound = plain8.attention(qr[at:at + n], *s.held(), len(s.k) - n, 128 ** -0.5)
+        assert plain8.within(got[at:at + n], y, bound) <= 1.0
+        at += n
+
+
+def test_tokens_taken_back():
+    """Lengths that go back inside the incomplete page, as after rejected draft tokens, and go on with other tokens."""
+    sv = Server(2, 4, 2, 64, 4, seed=10)
+    sv.step([100, 130])
+    for draft, kept, new in (([4, 4], [101, 128], [2, 1]), ([9, 3], [105, 129], [60, 3])):
+        sv.step(draft)
+        for s, n in zip(sv.seq, kept):
+            s.k, s.v = s.k[:n], s.v[:n]
+        b, Q, qr = sv.step(new)
+        sv.check_held(b)
+        sv.check_attention(b, Q, qr, new)
