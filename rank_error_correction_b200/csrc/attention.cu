@@ -171,7 +171,7 @@ __device__ __forceinline__ AttnSpan attn_span(const KvSeq& s, const KvBatchView&
 // warps.  The warps' results meet in shared memory, the shares' in the
 // workspace: the block that counts last on a unit adds its parts in order.
 // Bound by memory where there is enough of it: two sequences of 116,000 and
-// 126,000 tokens, 8 kv heads of 128: 497 MB in 94 us, 81 % of the copy bandwidth;
+// 126,000 tokens, 8 kv heads of 128: 497 MB in 92 us, 82 % of the copy bandwidth;
 // 64 sequences of 1 to 4096 tokens: 252 MB in 61 us, 64 % (each of 2.2 units of a
 // block drains its ring, and pays its tail and its merge).  One sequence of 500
 // tokens takes 11 us, all of it latency: lengths, page ids, codes, tail, results.
@@ -580,7 +580,8 @@ __global__ void __launch_bounds__(kAttnThreads, RN == 1 ? 3 : 2) kv_attention_ke
             // must not reach the others (0 x inf): it is taken out of the product and
             // its token's scores become NaN instead.  The others' largest magnitude
             // gives the tokens the power of two that brings it to 64 .. 128, as codes
-            // are, so that their weights share codes' range (2^-k plays s_V's part).
+            // are, so that their weights share codes' range (2^-k plays s_V's part).  It is below 1 where the
+            // largest passes 2^7: values 2^-21 of it and below then lose low bits.
             uint32_t poison = 0;
             __half2 am = __half2half2(__ushort_as_half(0));
             for (int i = lane; i < 16 * kCh; i += 32) {

@@ -17,8 +17,8 @@
 // (then O is rescaled in TMEM): weights stay below 2^14.
 // Warps: 0-3 and 4-7 softmax of tiles 0 and 1 (a thread per row), 8-11 convert
 // pages, 12 issues the MMAs.
-// 4096 new tokens of 32 heads of 128: 185 us, 744 TFLOP/s (45 % of the dense
-// rate); four chunks of 187 to 821 tokens, 8 kv heads: 103 us.  256 rows and 128
+// 4096 new tokens of 32 heads of 128: 186 us, 739 TFLOP/s (45 % of the dense
+// rate); four chunks of 187 to 821 tokens, 8 kv heads: 104 us.  256 rows and 128
 // tokens take 5000 clocks, of which the tensor pipe works 2050, the exponentials
 // 2050 and shared memory 2560, and issue slots are 42 % busy: what bounds it is
 // how far these overlap.  Slower: scores of a page in two buffers, so that a
