@@ -183,3 +183,46 @@ def test_weights_of_a_tail_have_22_bits(D, code):
     rel = np.log(2) * u24 * (6 * (x + x.max()) + 15 + 24) + 2.0 ** -22 + 2.0 ** -23
     b1 = (p[[10, 20]] @ rel[[10, 20]] + 2 * 2.0 ** -32) / p.sum() + 80 * 2 * u24 * abs(y)
     assert abs(y) < 0.01 and np.abs(got - y).max() <= b1 + 2.0 ** -11 * (abs(y) + b1) + 2.0 ** -25
+
+
+def fixed_point(q, k, v, start, scale):
+    """What the weights' fixed point adds to plain8.attention's bound where a sequence has few new tokens: of a complete page
+    each weight is off by 2^-23 of the largest of its row and page."""
+    n, Hq, D = q.shape
+    G = Hq // k.shape[1]
+    out = np.zeros((n, Hq, D))
+    full = len(k) // PAGE * PAGE                                     # (what is behind is in the tail)
+    for i in range(n):
+        m = min(len(k), start + i + 1)
+        for h in range(Hq):
+            if m <= 0:
+                continue
+            s = k[:m, h // G] @ q[i, h].astype(np.float64) * scale
+            w = np.exp(s - s.max())
+            w /= w.sum()
+            for p in range(0, min(m, full), PAGE):
+                out[i, h] += 2.0 ** -23 * w[p:p + PAGE].max() * np.abs(v[p:min(p + PAGE, m), h // G]).sum(0)
+    return out
+
+
+@pytest.mark.parametrize("seed", range(8))
+@pytest.mark.parametrize("Hq,Hkv,D,cached,new,scale,spread", [
+    (3, 3, 128, [100], [63], None, 30.0), (24, 3, 128, [28, 46, 61], [2, 1, 3], 0.5, 1.0), (28, 4, 64, [65, 100], [3, 2], None, 30.0),
+    (2, 1, 64, [6], [61], 0.5, 1.0), (4, 2, 64, [900, 700], [1, 3], 2.0, 5.0),
+])
+def test_one_token_far_ahead_of_the_others(Hq, Hkv, D, cached, new, scale, spread, seed):
+    """Rows whose largest weight is 10^5 and more times the next, with values that are zero there: what is left is the small
+    weights' share."""
+    sv = Server(len(new), Hq, Hkv, D, 17, seed=seed, spread=spread)
+    if any(cached):
+        sv.step(cached)
+    b, Q, qr = sv.step(new)
+    assert kernel_of(sv.cache, b, Hq) == "pages"
+    got = glowq.kv_attention(sv.cache, b, Q, scale=scale, workspace=sv.ws).cpu().numpy().reshape(-1, Hq, D)
+    scale, at = D ** -0.5 if scale is None else scale, 0
+    for s, n in zip(sv.seq, new):
+        k, v = s.held()
+        y, bound = plain8.attention(qr[at:at + n], k, v, len(k) - n, scale)
+        bound = bound + fixed_point(qr[at:at + n], k, v, len(k) - n, scale)
+        assert plain8.within(got[at:at + n], y, bound) <= 1.0
+        at += n
